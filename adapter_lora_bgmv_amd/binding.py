@@ -29,7 +29,8 @@ EXPORTS = ("lora_last_error", "lora_version", "lora_init", "lora_scale", "lora_s
            "lora_apply", "lora_apply_noalloc", "lora_apply_segmented", "lora_apply_moe_gather",
            "lora_set_profile_events", "lora_moe_grouped_shrink", "lora_moe_grouped_expand_fold",
            "lora_apply_moe_grouped", "lora_apply_stack", "lora_embedding_pair",
-           "lora_embed_rows")
+           "lora_embed_rows", "lora_kv_write", "lora_kv_read", "lora_kv_attend_workspace_bytes",
+           "lora_kv_attend", "lora_token_logprobs_workspace_bytes", "lora_token_logprobs")
 
 
 class LoraError(RuntimeError):
@@ -48,6 +49,18 @@ class lora_route_moe(C.Structure):
     _fields_ = [("a_table", C.c_void_p), ("b_table", C.c_void_p), ("scale_table", C.c_void_p),
                 ("max_loras", C.c_uint32), ("n_experts", C.c_uint32), ("k_in", C.c_uint32),
                 ("n_out", C.c_uint32), ("max_rank", C.c_uint32), ("dtype", C.c_int32)]
+
+
+class lora_kv_cache(C.Structure):
+    _fields_ = [("k", C.c_void_p), ("v", C.c_void_p), ("k_scale", C.c_void_p),
+                ("v_scale", C.c_void_p), ("n_pages", C.c_uint32), ("n_kv_heads", C.c_uint32),
+                ("head_dim", C.c_uint32), ("page_tokens", C.c_uint32)]
+
+
+class lora_kv_seqs(C.Structure):
+    _fields_ = [("page_table", C.c_void_p), ("row_indptr", C.c_void_p), ("kv_len", C.c_void_p),
+                ("n_seqs", C.c_uint32), ("max_pages", C.c_uint32), ("table_stride", C.c_uint32),
+                ("max_rows", C.c_uint32)]
 
 
 _lib = None
@@ -94,6 +107,15 @@ def lib() -> C.CDLL:
     L.lora_embedding_pair.argtypes = [i32, u32, u32, u32, u32, vp, u32, u32, vp, vp]
     L.lora_embed_rows.argtypes = [i32, u32, u32, vp, u32, C.POINTER(lora_route), vp, vp, u32, vp,
                                   u32, vp]
+    KP, SP = C.POINTER(lora_kv_cache), C.POINTER(lora_kv_seqs)
+    L.lora_kv_write.argtypes = [KP, SP, i32, vp, u32, vp, u32, u32, vp]
+    L.lora_kv_read.argtypes = [KP, SP, i32, vp, u32, vp, u32, u32, vp]
+    L.lora_kv_attend_workspace_bytes.restype = sz
+    L.lora_kv_attend_workspace_bytes.argtypes = [KP, SP, i32, u32, u32]
+    L.lora_kv_attend.argtypes = [KP, SP, i32, u32, vp, u32, C.c_float, u32, u32, vp, u32, vp, vp, sz, vp]
+    L.lora_token_logprobs_workspace_bytes.restype = sz
+    L.lora_token_logprobs_workspace_bytes.argtypes = [i32, u32, u32, u32]
+    L.lora_token_logprobs.argtypes = [i32, u32, vp, u32, vp, u32, u32, vp, vp, vp, vp, vp, vp, sz, vp]
     _lib = L
     return L
 
@@ -322,3 +344,87 @@ def lora_embed_rows(dtype: int, n_vocab: int, n_embd: int, E, e_row_stride: int,
     _check(lib().lora_embed_rows(dtype, n_vocab, n_embd, _ptr(E), e_row_stride, _route_ref(route),
                                  _ptr(token_ids), _ptr(seq_slot), n, _ptr(y), y_row_stride,
                                  _stream(stream)))
+
+
+# ---------------------------------------------------------------- verify step
+class KVCache:
+    """Device arrays of an 8-bit paged KV cache (lora_kv_cache): ``k`` and ``v``
+    uint8 ``[n_pages][n_kv_heads][page_tokens * head_dim]``, ``k_scale`` and
+    ``v_scale`` uint8 ``[n_pages][n_kv_heads]``, all contiguous."""
+
+    def __init__(self, k, v, k_scale, v_scale, *, page_tokens: int, head_dim: int):
+        import torch
+        n_pages, heads, size = k.shape
+        for t, shape in ((k, (n_pages, heads, page_tokens * head_dim)), (v, k.shape),
+                         (k_scale, (n_pages, heads)), (v_scale, (n_pages, heads))):
+            if t.dtype != torch.uint8 or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+                raise ValueError(f"cache array must be contiguous uint8 {tuple(shape)}: got {t.dtype} {tuple(t.shape)}")
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.n_pages, self.n_kv_heads, self.head_dim, self.page_tokens = n_pages, heads, head_dim, page_tokens
+        self.c = lora_kv_cache(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+                               n_pages, heads, head_dim, page_tokens)
+        self.ref = C.byref(self.c)
+
+    @classmethod
+    def empty(cls, n_pages: int, n_kv_heads: int, head_dim: int, page_tokens: int, device="cuda"):
+        import torch
+        k, v = (torch.empty(n_pages, n_kv_heads, page_tokens * head_dim, dtype=torch.uint8, device=device)
+                for _ in range(2))
+        ks, vs = (torch.empty(n_pages, n_kv_heads, dtype=torch.uint8, device=device) for _ in range(2))
+        return cls(k, v, ks, vs, page_tokens=page_tokens, head_dim=head_dim)
+
+
+class KVSeqs:
+    """The sequences of a call (lora_kv_seqs): device int32 ``page_table
+    [n_seqs][max_pages]`` (unit stride along its rows), ``row_indptr
+    [n_seqs + 1]`` and ``kv_len [n_seqs]``; their contents may be rewritten
+    between calls."""
+
+    def __init__(self, page_table, row_indptr, kv_len, *, max_rows: int = 0):
+        import torch
+        n_seqs, max_pages = page_table.shape
+        for t, shape in ((page_table, (n_seqs, max_pages)), (row_indptr, (n_seqs + 1,)), (kv_len, (n_seqs,))):
+            if t.dtype != torch.int32 or tuple(t.shape) != shape or (t.numel() > 1 and t.stride(-1) != 1 and t.shape[-1] > 1):
+                raise ValueError(f"sequence array must be int32 {shape} of unit stride: got {t.dtype} {tuple(t.shape)}")
+        stride = page_table.stride(0) if n_seqs > 1 else max_pages
+        self.page_table, self.row_indptr, self.kv_len = page_table, row_indptr, kv_len
+        self.n_seqs, self.max_pages, self.max_rows = n_seqs, max_pages, max_rows
+        self.c = lora_kv_seqs(page_table.data_ptr(), row_indptr.data_ptr(), kv_len.data_ptr(), n_seqs,
+                              max_pages, stride, max_rows)
+        self.ref = C.byref(self.c)
+
+
+def lora_kv_write(cache: KVCache, seqs: KVSeqs, dtype: int, k, k_row_stride: int, v, v_row_stride: int,
+                  n: int, stream=None):
+    _check(lib().lora_kv_write(cache.ref, seqs.ref, dtype, _ptr(k), k_row_stride, _ptr(v), v_row_stride,
+                               n, _stream(stream)))
+
+
+def lora_kv_read(cache: KVCache, seqs: KVSeqs, dtype: int, k, k_row_stride: int, v, v_row_stride: int,
+                 n: int, stream=None):
+    _check(lib().lora_kv_read(cache.ref, seqs.ref, dtype, _ptr(k), k_row_stride, _ptr(v), v_row_stride,
+                              n, _stream(stream)))
+
+
+def lora_kv_attend_workspace_bytes(cache: KVCache, seqs: KVSeqs, dtype: int, n_heads: int, n: int) -> int:
+    return int(lib().lora_kv_attend_workspace_bytes(cache.ref, seqs.ref, dtype, n_heads, n))
+
+
+def lora_kv_attend(cache: KVCache, seqs: KVSeqs, dtype: int, n_heads: int, q, q_row_stride: int,
+                   scale: float, window: int, n: int, out, out_row_stride: int, lse, workspace,
+                   workspace_bytes: int, stream=None):
+    _check(lib().lora_kv_attend(cache.ref, seqs.ref, dtype, n_heads, _ptr(q), q_row_stride, scale, window,
+                                n, _ptr(out), out_row_stride, _ptr(lse), _ptr(workspace),
+                                workspace_bytes, _stream(stream)))
+
+
+def lora_token_logprobs_workspace_bytes(dtype: int, n_vocab: int, n: int, top: int) -> int:
+    return int(lib().lora_token_logprobs_workspace_bytes(dtype, n_vocab, n, top))
+
+
+def lora_token_logprobs(dtype: int, n_vocab: int, logits, row_stride: int, token_ids, n: int, top: int,
+                        logp, entropy, rank, top_ids, top_logp, workspace, workspace_bytes: int,
+                        stream=None):
+    _check(lib().lora_token_logprobs(dtype, n_vocab, _ptr(logits), row_stride, _ptr(token_ids), n, top,
+                                     _ptr(logp), _ptr(entropy), _ptr(rank), _ptr(top_ids), _ptr(top_logp),
+                                     _ptr(workspace), workspace_bytes, _stream(stream)))

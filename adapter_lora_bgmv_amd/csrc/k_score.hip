@@ -1,0 +1,379 @@
+// k_score.hip -- log probabilities of given tokens, with entropy, rank and the top alternatives.
+//
+// For a row x of n_vocab logits, m its maximum and s = sum exp(x - m):
+//     logp   = x[id] - m - log s,
+//     entropy = log s - sum exp(x - m) (x - m) / s,
+//     rank   = 1 + the number of logits above x[id],
+//     top    = the `top` largest by (value, lower index first).
+// One pass over the logits: a workgroup's 256 threads take a chunk of the row
+// into registers (up to 16 vectors of 16 bytes a thread, all loads in flight
+// together), and everything above is computed from there.  The exponentials
+// run in base 2, t = (x - m) log2(e): the difference first, so that rows of
+// the type's lowest value stay finite.
+//
+// Top: the order is that of 64-bit keys, the value's bits in unsigned order
+// above the complement of the index, all of them different.  Of the 64
+// lanes' maxima a wave finds (by ballots, bit after bit) a value that `top`
+// of them reach; the largest of the four waves' values bounds the chunk's
+// `top` from below, and what reaches it, about `top` / 64 of each lane's
+// share, goes to a list in LDS.  An entry's place is the number of larger
+// keys in the list.  A list that would overflow (rows of equal values) takes
+// `top` rounds of the workgroup's maximum below the last instead.
+//
+// A row of several chunks leaves a record of each in the workspace; the last
+// chunk to arrive joins them, the lists by the same selection.
+//
+// HBM bounds large calls (every logit is read once), the exponentials and
+// compares follow closely: about 11 instructions a logit; latency bounds
+// small ones.
+#include "common.hpp"
+#include "verify.hpp"
+
+namespace lora {
+
+constexpr int kScoreList = 1024;  // entries of the LDS list
+typedef unsigned long long u64;
+
+// Unsigned order of an f32's bits is its value's order.
+__device__ __forceinline__ uint32_t ordered(float x) {
+  const uint32_t b = __float_as_uint(x);
+  return b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
+}
+__device__ __forceinline__ float from_ordered(uint32_t o) {
+  return __uint_as_float(o & 0x80000000u ? o ^ 0x80000000u : ~o);
+}
+__device__ __forceinline__ u64 key_of(float x, uint32_t index) { return (u64)ordered(x) << 32 | (uint32_t)~index; }
+
+template <typename T>
+struct Vec;
+template <>
+struct Vec<float> {
+  static constexpr int N = 4;
+  static __device__ float at(const uint4 &v, int e) {
+    return __uint_as_float(e == 0 ? v.x : e == 1 ? v.y : e == 2 ? v.z : v.w);
+  }
+  static __device__ float one(const float *p) { return *p; }
+};
+template <>
+struct Vec<u16> {
+  static constexpr int N = 8;
+  static __device__ float at(const uint4 &v, int e) {
+    const uint32_t w = e < 2 ? v.x : e < 4 ? v.y : e < 6 ? v.z : v.w;
+    return __uint_as_float(e & 1 ? w & 0xffff0000u : w << 16);
+  }
+  static __device__ float one(const u16 *p) { return bf2f(*p); }
+};
+
+__device__ __forceinline__ float wave_sum(float v) {
+#pragma unroll
+  for (int off = 32; off > 0; off >>= 1) v += __shfl_xor(v, off, 64);
+  return v;
+}
+__device__ __forceinline__ float wave_max(float v) {
+#pragma unroll
+  for (int off = 32; off > 0; off >>= 1) v = fmaxf(v, __shfl_xor(v, off, 64));
+  return v;
+}
+
+// A lower bound of the k-th largest of the wave's 64 keys: its upper 16 bits.
+__device__ __forceinline__ uint32_t kth_floor(uint32_t key, int k) {
+  uint32_t t = 0;
+#pragma unroll
+  for (int bit = 31; bit >= 16; --bit) {
+    const uint32_t c = t | 1u << bit;
+    if (__popcll(__ballot(key >= c)) >= k) t = c;
+  }
+  return t;
+}
+
+struct ScoreLds {
+  u64 list[kScoreList];
+  u64 top[kScoreMaxTop];
+  u64 red[4];
+  float m[4], s[4], sx[4], tot[4];
+  uint32_t floor[4];
+  int above[4];
+  int count;
+  unsigned arrived;
+};
+
+// The `k` largest keys of all that `each` passes to its argument, in order,
+// into lds.top; keys are distinct and not 0.  `floor`: a value (upper half)
+// that at least k of the keys reach.  `each(f)` calls f(key) for the
+// thread's keys, `any` whether the thread may hold one that reaches the floor.
+template <typename Each>
+__device__ __forceinline__ void select_top(int k, uint32_t floor, bool any, Each each, ScoreLds &lds) {
+  const int tid = threadIdx.x;
+  if (tid == 0) lds.count = 0;
+  if (tid < k) lds.top[tid] = 0;  // a chunk may hold fewer
+  __syncthreads();
+  if (any)
+    each([&](u64 key) {
+      if ((uint32_t)(key >> 32) >= floor && key) {
+        const int at = atomicAdd(&lds.count, 1);
+        if (at < kScoreList) lds.list[at] = key;
+      }
+    });
+  __syncthreads();
+  const int n = lds.count;
+  if (n <= kScoreList) {
+    for (int c = tid; c < n; c += kScoreThreads) {
+      const u64 mine = lds.list[c];
+      int above = 0;
+      for (int i = 0; i < n; ++i) above += lds.list[i] > mine;
+      if (above < k) lds.top[above] = mine;
+    }
+    __syncthreads();
+    return;
+  }
+  u64 last = ~0ull;
+  for (int r = 0; r < k; ++r) {
+    u64 best = 0;
+    each([&](u64 key) {
+      if (key < last && key > best) best = key;
+    });
+#pragma unroll
+    for (int off = 32; off > 0; off >>= 1) {
+      const u64 o = __shfl_xor(best, off, 64);
+      best = o > best ? o : best;
+    }
+    if ((tid & 63) == 0) lds.red[tid >> 6] = best;
+    __syncthreads();
+    best = lds.red[0];
+#pragma unroll
+    for (int w = 1; w < 4; ++w) best = lds.red[w] > best ? lds.red[w] : best;
+    if (tid == 0) lds.top[r] = best;
+    last = best;
+    __syncthreads();
+  }
+}
+
+constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
+
+// The results of a row from its maximum, sums, count and lds.top.
+__device__ __forceinline__ void finish(const ScoreArgs &a, int row, int id, float xt, float m, float s, float sx, int above,
+                                       const ScoreLds &lds) {
+  const int tid = threadIdx.x;
+  const float ls = s == 0.f ? 0.f : __builtin_amdgcn_logf(s);  // log2; s is 0 where every logit is -inf
+  const bool there = (unsigned)id < (unsigned)a.n_vocab;
+  if (tid == 0) {
+    // NaN or +inf in the row makes s NaN, and with it these
+    if (a.logp) a.logp[row] = there ? (xt - m) - kLn2 * ls : s == s ? -INFINITY : s;
+    if (a.entropy) a.entropy[row] = s == 0.f ? 0.f : kLn2 * (ls - sx / s);
+    if (a.rank) a.rank[row] = there ? above + 1 : 0;
+  }
+  if (tid < a.top) {
+    const u64 key = lds.top[tid];
+    a.top_ids[(size_t)row * a.top + tid] = (int32_t)~(uint32_t)key;
+    a.top_logp[(size_t)row * a.top + tid] = (from_ordered((uint32_t)(key >> 32)) - m) - kLn2 * ls;
+  }
+}
+
+template <typename T, int NV>
+__global__ __launch_bounds__(kScoreThreads) void score_kernel(ScoreArgs a) {
+  constexpr int VE = Vec<T>::N, kChunk = kScoreThreads * NV * VE;
+  __shared__ ScoreLds lds;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int row = blockIdx.x / a.chunks, chunk = blockIdx.x - row * a.chunks;
+  const T *x = (const T *)a.logits + (long long)row * a.stride;
+  // the grid of vectors begins at the 16-byte line that holds the row's first element
+  const int skew = (int)(((uintptr_t)x & 15) / sizeof(T));
+  const int first = chunk * kChunk - skew + tid * VE;  // index of the thread's first element
+  const int id = a.ids ? a.ids[row] : -1;
+
+  uint4 v[NV];
+  constexpr uint32_t kNegInf = sizeof(T) == 4 ? 0xff800000u : 0xff80ff80u;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int at = first + i * (kScoreThreads * VE);
+    if (at >= 0 && at + VE <= a.n_vocab) {
+      v[i] = ldg16(x + at);
+    } else {
+      v[i] = make_uint4(kNegInf, kNegInf, kNegInf, kNegInf);
+      if (at + VE > 0 && at < a.n_vocab) {
+        uint32_t w[4] = {kNegInf, kNegInf, kNegInf, kNegInf};
+#pragma unroll
+        for (int e = 0; e < VE; ++e)
+          if (at + e >= 0 && at + e < a.n_vocab) {
+            if constexpr (sizeof(T) == 4) w[e] = __float_as_uint(x[at + e]);
+            else w[e / 2] = e & 1 ? (w[e / 2] & 0xffffu) | (uint32_t)x[at + e] << 16 : (w[e / 2] & 0xffff0000u) | x[at + e];
+          }
+        v[i] = make_uint4(w[0], w[1], w[2], w[3]);
+      }
+    }
+  }
+  const bool there = (unsigned)id < (unsigned)a.n_vocab;
+  const float xt = there ? Vec<T>::one(x + id) : INFINITY;  // nothing is above +inf
+
+  float mx = -INFINITY;
+#pragma unroll
+  for (int i = 0; i < NV; ++i)
+#pragma unroll
+    for (int e = 0; e < VE; ++e) mx = fmaxf(mx, Vec<T>::at(v[i], e));
+  const float wm = wave_max(mx);
+  const bool holds = first < a.n_vocab;  // the thread has an element at all
+  if (a.top) {
+    const uint32_t f = kth_floor(holds ? ordered(mx) : 0u, a.top);
+    if (lane == 0) lds.floor[wave] = f;
+  }
+  if (lane == 0) lds.m[wave] = wm;
+  __syncthreads();
+  const float m_raw = fmaxf(fmaxf(lds.m[0], lds.m[1]), fmaxf(lds.m[2], lds.m[3]));
+  const float m = m_raw == -INFINITY ? 0.f : m_raw;
+  float s = 0.f, sx = 0.f;
+  int above = 0;
+#pragma unroll
+  for (int i = 0; i < NV; ++i)
+#pragma unroll
+    for (int e = 0; e < VE; ++e) {
+      const float y = Vec<T>::at(v[i], e);
+      const float t = (y - m) * kLog2e, p = __builtin_amdgcn_exp2f(t);
+      s += p;
+      sx = fmaf(p, fmaxf(t, -1e4f), sx);  // p is 0 far below; the bound keeps 0 x inf out
+      above += y > xt;
+    }
+  s = wave_sum(s);
+  sx = wave_sum(sx);
+#pragma unroll
+  for (int off = 32; off > 0; off >>= 1) above += __shfl_xor(above, off, 64);
+  if (lane == 0) {
+    lds.s[wave] = s;
+    lds.sx[wave] = sx;
+    lds.above[wave] = above;
+  }
+  if (a.top) {
+    const uint32_t f = max(max(lds.floor[0], lds.floor[1]), max(lds.floor[2], lds.floor[3]));
+    auto each = [&](auto &&use) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int e = 0; e < VE; ++e) {
+          const int at = first + i * (kScoreThreads * VE) + e;
+          if (at >= 0 && at < a.n_vocab) use(key_of(Vec<T>::at(v[i], e), (uint32_t)at));
+        }
+    };
+    select_top(a.top, f, holds && ordered(mx) >= f, each, lds);
+  } else {
+    __syncthreads();
+  }
+  s = (lds.s[0] + lds.s[1]) + (lds.s[2] + lds.s[3]);
+  sx = (lds.sx[0] + lds.sx[1]) + (lds.sx[2] + lds.sx[3]);
+  above = (lds.above[0] + lds.above[1]) + (lds.above[2] + lds.above[3]);
+  if (a.chunks == 1) {
+    finish(a, row, id, xt, m, s, sx, above, lds);
+    return;
+  }
+
+  // the chunk's record: {m, s, sx, above}, then the keys
+  const size_t rec = score_record_bytes(a.top);
+  char *base = (char *)a.part + (size_t)row * a.chunks * rec;
+  const __amdgpu_buffer_rsrc_t mine = coherent_rsrc(base + chunk * rec, (uint32_t)rec);
+  if (tid == 0) st16_coherent(mine, 0, 0, f32x4{m_raw, s, sx, __int_as_float(above)});
+  if (2 * tid < a.top) {
+    const u64 k0 = lds.top[2 * tid], k1 = 2 * tid + 1 < a.top ? lds.top[2 * tid + 1] : 0;
+    st16_coherent(mine, 16 + 16 * tid, 0, f32x4{__uint_as_float((uint32_t)k0), __uint_as_float((uint32_t)(k0 >> 32)),
+                                                __uint_as_float((uint32_t)k1), __uint_as_float((uint32_t)(k1 >> 32))});
+  }
+  wait_vmcnt<0>();
+  asm volatile("" ::: "memory");
+  __syncthreads();
+  if (tid == 0) {
+    const unsigned got = __hip_atomic_fetch_add(a.cnt + row, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    if (got == (unsigned)a.chunks - 1) __hip_atomic_store(a.cnt + row, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    lds.arrived = got;
+  }
+  __syncthreads();
+  if (lds.arrived != (unsigned)a.chunks - 1) return;
+
+  // join, a chunk's numbers on each of the first threads (kScoreMaxChunks <= 256)
+  f32x4 r = {-INFINITY, 0.f, 0.f, 0.f};
+  const __amdgpu_buffer_rsrc_t all = coherent_rsrc(base, (uint32_t)(rec * a.chunks));
+  if (tid < a.chunks) r = ld16_coherent(all, (uint32_t)(tid * rec), 0);
+  // pairs of keys: pair p of chunk c on thread c pairs + p, `rounds` of them
+  const int pairs = (a.top + 1) / 2;
+  constexpr int kRounds = kScoreMaxChunks * (kScoreMaxTop / 2) / kScoreThreads;
+  u64 keys[2 * kRounds];
+  uint32_t best = 0;
+#pragma unroll
+  for (int i = 0; i < kRounds; ++i) {
+    const int at = tid + i * kScoreThreads;
+    keys[2 * i] = keys[2 * i + 1] = 0;
+    if (at < a.chunks * pairs) {
+      const int c = at / pairs, p = at - c * pairs;
+      const f32x4 w = ld16_coherent(all, (uint32_t)(c * rec + 16 + 16 * p), 0);
+      keys[2 * i] = (u64)__float_as_uint(w[1]) << 32 | __float_as_uint(w[0]);
+      keys[2 * i + 1] = (u64)__float_as_uint(w[3]) << 32 | __float_as_uint(w[2]);
+      best = max(best, __float_as_uint(w[1]));  // a record's keys come in order: the pair's first is the larger
+    }
+  }
+  const float wmx = wave_max(r[0]);
+  if (lane == 0) lds.m[wave] = wmx;
+  if (a.top) {
+    const uint32_t f = kth_floor(best, a.top);
+    if (lane == 0) lds.floor[wave] = f;
+  }
+  __syncthreads();
+  const float M_raw = fmaxf(fmaxf(lds.m[0], lds.m[1]), fmaxf(lds.m[2], lds.m[3]));
+  const float M = M_raw == -INFINITY ? 0.f : M_raw;
+  // a chunk's terms move to the common maximum: t + (its m - M) log2(e)
+  const float by = r[0] == -INFINITY ? 0.f : (r[0] - M) * kLog2e;
+  const float f2 = r[0] == -INFINITY && r[1] == 0.f ? 0.f : __builtin_amdgcn_exp2f(by);
+  s = wave_sum(r[1] * f2);
+  sx = wave_sum((r[2] + (f2 == 0.f ? 0.f : r[1] * by)) * f2);
+  above = __float_as_int(r[3]);
+#pragma unroll
+  for (int off = 32; off > 0; off >>= 1) above += __shfl_xor(above, off, 64);
+  __syncthreads();
+  if (lane == 0) {
+    lds.s[wave] = s;
+    lds.sx[wave] = sx;
+    lds.above[wave] = above;
+  }
+  if (a.top) {
+    const uint32_t f = max(max(lds.floor[0], lds.floor[1]), max(lds.floor[2], lds.floor[3]));
+    auto each = [&](auto &&use) {
+#pragma unroll
+      for (int i = 0; i < 2 * kRounds; ++i)
+        if (keys[i]) use(keys[i]);
+    };
+    select_top(a.top, f, best >= f, each, lds);
+  } else {
+    __syncthreads();
+  }
+  s = (lds.s[0] + lds.s[1]) + (lds.s[2] + lds.s[3]);
+  sx = (lds.sx[0] + lds.sx[1]) + (lds.sx[2] + lds.sx[3]);
+  above = (lds.above[0] + lds.above[1]) + (lds.above[2] + lds.above[3]);
+  finish(a, row, id, xt, M, s, sx, above, lds);
+}
+
+// ---------------------------------------------------------------- launcher
+int score_chunks(int n_vocab, int dtype, int vecs) {
+  const int ve = dtype == 0 ? 4 : 8, chunk = kScoreThreads * vecs * ve;
+  return (n_vocab + ve - 1 + chunk - 1) / chunk;  // a row may begin up to ve - 1 elements into its first vector
+}
+// The longest chunks that still make about four workgroups a CU; the
+// shortest where no length does.
+int score_vecs(int n, int n_vocab, int dtype) {
+  int vecs = kScoreMaxVecs;
+  while (vecs > 2 && (long long)n * score_chunks(n_vocab, dtype, vecs) < 1024 &&
+         score_chunks(n_vocab, dtype, vecs / 2) <= kScoreMaxChunks)
+    vecs /= 2;
+  return vecs;
+}
+
+template <typename T>
+static void go(const ScoreArgs &a, int vecs, hipStream_t st) {
+  const dim3 grid(a.n * a.chunks), block(kScoreThreads);
+  if (vecs == 2) hipLaunchKernelGGL((score_kernel<T, 2>), grid, block, 0, st, a);
+  else if (vecs == 4) hipLaunchKernelGGL((score_kernel<T, 4>), grid, block, 0, st, a);
+  else if (vecs == 8) hipLaunchKernelGGL((score_kernel<T, 8>), grid, block, 0, st, a);
+  else hipLaunchKernelGGL((score_kernel<T, 16>), grid, block, 0, st, a);
+}
+
+hipError_t launch_score(const ScoreArgs &a, int dtype, int vecs, hipStream_t st) {
+  if (dtype == 0) go<float>(a, vecs, st);
+  else go<u16>(a, vecs, st);
+  return hipGetLastError();
+}
+
+}  // namespace lora

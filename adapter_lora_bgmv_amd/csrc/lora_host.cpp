@@ -13,6 +13,7 @@
 #include <mutex>
 
 #include "../../include/lora_mi355x.h"
+#include "host.hpp"
 #include "launch.hpp"
 
 using namespace lora;
@@ -25,6 +26,12 @@ namespace {
 thread_local char g_err[512];
 thread_local hipEvent_t g_prof[4];
 thread_local bool g_prof_on = false;
+int g_dev_ok[64];   // 0 unknown, 1 gfx950, -1 other
+int g_dev_cus[64];  // compute units, once known
+
+}  // namespace
+
+namespace lora {
 
 void prof_record(int i, hipStream_t st) {
   if (g_prof_on) (void)hipEventRecord(g_prof[i], st);
@@ -45,12 +52,7 @@ int launch_status(hipError_t e, const char *what) {
   return LORA_OK;
 }
 
-bool aligned16(const void *p) { return ((uintptr_t)p & 15u) == 0; }
-
 // ------------------------------------------------------------ device check
-int g_dev_ok[64];   // 0 unknown, 1 gfx950, -1 other
-int g_dev_cus[64];  // compute units, once known
-
 int check_device(const char *what) {
   int dev = 0;
   if (hipGetDevice(&dev) != hipSuccess)
@@ -69,6 +71,10 @@ int check_device(const char *what) {
   if (g_dev_ok[dev] < 0) return fail(LORA_ERR_LAUNCH, "%s: device %d is not a gfx950", what, dev);
   return LORA_OK;
 }
+
+}  // namespace lora
+
+namespace {
 
 // The current device's compute units (0 if it was never checked).
 int current_cus() {
@@ -249,7 +255,6 @@ WsLayout ws_layout(const Cfg &c, int n, int R, int k_in, size_t data_base = 0) {
   return w;
 }
 
-constexpr uint32_t kMaxRows = 16384;
 constexpr uint32_t kMaxRank = 256;
 
 // ------------------------------------------------------------ validation

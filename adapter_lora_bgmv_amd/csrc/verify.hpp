@@ -1,0 +1,132 @@
+// verify.hpp -- arguments and launchers of the KV cache, attention and scoring kernels.  Not part of the ABI.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "common.hpp"
+
+namespace lora {
+
+// The cache and the sequences of one call (lora_kv_cache, lora_kv_seqs), as the kernels take them.
+struct KvDev {
+  uint8_t *k, *v;    // [n_pages][H][P D] codes
+  uint8_t *ke, *ve;  // [n_pages][H] exponent bytes
+  int n_pages, H;
+  int page_shift;    // log2 of the page's tokens P
+  const int32_t *table;  // [n_seqs][table_stride]
+  int table_stride, max_pages;
+  const int32_t *indptr;  // [n_seqs + 1]
+  const int32_t *kv_len;  // [n_seqs]
+  int n_seqs, n;
+};
+
+// One sequence's rows and tokens, made safe: rows [row0, row0 + rows) lie in
+// [0, n); row j holds position start + j, start = len - rows, which may be
+// negative; tokens at or past `cap` have no page.
+struct SeqDev {
+  int row0, rows, len, start;
+};
+
+__device__ __forceinline__ SeqDev load_seq(const KvDev &a, int i) {
+  const int lo = a.indptr[i], hi = a.indptr[i + 1], len = a.kv_len[i];
+  SeqDev s;
+  s.row0 = min(max(lo, 0), a.n);
+  s.rows = max(min(max(hi, 0), a.n) - s.row0, 0);
+  s.len = max(len, 0);
+  s.start = s.len - s.rows;
+  return s;
+}
+
+// Tokens the page table has room for (the host keeps max_pages << page_shift below 2^31).
+__device__ __forceinline__ int kv_cap(const KvDev &a) { return a.max_pages << a.page_shift; }
+
+// The page of logical page `p` of sequence i, or -1: an entry outside
+// [0, n_pages) names none.
+__device__ __forceinline__ int page_of(const KvDev &a, int i, int p) {
+  const int id = a.table[(size_t)i * a.table_stride + p];
+  return (unsigned)id < (unsigned)a.n_pages ? id : -1;
+}
+
+__device__ __forceinline__ int wave_incl_scan(int v, int lane) {
+#pragma unroll
+  for (int off = 1; off < 64; off <<= 1) {
+    const int o = __shfl_up(v, off, 64);
+    if (lane >= off) v += o;
+  }
+  return v;
+}
+
+// The e4m3 byte pair conversions (gfx950).
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+
+hipError_t launch_kv_write(const KvDev &kv, int dim, int dtype, const void *k, int k_stride, const void *v, int v_stride,
+                           hipStream_t st);
+hipError_t launch_kv_read(const KvDev &kv, int dim, int dtype, void *k, int k_stride, void *v, int v_stride,
+                          hipStream_t st);
+
+// The attention over the cache (k_attend.hip).
+struct AttendArgs {
+  KvDev kv;
+  const void *q;  // [n][q_stride], head h at h D
+  int q_stride;
+  void *out;      // [n][out_stride]
+  int out_stride;
+  float *lse;     // [n][heads] or null
+  int heads, G;   // query heads, and per key/value head
+  float scale;    // softmax scale times log2(e)
+  int window;     // 0: none
+  int cols_lo, cols_hi;  // takes the sequences whose rows x G lie in (cols_lo, cols_hi]
+  int per_head;   // workgroups per key/value head that the tiles are spread over
+  float *part;    // partial results of split units, kAttendSlots slots
+  unsigned *cnt;  // [2][kAttendSlots] arrivals of a group of chunks and of a unit's groups, zero between calls
+};
+// Workgroups that a launch's tiles are spread over, and the partial slots
+// that takes: a unit is split into nc > 1 chunks only where its tiles exceed
+// a chunk's, so the split units' chunks are fewer than twice as many.
+constexpr int kAttendTarget = 512;
+constexpr int kAttendSlots = 2 * kAttendTarget;
+// Columns (row, query head of the group) of a unit: 16 nb where the waves
+// share out the tiles, 64 nb where they share out the columns (wide).
+constexpr int attend_wide_nb(int dim) { return dim > 128 ? 1 : 2; }
+constexpr int attend_max_nb(int dim) { return dim > 128 ? 1 : 3; }
+constexpr int kAttendNarrowCols = 64;  // sequences of more columns take the wide form (bf16)
+hipError_t launch_attend(const AttendArgs &a, int dim, int dtype, int nb, bool wide, hipStream_t st);
+
+// Scores of given tokens over rows of logits (k_score.hip).
+constexpr int kScoreThreads = 256;
+constexpr int kScoreMaxTop = 32;
+constexpr int kScoreMaxChunks = 128;  // of a row
+constexpr int kScoreMaxVecs = 16;     // 16-byte vectors a thread holds
+struct ScoreArgs {
+  const void *logits;  // [n][stride]
+  long long stride;
+  int n, n_vocab, top;
+  const int32_t *ids;  // [n]
+  float *logp, *entropy;  // [n], or null
+  int32_t *rank;          // [n] or null
+  int32_t *top_ids;       // [n][top]
+  float *top_logp;        // [n][top]
+  int chunks;      // workgroups of a row
+  float *part;     // [n][chunks] records, see k_score.hip
+  unsigned *cnt;   // [n] arrivals, zero between calls
+};
+// 16-byte vectors per thread for n rows, and the chunks that makes of a row.
+int score_vecs(int n, int n_vocab, int dtype);
+int score_chunks(int n_vocab, int dtype, int vecs);
+// Bytes of one chunk's record: maximum, sum, weighted sum, count, then the top keys.
+__host__ __device__ inline size_t score_record_bytes(int top) { return 16 + 8 * (size_t)((top + 1) / 2 * 2); }
+hipError_t launch_score(const ScoreArgs &a, int dtype, int vecs, hipStream_t st);
+
+// Upper bound of the pages that n rows of n_seqs sequences touch: a sequence
+// of m rows touches at most m pages and at most (m + P - 2) / P + 1.
+inline int kv_max_touched(int n, int n_seqs, int page) {
+  const int s = n < n_seqs ? n : n_seqs;
+  const int by_page = n / page + 2 * s;
+  return n < by_page ? n : by_page;
+}
+
+}  // namespace lora

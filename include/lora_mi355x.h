@@ -186,7 +186,8 @@ size_t lora_workspace_bytes(int32_t op, int32_t dtype, uint32_t n_rows, uint32_t
  * measured apart from everything else).  With n >= 4 HIP events set, every
  * later fused call on the calling thread (lora_apply, lora_apply_segmented,
  * lora_apply_moe_gather, lora_apply_moe_grouped, lora_apply_stack,
- * lora_embed_rows) records on its stream events[0] before its first kernel, events[1] right before
+ * lora_embed_rows, lora_kv_write, lora_kv_read, lora_kv_attend,
+ * lora_token_logprobs) records on its stream events[0] before its first kernel, events[1] right before
  * its main kernel (after the route plan and shrink kernel where there is
  * one), events[2] right after the main kernel, and events[3] after its last
  * kernel (the decode epilogue, or a stack's further levels, where there are
@@ -398,6 +399,139 @@ int lora_apply_stack(int32_t dtype, uint32_t n_out, uint32_t k_in, const void *W
                      const int32_t *const *seq_slots, uint32_t n_levels, const void *x,
                      uint32_t x_row_stride, uint32_t n, void *y, uint32_t y_row_stride,
                      void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Verify-step operators: the KV cache behind a [Q|K|V] projection, the
+ * attention that reads it, and the scores of given tokens behind the
+ * vocabulary projection.  The conventions above hold: caller-owned buffers,
+ * launches on `stream` only, device values (lengths, page ids, token ids)
+ * never validated on the host and any value of them defined below.
+ *
+ * The cache keeps keys and values in 8 bits.  It is cut into pages of
+ * page_tokens tokens; a page's head holds page_tokens x head_dim e4m3 codes
+ * of K, as many of V, and one scale byte for each.  A code c under scale
+ * byte e stands for c * 2^(e - 127).  All arrays are [dev]:
+ *   k, v              [n_pages][n_kv_heads][page_tokens * head_dim] bytes
+ *   k_scale, v_scale  [n_pages][n_kv_heads] bytes
+ * Within a page's head (token t, dim d) lies, in the order in which the
+ * attention's matrix operands read it, at byte
+ *   K: (((t/16 * 4 + t%16/4) * (head_dim/16) + d/16) * 4 + t%4) * 16 + d%16
+ *   V: (t/16 * head_dim + d) * 16 + t%16
+ * lora_kv_write and lora_kv_read are the way in and out of that order; pages
+ * may be moved whole.  The struct itself is [host].
+ */
+typedef struct lora_kv_cache {
+  void *k;
+  void *v;
+  uint8_t *k_scale;
+  uint8_t *v_scale;
+  uint32_t n_pages;
+  uint32_t n_kv_heads;
+  uint32_t head_dim;    /* 64, 128 or 256 */
+  uint32_t page_tokens; /* 16, 32, 64 or 128 */
+} lora_kv_cache;
+
+/*
+ * The sequences of one call.  All arrays are [dev] int32.  Sequence i owns
+ * the call's rows row_indptr[i] .. row_indptr[i+1]-1 (row_indptr is
+ * [n_seqs+1], non-decreasing), which are its LAST tokens: with m rows and
+ * kv_len[i] tokens, these rows' own included, row j stands at position
+ * kv_len[i] - m + j.  The same struct serves the write, the attention and the
+ * read of a step.  Position p lies in page
+ * page_table[i * table_stride + p / page_tokens]; an entry outside
+ * [0, n_pages), a position below 0 and one at or past max_pages *
+ * page_tokens name no page: such a token is not written, not read back, and
+ * seen by no row.  A negative kv_len counts as 0.  Row ranges that leave
+ * [0, n) or decrease never make a call touch memory outside its operands,
+ * but which rows are processed is then unspecified, and a workspace must be
+ * zero-filled again.
+ * max_rows is a bound [host] on every sequence's rows (0: none known): it
+ * chooses kernels and never changes which rows are processed.
+ */
+typedef struct lora_kv_seqs {
+  const int32_t *page_table; /* [n_seqs][table_stride >= max_pages] */
+  const int32_t *row_indptr; /* [n_seqs + 1] */
+  const int32_t *kv_len;     /* [n_seqs] */
+  uint32_t n_seqs;
+  uint32_t max_pages;
+  uint32_t table_stride;
+  uint32_t max_rows;
+} lora_kv_seqs;
+
+/*
+ * Quantises rows into the cache.  k and v are [dev] [n][row stride], head h
+ * of a row at h * head_dim (the K and the V columns of an interleaved
+ * [Q|K|V] row, say).  A page's scale is the smallest power of two s with
+ * |x| <= 448 s for its finite values, within 2^-117 .. 2^120, and every value
+ * is rounded once to nearest even; infinities and NaN are stored as NaN.  A
+ * page that the call begins at its first token starts afresh.  A page that
+ * held tokens before the call's keeps at least its scale: where the new
+ * tokens need a larger one, the old tokens' codes move to it (exactly, but
+ * for those that become subnormal).  Bytes of a page past the call's tokens
+ * are left alone.  A page that a call writes may belong to one sequence only.
+ * Strides are multiples of 8 (bf16) or 4 (f32) elements and pointers 16-byte
+ * aligned.  No workspace.
+ */
+int lora_kv_write(const lora_kv_cache *cache, const lora_kv_seqs *seqs, int32_t dtype, const void *k,
+                  uint32_t k_row_stride, const void *v, uint32_t v_row_stride, uint32_t n, void *stream);
+
+/*
+ * Reads the tokens of the call's rows back, the inverse of lora_kv_write with
+ * the same arguments (with row_indptr the running sum of kv_len: whole
+ * sequences).  The values are exact in either dtype.  Rows whose position
+ * names no page are not written.
+ */
+int lora_kv_read(const lora_kv_cache *cache, const lora_kv_seqs *seqs, int32_t dtype, void *k,
+                 uint32_t k_row_stride, void *v, uint32_t v_row_stride, uint32_t n, void *stream);
+
+/*
+ * Attention of the call's rows over the cache:
+ *   out[row][h] = sum over tokens t of softmax_t(scale q[row][h] . k_t) v_t,
+ * with key/value head h / (n_heads / n_kv_heads), over the tokens at
+ * positions up to the row's own and, for window > 0, the last `window` of
+ * those.  lse (may be NULL) is [dev] f32 [n][n_heads]: the natural logarithm
+ * of the softmax denominators.  A row that sees no token is written as zeros,
+ * its lse -infinity; a row outside every sequence is not written.  q and out
+ * are [dev] [n][row stride], head h at h * head_dim, strides and pointers as
+ * in lora_kv_write; scale is finite and above 0.  What a token that a row
+ * does not see holds, NaN included, does not reach that row.  Scores, sums
+ * and outputs run in f32 (bf16 calls round the weights to 11 bits before the
+ * product with v); out is rounded once.  The order of every sum follows from
+ * the call's lengths alone.  workspace [dev] of at least
+ * lora_kv_attend_workspace_bytes(...) bytes (a function of the head counts
+ * and sizes, dtype, n, n_seqs and max_rows), zero-filled before its first
+ * use with these.
+ */
+size_t lora_kv_attend_workspace_bytes(const lora_kv_cache *cache, const lora_kv_seqs *seqs, int32_t dtype,
+                                      uint32_t n_heads, uint32_t n);
+int lora_kv_attend(const lora_kv_cache *cache, const lora_kv_seqs *seqs, int32_t dtype, uint32_t n_heads,
+                   const void *q, uint32_t q_row_stride, float scale, uint32_t window, uint32_t n, void *out,
+                   uint32_t out_row_stride, float *lse, void *workspace, size_t workspace_bytes,
+                   void *stream);
+
+/*
+ * Scores of given tokens over rows of logits x [dev] [n][row_stride >=
+ * n_vocab], any alignment of whole elements (dtype is the logits'):
+ *   logp[i]    = x[i][token_ids[i]] - log sum exp x[i]
+ *   entropy[i] = -sum p log p over the row's distribution (may be NULL)
+ *   rank[i]    = 1 + the number of logits above the token's (may be NULL)
+ *   top_ids, top_logp [n][top]: the `top` largest by value, equal values by
+ *                the lower index first, top <= 32 (not read for top == 0)
+ * All outputs are [dev] f32 or int32, sums in f32.  Logits of -infinity have
+ * probability 0.  A token id outside [0, n_vocab) has logp -infinity and
+ * rank 0.  A row whose every logit is -infinity has logp, top_logp -infinity
+ * and entropy 0.  A row that holds NaN or +infinity has no distribution: its
+ * logp, entropy and top_logp are NaN, its rank and top_ids unspecified
+ * (top_ids in [0, n_vocab)).  workspace [dev] of at least
+ * lora_token_logprobs_workspace_bytes(...) bytes, which may be 0,
+ * zero-filled before its first use with a shape.
+ */
+#define LORA_MAX_VOCAB (1u << 20)
+size_t lora_token_logprobs_workspace_bytes(int32_t dtype, uint32_t n_vocab, uint32_t n, uint32_t top);
+int lora_token_logprobs(int32_t dtype, uint32_t n_vocab, const void *logits, uint32_t row_stride,
+                        const int32_t *token_ids, uint32_t n, uint32_t top, float *logp, float *entropy,
+                        int32_t *rank, int32_t *top_ids, float *top_logp, void *workspace,
+                        size_t workspace_bytes, void *stream);
 
 #ifdef __cplusplus
 }
