@@ -5,27 +5,32 @@
 //     entropy = log s - sum exp(x - m) (x - m) / s,
 //     rank   = 1 + the number of logits above x[id],
 //     top    = the `top` largest by (value, lower index first).
-// One pass over the logits: a workgroup's 256 threads take a chunk of the row
-// into registers (up to 16 vectors of 16 bytes a thread, all loads in flight
-// together), and everything above is computed from there.  The exponentials
-// run in base 2, t = (x - m) log2(e): the difference first, so that rows of
-// the type's lowest value stay finite.
+// One pass over the logits: a workgroup of 256 threads streams a row (or a
+// chunk of it, where rows are few), a batch of 32 logits a thread at a time
+// with the next batch's loads in flight, and every thread keeps its own
+// running maximum, sums and count; they meet once at the end.  The
+// exponentials run in base 2, t = (x - m) log2(e): the difference first, so
+// that rows of the type's lowest value stay finite.
 //
 // Top: the order is that of 64-bit keys, the value's bits in unsigned order
 // above the complement of the index, all of them different.  Of the 64
 // lanes' maxima a wave finds (by ballots, bit after bit) a value that `top`
-// of them reach; the largest of the four waves' values bounds the chunk's
-// `top` from below, and what reaches it, about `top` / 64 of each lane's
-// share, goes to a list in LDS.  An entry's place is the number of larger
-// keys in the list.  A list that would overflow (rows of equal values) takes
-// `top` rounds of the workgroup's maximum below the last instead.
+// of them reach: no smaller logit can be among the `top`.  A lane whose batch
+// reaches it puts what does on a list in LDS, and the wave's value is found
+// anew; after a few batches that is rare.  At the end the list shrinks to
+// what reaches the largest of the four waves' values, and an entry's place is
+// the number of larger keys.  Where the list overflows (equal or rising
+// logits) the chunk is read again for what reaches the final value, and where
+// even that is too much, once for every place.
 //
 // A row of several chunks leaves a record of each in the workspace; the last
 // chunk to arrive joins them, the lists by the same selection.
 //
-// HBM bounds large calls (every logit is read once), the exponentials and
-// compares follow closely: about 11 instructions a logit; latency bounds
+// HBM bounds large calls (every logit is read once) and the exponentials
+// and compares follow closely, about 12 issue slots a logit; latency bounds
 // small ones.
+#include <algorithm>
+
 #include "common.hpp"
 #include "verify.hpp"
 
@@ -33,6 +38,7 @@ namespace lora {
 
 constexpr int kScoreList = 1024;  // entries of the LDS list
 typedef unsigned long long u64;
+constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
 
 // Unsigned order of an f32's bits is its value's order.
 __device__ __forceinline__ uint32_t ordered(float x) {
@@ -87,40 +93,50 @@ __device__ __forceinline__ uint32_t kth_floor(uint32_t key, int k) {
 }
 
 struct ScoreLds {
-  u64 list[kScoreList];
+  u64 list[kScoreList], kept[kScoreList];
   u64 top[kScoreMaxTop];
   u64 red[4];
-  float m[4], s[4], sx[4], tot[4];
+  float m[4], s[4], sx[4];
   uint32_t floor[4];
   int above[4];
-  int count;
+  int count, kept_count;
   unsigned arrived;
 };
 
-// The `k` largest keys of all that `each` passes to its argument, in order,
-// into lds.top; keys are distinct and not 0.  `floor`: a value (upper half)
-// that at least k of the keys reach.  `each(f)` calls f(key) for the
-// thread's keys, `any` whether the thread may hold one that reaches the floor.
+// Puts a key on a list in LDS; what no longer fits is only counted.
+__device__ __forceinline__ void put(u64 *list, int *count, u64 key) {
+  const int at = atomicAdd(count, 1);
+  if (at < kScoreList) list[at] = key;
+}
+
+// The `k` largest keys into lds.top, in order (0 where there are fewer).
+// `floor`: a value (upper half) that at least k of the keys reach, if there
+// are k.  lds.list holds every key that reaches it, unless lds.count says
+// that it overflowed: then `each(f)` calls f(key) for the thread's keys.
+// Called by the whole workgroup after a barrier; ends with one.
 template <typename Each>
-__device__ __forceinline__ void select_top(int k, uint32_t floor, bool any, Each each, ScoreLds &lds) {
+__device__ __forceinline__ void select_top(int k, uint32_t floor, Each each, ScoreLds &lds) {
   const int tid = threadIdx.x;
-  if (tid == 0) lds.count = 0;
-  if (tid < k) lds.top[tid] = 0;  // a chunk may hold fewer
-  __syncthreads();
-  if (any)
-    each([&](u64 key) {
-      if ((uint32_t)(key >> 32) >= floor && key) {
-        const int at = atomicAdd(&lds.count, 1);
-        if (at < kScoreList) lds.list[at] = key;
-      }
-    });
-  __syncthreads();
   const int n = lds.count;
+  if (tid == 0) lds.kept_count = 0;
+  if (tid < k) lds.top[tid] = 0;
+  __syncthreads();
   if (n <= kScoreList) {
-    for (int c = tid; c < n; c += kScoreThreads) {
-      const u64 mine = lds.list[c];
+    for (int c = tid; c < n; c += kScoreThreads)
+      if ((uint32_t)(lds.list[c] >> 32) >= floor) put(lds.kept, &lds.kept_count, lds.list[c]);
+  } else {
+    each([&](u64 key) {
+      if ((uint32_t)(key >> 32) >= floor) put(lds.kept, &lds.kept_count, key);
+    });
+  }
+  __syncthreads();
+  const int kept = lds.kept_count;
+  if (kept <= kScoreList) {
+    for (int c = tid; c < kept; c += kScoreThreads) {
+      const u64 mine = lds.kept[c];
       int above = 0;
-      for (int i = 0; i < n; ++i) above += lds.list[i] > mine;
+#pragma unroll 4
+      for (int i = 0; i < kept; ++i) above += lds.kept[i] > mine;
       if (above < k) lds.top[above] = mine;
     }
     __syncthreads();
@@ -148,8 +164,6 @@ __device__ __forceinline__ void select_top(int k, uint32_t floor, bool any, Each
   }
 }
 
-constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
-
 // The results of a row from its maximum, sums, count and lds.top.
 __device__ __forceinline__ void finish(const ScoreArgs &a, int row, int id, float xt, float m, float s, float sx, int above,
                                        const ScoreLds &lds) {
@@ -169,73 +183,107 @@ __device__ __forceinline__ void finish(const ScoreArgs &a, int row, int id, floa
   }
 }
 
-template <typename T, int NV>
+template <typename T>
 __global__ __launch_bounds__(kScoreThreads) void score_kernel(ScoreArgs a) {
-  constexpr int VE = Vec<T>::N, kChunk = kScoreThreads * NV * VE;
+  constexpr int VE = Vec<T>::N, NV = kScoreBatch / VE, kStride = kScoreThreads * VE;
   __shared__ ScoreLds lds;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int row = blockIdx.x / a.chunks, chunk = blockIdx.x - row * a.chunks;
   const T *x = (const T *)a.logits + (long long)row * a.stride;
   // the grid of vectors begins at the 16-byte line that holds the row's first element
   const int skew = (int)(((uintptr_t)x & 15) / sizeof(T));
-  const int first = chunk * kChunk - skew + tid * VE;  // index of the thread's first element
-  const int id = a.ids ? a.ids[row] : -1;
+  const int begin = chunk * a.batches * (NV * kStride) - skew + tid * VE;  // index of the thread's first element
+  const int id = a.ids[row];
+  if (tid == 0) lds.count = 0;
+  __syncthreads();
 
-  uint4 v[NV];
   constexpr uint32_t kNegInf = sizeof(T) == 4 ? 0xff800000u : 0xff80ff80u;
+  auto load = [&](int at) -> uint4 {  // elements outside the row: -inf
+    if (at >= 0 && at + VE <= a.n_vocab) return ldg16(x + at);
+    uint32_t w[4] = {kNegInf, kNegInf, kNegInf, kNegInf};
+    if (at + VE > 0 && at < a.n_vocab) {
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int at = first + i * (kScoreThreads * VE);
-    if (at >= 0 && at + VE <= a.n_vocab) {
-      v[i] = ldg16(x + at);
-    } else {
-      v[i] = make_uint4(kNegInf, kNegInf, kNegInf, kNegInf);
-      if (at + VE > 0 && at < a.n_vocab) {
-        uint32_t w[4] = {kNegInf, kNegInf, kNegInf, kNegInf};
-#pragma unroll
-        for (int e = 0; e < VE; ++e)
-          if (at + e >= 0 && at + e < a.n_vocab) {
-            if constexpr (sizeof(T) == 4) w[e] = __float_as_uint(x[at + e]);
-            else w[e / 2] = e & 1 ? (w[e / 2] & 0xffffu) | (uint32_t)x[at + e] << 16 : (w[e / 2] & 0xffff0000u) | x[at + e];
-          }
-        v[i] = make_uint4(w[0], w[1], w[2], w[3]);
-      }
+      for (int e = 0; e < VE; ++e)
+        if (at + e >= 0 && at + e < a.n_vocab) {
+          if constexpr (sizeof(T) == 4) w[e] = __float_as_uint(x[at + e]);
+          else w[e / 2] = e & 1 ? (w[e / 2] & 0xffffu) | (uint32_t)x[at + e] << 16 : (w[e / 2] & 0xffff0000u) | x[at + e];
+        }
     }
-  }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+  };
+  uint4 next[NV];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) next[i] = load(begin + i * kStride);
   const bool there = (unsigned)id < (unsigned)a.n_vocab;
   const float xt = there ? Vec<T>::one(x + id) : INFINITY;  // nothing is above +inf
 
-  float mx = -INFINITY;
+  float m = -INFINITY, s = 0.f, sx = 0.f;  // the thread's maximum, and its sums against it
+  int above = 0;                           // the wave's
+  uint32_t floor = 0;                      // `top` of the wave's lanes reach it
+  for (int b = 0; b < a.batches; ++b) {
+    const int first = begin + b * (NV * kStride);
+    if (b * (NV * kStride) + begin - tid * VE >= a.n_vocab) break;  // the last chunk may hold fewer
+    uint4 v[NV];
 #pragma unroll
-  for (int i = 0; i < NV; ++i)
+    for (int i = 0; i < NV; ++i) v[i] = next[i];
+    if (b + 1 < a.batches) {
 #pragma unroll
-    for (int e = 0; e < VE; ++e) mx = fmaxf(mx, Vec<T>::at(v[i], e));
-  const float wm = wave_max(mx);
-  const bool holds = first < a.n_vocab;  // the thread has an element at all
-  if (a.top) {
-    const uint32_t f = kth_floor(holds ? ordered(mx) : 0u, a.top);
-    if (lane == 0) lds.floor[wave] = f;
+      for (int i = 0; i < NV; ++i) next[i] = load(first + (NV + i) * kStride);
+    }
+    float mx = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+      for (int e = 0; e < VE; ++e) mx = fmaxf(mx, Vec<T>::at(v[i], e));
+    if (__any(mx > m)) {
+      const float mn = fmaxf(m, mx);
+      const float by = m == -INFINITY ? 0.f : (m - mn) * kLog2e;  // with no maximum yet the sums are 0
+      const float f = __builtin_amdgcn_exp2f(by);
+      sx = (sx + (f == 0.f ? 0.f : s * by)) * f;
+      s *= f;
+      m = mn;
+    }
+    const bool holds = first < a.n_vocab;  // the lane has an element of the row in this batch
+    if (a.top && __any(holds && ordered(mx) >= floor)) {
+      // lanes without elements count as lower than any
+      floor = max(floor, kth_floor(begin < a.n_vocab ? ordered(m) : 0u, a.top));
+      if (holds && ordered(mx) >= floor) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+          for (int e = 0; e < VE; ++e) {
+            const int at = first + i * kStride + e;
+            const u64 key = key_of(Vec<T>::at(v[i], e), (uint32_t)at);
+            if ((uint32_t)(key >> 32) >= floor && at >= 0 && at < a.n_vocab) put(lds.list, &lds.count, key);
+          }
+      }
+    }
+    const float base = m == -INFINITY ? 0.f : m;
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+      for (int e = 0; e < VE; ++e) {
+        const float y = Vec<T>::at(v[i], e);
+        const float t = (y - base) * kLog2e, p = __builtin_amdgcn_exp2f(t);
+        s += p;
+        sx = fmaf(p, fmaxf(t, -1e4f), sx);  // p is 0 far below; the bound keeps 0 x inf out
+        above += __popcll(__ballot(y > xt));
+      }
   }
-  if (lane == 0) lds.m[wave] = wm;
+  const float wm = wave_max(m);
+  if (lane == 0) {
+    lds.m[wave] = wm;
+    lds.floor[wave] = floor;
+  }
   __syncthreads();
   const float m_raw = fmaxf(fmaxf(lds.m[0], lds.m[1]), fmaxf(lds.m[2], lds.m[3]));
-  const float m = m_raw == -INFINITY ? 0.f : m_raw;
-  float s = 0.f, sx = 0.f;
-  int above = 0;
-#pragma unroll
-  for (int i = 0; i < NV; ++i)
-#pragma unroll
-    for (int e = 0; e < VE; ++e) {
-      const float y = Vec<T>::at(v[i], e);
-      const float t = (y - m) * kLog2e, p = __builtin_amdgcn_exp2f(t);
-      s += p;
-      sx = fmaf(p, fmaxf(t, -1e4f), sx);  // p is 0 far below; the bound keeps 0 x inf out
-      above += y > xt;
-    }
-  s = wave_sum(s);
-  sx = wave_sum(sx);
-#pragma unroll
-  for (int off = 32; off > 0; off >>= 1) above += __shfl_xor(above, off, 64);
+  {
+    const float by = m == -INFINITY ? 0.f : (m - m_raw) * kLog2e;
+    const float f = __builtin_amdgcn_exp2f(by);
+    sx = wave_sum((sx + (f == 0.f ? 0.f : s * by)) * f);
+    s = wave_sum(s * f);
+  }
+  m = m_raw == -INFINITY ? 0.f : m_raw;
   if (lane == 0) {
     lds.s[wave] = s;
     lds.sx[wave] = sx;
@@ -244,15 +292,16 @@ __global__ __launch_bounds__(kScoreThreads) void score_kernel(ScoreArgs a) {
   if (a.top) {
     const uint32_t f = max(max(lds.floor[0], lds.floor[1]), max(lds.floor[2], lds.floor[3]));
     auto each = [&](auto &&use) {
-#pragma unroll
-      for (int i = 0; i < NV; ++i)
+      for (int i = 0; i < a.batches * NV; ++i) {
+        const uint4 w = load(begin + i * kStride);
 #pragma unroll
         for (int e = 0; e < VE; ++e) {
-          const int at = first + i * (kScoreThreads * VE) + e;
-          if (at >= 0 && at < a.n_vocab) use(key_of(Vec<T>::at(v[i], e), (uint32_t)at));
+          const int at = begin + i * kStride + e;
+          if (at >= 0 && at < a.n_vocab) use(key_of(Vec<T>::at(w, e), (uint32_t)at));
         }
+      }
     };
-    select_top(a.top, f, holds && ordered(mx) >= f, each, lds);
+    select_top(a.top, f, each, lds);
   } else {
     __syncthreads();
   }
@@ -312,6 +361,7 @@ __global__ __launch_bounds__(kScoreThreads) void score_kernel(ScoreArgs a) {
     const uint32_t f = kth_floor(best, a.top);
     if (lane == 0) lds.floor[wave] = f;
   }
+  if (tid == 0) lds.count = 0;
   __syncthreads();
   const float M_raw = fmaxf(fmaxf(lds.m[0], lds.m[1]), fmaxf(lds.m[2], lds.m[3]));
   const float M = M_raw == -INFINITY ? 0.f : M_raw;
@@ -336,7 +386,12 @@ __global__ __launch_bounds__(kScoreThreads) void score_kernel(ScoreArgs a) {
       for (int i = 0; i < 2 * kRounds; ++i)
         if (keys[i]) use(keys[i]);
     };
-    select_top(a.top, f, best >= f, each, lds);
+    if (best >= f)
+      each([&](u64 key) {
+        if ((uint32_t)(key >> 32) >= f) put(lds.list, &lds.count, key);
+      });
+    __syncthreads();
+    select_top(a.top, f, each, lds);
   } else {
     __syncthreads();
   }
@@ -347,32 +402,23 @@ __global__ __launch_bounds__(kScoreThreads) void score_kernel(ScoreArgs a) {
 }
 
 // ---------------------------------------------------------------- launcher
-int score_chunks(int n_vocab, int dtype, int vecs) {
-  const int ve = dtype == 0 ? 4 : 8, chunk = kScoreThreads * vecs * ve;
-  return (n_vocab + ve - 1 + chunk - 1) / chunk;  // a row may begin up to ve - 1 elements into its first vector
-}
-// The longest chunks that still make about four workgroups a CU; the
-// shortest where no length does.
-int score_vecs(int n, int n_vocab, int dtype) {
-  int vecs = kScoreMaxVecs;
-  while (vecs > 2 && (long long)n * score_chunks(n_vocab, dtype, vecs) < 1024 &&
-         score_chunks(n_vocab, dtype, vecs / 2) <= kScoreMaxChunks)
-    vecs /= 2;
-  return vecs;
+// Workgroups of a row, and the batches each takes: one where the rows alone
+// make about four workgroups a CU, otherwise as many as make that, down to a
+// batch each.
+ScoreSplit score_split(int n, int n_vocab, int dtype) {
+  const int ve = dtype == 0 ? 4 : 8, batch = kScoreThreads * kScoreBatch;
+  const int all = (n_vocab + ve - 1 + batch - 1) / batch;  // a row may begin up to ve - 1 elements into its first vector
+  const int want = std::min(all, (1024 + n - 1) / n);
+  ScoreSplit r;
+  r.batches = (all + want - 1) / want;
+  r.chunks = (all + r.batches - 1) / r.batches;
+  return r;
 }
 
-template <typename T>
-static void go(const ScoreArgs &a, int vecs, hipStream_t st) {
+hipError_t launch_score(const ScoreArgs &a, int dtype, hipStream_t st) {
   const dim3 grid(a.n * a.chunks), block(kScoreThreads);
-  if (vecs == 2) hipLaunchKernelGGL((score_kernel<T, 2>), grid, block, 0, st, a);
-  else if (vecs == 4) hipLaunchKernelGGL((score_kernel<T, 4>), grid, block, 0, st, a);
-  else if (vecs == 8) hipLaunchKernelGGL((score_kernel<T, 8>), grid, block, 0, st, a);
-  else hipLaunchKernelGGL((score_kernel<T, 16>), grid, block, 0, st, a);
-}
-
-hipError_t launch_score(const ScoreArgs &a, int dtype, int vecs, hipStream_t st) {
-  if (dtype == 0) go<float>(a, vecs, st);
-  else go<u16>(a, vecs, st);
+  if (dtype == 0) hipLaunchKernelGGL((score_kernel<float>), grid, block, 0, st, a);
+  else hipLaunchKernelGGL((score_kernel<u16>), grid, block, 0, st, a);
   return hipGetLastError();
 }
 

@@ -100,7 +100,7 @@ hipError_t launch_attend(const AttendArgs &a, int dim, int dtype, int nb, bool w
 constexpr int kScoreThreads = 256;
 constexpr int kScoreMaxTop = 32;
 constexpr int kScoreMaxChunks = 128;  // of a row
-constexpr int kScoreMaxVecs = 16;     // 16-byte vectors a thread holds
+constexpr int kScoreBatch = 32;       // logits of a thread at a time
 struct ScoreArgs {
   const void *logits;  // [n][stride]
   long long stride;
@@ -111,15 +111,17 @@ struct ScoreArgs {
   int32_t *top_ids;       // [n][top]
   float *top_logp;        // [n][top]
   int chunks;      // workgroups of a row
+  int batches;     // of a chunk
   float *part;     // [n][chunks] records, see k_score.hip
   unsigned *cnt;   // [n] arrivals, zero between calls
 };
-// 16-byte vectors per thread for n rows, and the chunks that makes of a row.
-int score_vecs(int n, int n_vocab, int dtype);
-int score_chunks(int n_vocab, int dtype, int vecs);
+struct ScoreSplit {
+  int chunks, batches;
+};
+ScoreSplit score_split(int n, int n_vocab, int dtype);
 // Bytes of one chunk's record: maximum, sum, weighted sum, count, then the top keys.
 __host__ __device__ inline size_t score_record_bytes(int top) { return 16 + 8 * (size_t)((top + 1) / 2 * 2); }
-hipError_t launch_score(const ScoreArgs &a, int dtype, int vecs, hipStream_t st);
+hipError_t launch_score(const ScoreArgs &a, int dtype, hipStream_t st);
 
 // Upper bound of the pages that n rows of n_seqs sequences touch: a sequence
 // of m rows touches at most m pages and at most (m + P - 2) / P + 1.

@@ -230,7 +230,7 @@ size_t lora_token_logprobs_workspace_bytes(int32_t dtype, uint32_t n_vocab, uint
   if (n == 0 || n > kMaxRows || n_vocab == 0 || n_vocab > LORA_MAX_VOCAB || top > (uint32_t)kScoreMaxTop ||
       (dtype != LORA_F32 && dtype != LORA_BF16))
     return 0;
-  const int chunks = score_chunks((int)n_vocab, dtype, score_vecs((int)n, (int)n_vocab, dtype));
+  const int chunks = score_split((int)n, (int)n_vocab, dtype).chunks;
   return chunks > 1 ? up256((size_t)n * 4) + (size_t)n * chunks * score_record_bytes((int)top) : 0;
 }
 
@@ -255,7 +255,6 @@ int lora_token_logprobs(int32_t dtype, uint32_t n_vocab, const void *logits, uin
   const size_t size = dtype == LORA_F32 ? 4 : 2;
   if ((uintptr_t)logits % size)
     return fail(LORA_ERR_UNSUPPORTED, "%s: logits %p must be aligned to their %zu bytes", what, logits, size);
-  const int vecs = score_vecs((int)n, (int)n_vocab, dtype);
   const size_t need = lora_token_logprobs_workspace_bytes(dtype, n_vocab, n, top);
   if (need && (!workspace || workspace_bytes < need))
     return fail(LORA_ERR_WORKSPACE, "%s: [n %u x n_vocab %u] top %u: workspace %p of %zu bytes, %zu needed", what, n, n_vocab, top,
@@ -275,11 +274,13 @@ int lora_token_logprobs(int32_t dtype, uint32_t n_vocab, const void *logits, uin
   a.rank = rank;
   a.top_ids = top_ids;
   a.top_logp = top_logp;
-  a.chunks = score_chunks((int)n_vocab, dtype, vecs);
+  const ScoreSplit split = score_split((int)n, (int)n_vocab, dtype);
+  a.chunks = split.chunks;
+  a.batches = split.batches;
   a.cnt = (unsigned *)workspace;
   a.part = (float *)((char *)workspace + up256((size_t)n * 4));
   hipStream_t st = (hipStream_t)stream;
-  return timed(what, st, [&] { return launch_score(a, dtype, vecs, st); });
+  return timed(what, st, [&] { return launch_score(a, dtype, st); });
 }
 
 }  // extern "C"
