@@ -64,6 +64,7 @@ class lora_kv_seqs(C.Structure):
 
 
 _lib = None
+_lookup = []  # the calls that look up the current stream, once torch is there
 
 
 def lib() -> C.CDLL:
@@ -131,8 +132,11 @@ def _ptr(t) -> Optional[int]:
 
 def _stream(stream) -> Optional[int]:
     if stream is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        if not _lookup:
+            import torch
+            _lookup.extend((torch.cuda.current_device, torch._C._cuda_getCurrentRawStream))
+        device, raw = _lookup  # the current stream's handle without a Stream object: 0.3 us for 2.9
+        return raw(device())
     return getattr(stream, "cuda_stream", stream)
 
 

@@ -7,14 +7,14 @@
 // and v_t = 2^b d_t with the page's exponents a, b and e4m3 codes c, d.
 //
 // The codes go into the matrix instructions as they are: e4m3 numbers are
-// exact in bf16 and in f16, so a code costs half a conversion instruction
-// and the scales never touch an element.  With S = q . c the weight times
-// the page's value scale is
-//     2^(S 2^a scale log2(e) + b - M),
-// one fma and one exp2 a score, and M, the running maximum of that exponent,
-// keeps it in (0, 1]; the accumulators sum it against the codes d and the
-// denominator sums it times 2^-b.  No choice of page scales overflows or
-// loses bits this way.
+// exact in bf16 and in f16, and the instruction that converts two of them
+// multiplies by a power of two as well, so the pages' scales cost nothing.
+// Keys become bf16, 2^a c, whose range holds every exponent.  Values of bf16
+// calls become f16, 2^b d: exact for b within [-21, 0] (pages whose largest
+// value lies between 1e-4 and 448), which is what models hold.  The weights
+// of other pages take the rest of the exponent, 2^rest p, and then two
+// maxima run, of the exponents with and without the rest, so that neither
+// the sums against v nor the denominators lose anything (`mixed`).
 //
 // A column is a (row, query head of the group) pair; a wave holds 16 NB
 // columns and walks tiles of 64 tokens.  K's tile is the A operand (64
@@ -22,32 +22,34 @@
 // tile is chosen so that lane (column, g) ends up with the scores of the 16
 // tokens of 16-token group g: those are the B operand of the second product
 // as they stand, V's 16 bytes of a dim the A operand, and a lane's 16 tokens
-// share one page, one a and one b.  No score crosses a lane but in the
-// column's maximum, and every load is 16 bytes a lane in runs of 256.
+// share one page, one a and one b.  The running maximum M is allowed to lag
+// the true one by 2^kLag: only a tile that exceeds it looks across lanes and
+// rescales the sums, which after a few tiles is rare.
 //
-// Rounding: bf16 calls take q as it is and round the weights to f16 (2^-12,
-// an eighth of the output's own half step); f32 calls split q and the
+// Rounding: bf16 calls take q as it is and round the weights, 2^10 at the
+// running maximum, to f16 (2^-12, an eighth of the output's own half step;
+// weights down to 2^-34 of the largest count); f32 calls split q and the
 // weights into three bf16 terms (24 bits) and take three products of each.
 // Scores, sums and outputs accumulate in f32.
 //
-// Two forms share the code.  Decode and verify (few columns a sequence): the
-// workgroup's four waves take every fourth tile of the unit and are joined
-// through LDS.  Wide (many rows): the waves take 16 NB columns each.  In
-// both, the call's tiles are shared out in chunks of equal length over about
-// kAttendTarget workgroups, from the lengths in device memory, so long and
-// short sequences balance; a unit (sequence, head, columns) of several
-// chunks is joined inside the launch by the last to arrive, in groups of
-// about the square root of their number so that no join is long.
+// Two forms share the code.  Narrow (up to 16 columns a sequence: decode):
+// each wave of a workgroup takes every fourth tile straight into registers,
+// and the four are joined through LDS.  Wide (more columns): the waves take
+// 16 NB columns each and share the tiles, which LDS-DMA brings in up to two
+// ahead.  In both, the call's tiles are shared out in chunks of equal length
+// over about one round of workgroups, from the lengths in device memory, so
+// long and short sequences balance; a unit (sequence, head, columns) of
+// several chunks leaves its sums in the workspace, and a second kernel joins
+// them.
 #include "common.hpp"
 #include "verify.hpp"
 
 namespace lora {
 
-constexpr int kTile = 64;      // tokens
-constexpr int kMaxGroup = 32;  // chunks of a group, groups of a unit
-static_assert(kMaxGroup * kMaxGroup >= kAttendTarget, "two levels of groups cover a unit's chunks");
-
-typedef int i32x2 __attribute__((ext_vector_type(2)));
+constexpr int kTile = 64;    // tokens
+constexpr float kLag = 5.f;  // log2 of how far the running maximum may lag
+constexpr float kTop = 10.f; // log2 of the weight at the running maximum: with the lag 2^15, in f16's range
+constexpr float kNone = -3e38f;  // the maximum of a column that saw nothing yet
 
 // max / sum over the four lane groups l / 16 that hold a column's tokens.
 __device__ __forceinline__ float groups_max(float x) {
@@ -63,20 +65,20 @@ __device__ __forceinline__ float groups_sum(float x) {
   return __uint_as_float(s[0]) + __uint_as_float(s[1]);
 }
 
-// Eight codes (two dwords) as a matrix operand.
-__device__ __forceinline__ uint4 codes_bf16(uint32_t lo, uint32_t hi) {
-  const bf16x2 a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.0f, false);
-  const bf16x2 b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.0f, true);
-  const bf16x2 c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.0f, false);
-  const bf16x2 d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.0f, true);
+// Eight codes (two dwords) times a power of two as a matrix operand.
+__device__ __forceinline__ uint4 codes_bf16(uint32_t lo, uint32_t hi, float scale) {
+  const bf16x2 a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, scale, false);
+  const bf16x2 b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, scale, true);
+  const bf16x2 c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, scale, false);
+  const bf16x2 d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, scale, true);
   return make_uint4(__builtin_bit_cast(uint32_t, a), __builtin_bit_cast(uint32_t, b), __builtin_bit_cast(uint32_t, c),
                     __builtin_bit_cast(uint32_t, d));
 }
-__device__ __forceinline__ uint4 codes_f16(uint32_t lo, uint32_t hi) {
-  const f16x2 a = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, 1.0f, false);
-  const f16x2 b = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, 1.0f, true);
-  const f16x2 c = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, 1.0f, false);
-  const f16x2 d = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, 1.0f, true);
+__device__ __forceinline__ uint4 codes_f16(uint32_t lo, uint32_t hi, float scale) {
+  const f16x2 a = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, scale, false);
+  const f16x2 b = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, scale, true);
+  const f16x2 c = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, scale, false);
+  const f16x2 d = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, scale, true);
   return make_uint4(__builtin_bit_cast(uint32_t, a), __builtin_bit_cast(uint32_t, b), __builtin_bit_cast(uint32_t, c),
                     __builtin_bit_cast(uint32_t, d));
 }
@@ -116,6 +118,9 @@ __device__ __forceinline__ uint32_t nan_bytes(uint32_t w) {
   return (f >> 7) * 0xffu;
 }
 
+// The lowest n of 16 bits, 0 <= n <= 16 once clamped.
+__device__ __forceinline__ uint32_t live_bits(int n) { return (1u << min(max(n, 0), 16)) - 1u; }
+
 // Bytes of four tokens from t0 that lie in [lo, hi).
 __device__ __forceinline__ uint32_t live_bytes(int t0, int lo, int hi) {
   const int a = min(max(lo - t0, 0), 4), b = min(max(hi - t0, 0), 4);
@@ -133,16 +138,21 @@ __device__ __forceinline__ int seq_blocks(const AttendArgs &a, const SeqDev &s) 
   const int cols = s.rows * a.G;
   return cols > a.cols_lo && cols <= a.cols_hi ? (cols + CB - 1) / CB : 0;
 }
-// Tiles that some row of the sequence sees; 1 where none does (its rows are written as zeros).
-__device__ __forceinline__ int seq_tiles(const AttendArgs &a, const SeqDev &s, int cap) {
+// Tiles that a unit of the sequence sees at most; 1 where it sees none (its rows are written as zeros).
+template <int CB>
+__device__ __forceinline__ int unit_tiles(const AttendArgs &a, const SeqDev &s, int cap) {
   const int lo = a.window ? max(0, s.start + 1 - a.window) : 0, hi = min(s.len, cap);
-  return hi > lo ? ((hi + kTile - 1) / kTile) - lo / kTile : 1;
+  if (hi <= lo) return 1;
+  const int all = (hi + kTile - 1) / kTile - lo / kTile;
+  // tokens under a window: its own and one more for every further row of the unit
+  return a.window ? min(all, (int)(((long long)a.window + CB / a.G + kTile) / kTile) + 1) : all;
 }
 
 // Item u of a head's list: units in order, each with its chunks.  Every wave
-// finds it by itself (lane l counts `per` sequences).
+// finds it by itself (lane l counts `per` sequences).  *slots: of a head's
+// split units together.
 template <int CB>
-__device__ __forceinline__ bool find_work(const AttendArgs &a, int u, int lane, Work *w) {
+__device__ __forceinline__ bool find_work(const AttendArgs &a, int u, int lane, Work *w, int *all_slots) {
   const int per = (a.kv.n_seqs + 63) >> 6, cap = kv_cap(a.kv);
   const int i0 = lane * per, i1 = min(i0 + per, a.kv.n_seqs);
   SeqDev first = {0, 0, 0, 0};  // the lane's only sequence where per is 1
@@ -150,26 +160,27 @@ __device__ __forceinline__ bool find_work(const AttendArgs &a, int u, int lane, 
   long long total = 0;
   for (int i = i0; i < i1; ++i) {
     const SeqDev s = i == i0 ? first : load_seq(a.kv, i);
-    total += (long long)seq_blocks<CB>(a, s) * seq_tiles(a, s, cap);
+    total += (long long)seq_blocks<CB>(a, s) * unit_tiles<CB>(a, s, cap);
   }
 #pragma unroll
   for (int off = 32; off > 0; off >>= 1) total += __shfl_xor(total, off, 64);
   const long long len = (total + a.per_head - 1) / a.per_head;
-  const int c = (int)min(max(len, 1ll), 1ll << 30);  // tiles of a chunk at most
+  const int c = (int)min(max(len, (long long)a.min_tiles), 1ll << 30);  // tiles of a chunk at most
   int items = 0, slots = 0;
   for (int i = i0; i < i1; ++i) {
     const SeqDev s = i == i0 ? first : load_seq(a.kv, i);
-    const int b = seq_blocks<CB>(a, s), nc = (seq_tiles(a, s, cap) + c - 1) / c;
+    const int b = seq_blocks<CB>(a, s), nc = (unit_tiles<CB>(a, s, cap) + c - 1) / c;
     items += b * nc;
     slots += nc > 1 ? b * nc : 0;
   }
   const int incl = wave_incl_scan(items, lane), sincl = wave_incl_scan(slots, lane);
+  *all_slots = __builtin_amdgcn_readlane(sincl, 63);
   int found = -1, block = 0, chunk = 0, nc_of = 1, slot = 0;
   if (u < incl && u >= incl - items) {
     int at = incl - items, sat = sincl - slots;
     for (int i = i0; i < i1; ++i) {
       const SeqDev s = i == i0 ? first : load_seq(a.kv, i);
-      const int b = seq_blocks<CB>(a, s), nc = (seq_tiles(a, s, cap) + c - 1) / c;
+      const int b = seq_blocks<CB>(a, s), nc = (unit_tiles<CB>(a, s, cap) + c - 1) / c;
       if (u < at + b * nc) {
         found = i;
         nc_of = nc;
@@ -200,118 +211,307 @@ __device__ __forceinline__ bool find_work(const AttendArgs &a, int u, int lane, 
 }
 
 // ---------------------------------------------------------------- results
-// Four dims of a finished column: row0 + j, head; v already divided.
+// The exponents b of values that the matrix operand takes, as bytes, and
+// what it adds to them.
 template <bool F32>
-__device__ __forceinline__ void store_out(const AttendArgs &a, int row, int head, int D, int d, f32x4 v) {
-  if constexpr (F32)
-    *(float4 *)((float *)a.out + (size_t)row * a.out_stride + head * D + d) = make_float4(v[0], v[1], v[2], v[3]);
-  else
-    *(uint2 *)((u16 *)a.out + (size_t)row * a.out_stride + head * D + d) =
-        make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
+struct ValueExp {
+  static constexpr int kLo = F32 ? 10 : 106, kHi = F32 ? 227 : 127, kAdd = F32 ? 0 : 6;
+};
+// What a column's sums are multiplied by at the end.  A row that saw nothing
+// has l = 0 and is zero; a NaN denominator stays one.
+template <bool F32>
+__device__ __forceinline__ float final_scale(float M, float Ml, float l) {
+  return l == 0.f ? 0.f : 1.f / l * __builtin_amdgcn_exp2f(M - Ml - (float)ValueExp<F32>::kAdd);
 }
-__device__ __forceinline__ void store_lse(const AttendArgs &a, int row, int head, float M, float l) {
-  // a column that saw nothing has M = -inf and l = 0
-  if (a.lse) a.lse[(size_t)row * a.heads + head] = M == -INFINITY ? -INFINITY : 0.6931471805599453f * (M + __builtin_amdgcn_logf(l));
+// Four dims of a finished column.
+template <bool F32>
+__device__ __forceinline__ void store_out(void *out, size_t at, f32x4 v) {
+  if constexpr (F32) *(float4 *)((float *)out + at) = make_float4(v[0], v[1], v[2], v[3]);
+  else *(uint2 *)((u16 *)out + at) = make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
 }
-// A row that sees nothing is zero; a NaN denominator stays one.
-__device__ __forceinline__ float denominator(float l) { return l == 0.f ? 0.f : 1.f / l; }
+__device__ __forceinline__ float lse_of(float Ml, float l) {
+  return l == 0.f ? -INFINITY : 0.6931471805599453f * (Ml - kTop + __builtin_amdgcn_logf(l));
+}
 
-// A partial result's place: [CB][D] sums, then M and l per column.
-template <int D, int CB>
-struct Slot {
-  static constexpr int kFloats = CB * (D + 2);
-  float *p;
-  __device__ Slot(const AttendArgs &a, int i) : p(a.part + (size_t)i * kFloats) {}
-  __device__ __amdgpu_buffer_rsrc_t sums() const { return coherent_rsrc(p, CB * D * 4); }
-  __device__ void put_ml(int col, float M, float l) const {
-    __hip_atomic_store(p + CB * D + col, M, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    __hip_atomic_store(p + CB * D + CB + col, l, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+// ---------------------------------------------------------------- a wave's columns
+template <int D, int NB, bool F32>
+struct Columns {
+  static constexpr int NS = D / 32, ND = D / 16, NT = F32 ? 3 : 1;
+  uint4 q[NB][NS][NT];
+  f32x4 acc[NB][ND];
+  // sums run against 2^(M - kTop), the denominators l against 2^(Ml - kTop); Ml is M unless `mixed`
+  float M[NB], Ml[NB], l[NB];
+  int hi[NB], lo[NB];  // a column sees the tokens [lo, hi)
+  bool mixed;
+
+  // Columns [c0, c1) of the sequence.
+  __device__ __forceinline__ void load(const AttendArgs &a, const Work &w, int h, int c0, int c1, int r, int g) {
+    mixed = false;
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) {
+      const int c = c0 + nb * 16 + r;
+      const bool ok = c < c1;
+      const int j = ok ? c / a.G : 0;
+      hi[nb] = ok ? w.s.start + j + 1 : 0;
+      lo[nb] = ok && a.window ? w.s.start + j + 1 - a.window : 0;
+      const size_t at = (size_t)(w.s.row0 + j) * a.q_stride + (h * a.G + (ok ? c - j * a.G : 0)) * D;
+#pragma unroll
+      for (int s = 0; s < NS; ++s) {
+        const int d = 16 * (4 * (s >> 1) + g) + 8 * (s & 1);
+        if constexpr (F32) {
+          float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+          if (ok) {
+            const uint4 u = ldg16((const float *)a.q + at + d), v = ldg16((const float *)a.q + at + d + 4);
+            x[0] = __uint_as_float(u.x); x[1] = __uint_as_float(u.y); x[2] = __uint_as_float(u.z); x[3] = __uint_as_float(u.w);
+            x[4] = __uint_as_float(v.x); x[5] = __uint_as_float(v.y); x[6] = __uint_as_float(v.z); x[7] = __uint_as_float(v.w);
+          }
+          split3(x, q[nb][s]);
+        } else {
+          q[nb][s][0] = ok ? ldg16((const u16 *)a.q + at + d) : z4();
+        }
+      }
+      M[nb] = Ml[nb] = kNone;
+      l[nb] = 0.f;
+#pragma unroll
+      for (int dt = 0; dt < ND; ++dt) acc[nb][dt] = f32x4{0.f, 0.f, 0.f, 0.f};
+    }
+  }
+
+  // The weights of one tile's scores S, as operands; the sums so far are
+  // rescaled where the maximum moves.  `rest` is what the lane's value
+  // exponent leaves over (0 unless MIXED).
+  template <bool MIXED>
+  __device__ __forceinline__ void weigh(const f32x4 (&S)[NB][4], float cs, float rest, uint4 (&pf)[NB][2][NT]) {
+    float top[NB], topl[NB];
+    bool far = false;
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) {
+      float mx = S[nb][0][0];
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) mx = fmaxf(mx, S[nb][j][i]);
+      topl[nb] = mx * cs;
+      top[nb] = MIXED ? topl[nb] + rest : topl[nb];
+      far |= top[nb] > M[nb] + kLag;
+      if (MIXED) far |= topl[nb] > Ml[nb] + kLag;
+    }
+    if (__any(far)) {
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb) {
+        const float Mn = fmaxf(M[nb], groups_max(top[nb])), f = __builtin_amdgcn_exp2f(M[nb] - Mn);
+        M[nb] = Mn;
+        if (MIXED) {
+          const float Mln = fmaxf(Ml[nb], groups_max(topl[nb]));
+          l[nb] *= __builtin_amdgcn_exp2f(Ml[nb] - Mln);
+          Ml[nb] = Mln;
+        } else {
+          l[nb] *= f;
+        }
+#pragma unroll
+        for (int dt = 0; dt < ND; ++dt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[nb][dt][e] *= f;
+      }
+    }
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) {
+      const float b = kTop - M[nb] + (MIXED ? rest : 0.f), bl = kTop - Ml[nb];
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        float p[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float x = S[nb][2 * s + (e >> 2)][e & 3];
+          p[e] = __builtin_amdgcn_exp2f(fmaf(x, cs, b));
+          l[nb] += MIXED ? __builtin_amdgcn_exp2f(fmaf(x, cs, bl)) : p[e];
+        }
+        if constexpr (F32) split3(p, pf[nb][s]);
+        else pf[nb][s][0] = make_uint4(pack_f16(p[0], p[1]), pack_f16(p[2], p[3]), pack_f16(p[4], p[5]), pack_f16(p[6], p[7]));
+      }
+    }
+  }
+
+  // sums += weights x sixteen dims' codes of the tile
+  __device__ __forceinline__ void add(int dt, const uint4 &x, float scale, const uint4 (&pf)[NB][2][NT]) {
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      const uint32_t lo = s ? x.z : x.x, hi = s ? x.w : x.y;
+      if constexpr (F32) {
+        const uint4 vf = codes_bf16(lo, hi, scale);
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+          for (int n = 0; n < 3; ++n) acc[nb][dt] = mfma16(vf, pf[nb][s][2 - n], acc[nb][dt]);
+      } else {
+        const uint4 vf = codes_f16(lo, hi, scale);
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) acc[nb][dt] = mfma16_f16(vf, pf[nb][s][0], acc[nb][dt]);
+      }
+    }
+  }
+
+  // One tile, from token tok.  kinfo is the record (PageInfo) of the group
+  // whose keys the lane loads (r / 4), vinfo of group g; kf(j, n) gives 16
+  // bytes of keys, vf(dt) 16 bytes of values; after_keys runs once the keys
+  // are used up.  [lo_all, hi_all) are the tokens that all columns see,
+  // [lo_any, hi_any) those that any column of the workgroup does.
+  template <typename K, typename V, typename F>
+  __device__ __forceinline__ void tile(int tok, int kinfo, int vinfo, float cs, int lo_all, int hi_all, int lo_any, int hi_any,
+                                       int g, K kf, V vf, F after_keys) {
+    using X = ValueExp<F32>;
+    const float ks = __uint_as_float((uint32_t)(kinfo & 255) << 23);
+    // scores: lane (column r, g) gets tokens 16 g + 4 j + i of the tile
+    f32x4 S[NB][4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb) S[nb][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int n = 0; n < D / 64; ++n) {
+        const uint4 x = kf(j, n);
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+          const uint4 kk = s ? codes_bf16(x.z, x.w, ks) : codes_bf16(x.x, x.y, ks);
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+            for (int t = 0; t < NT; ++t) S[nb][j] = mfma16(kk, q[nb][2 * n + s][NT - 1 - t], S[nb][j]);
+        }
+      }
+    }
+    after_keys();
+
+    const int tok0 = tok + 16 * g;
+    const bool page = vinfo >> 16;
+    const bool masked = tok < lo_all || tok + kTile > hi_all || __any(!page);
+    if (masked) {
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb) {
+        const uint32_t see = page ? live_bits(hi[nb] - tok0) & ~live_bits(lo[nb] - tok0) : 0u;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t m = (uint32_t)((int32_t)(see << (31 - 4 * j - i)) >> 31);
+            S[nb][j][i] = __uint_as_float((__float_as_uint(S[nb][j][i]) & m) | (0xff800000u & ~m));
+          }
+      }
+    }
+    const int ve = (vinfo >> 8) & 255, vc = min(max(ve, X::kLo), X::kHi);
+    const float vs = __uint_as_float((uint32_t)(vc + X::kAdd) << 23);
+    uint4 pf[NB][2][NT];
+    if (!mixed && __any(ve != vc)) {
+      mixed = true;
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb) Ml[nb] = M[nb];
+    }
+    if (mixed) weigh<true>(S, cs, (float)(ve - vc), pf);
+    else weigh<false>(S, cs, 0.f, pf);
+    if (!masked) {
+#pragma unroll
+      for (int dt = 0; dt < ND; ++dt) add(dt, vf(dt), vs, pf);
+      return;
+    }
+    // tokens that no column sees may hold anything: their bytes become
+    // zeros, and so do NaN codes, which would reach the columns that do
+    // not see them too
+    uint32_t keep[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) keep[i] = page ? live_bytes(tok0 + 4 * i, lo_any, hi_any) : 0u;
+#pragma unroll
+    for (int dt = 0; dt < ND; ++dt) {
+      uint4 x = vf(dt);
+      x = make_uint4(x.x & keep[0], x.y & keep[1], x.z & keep[2], x.w & keep[3]);
+      const uint4 nan = make_uint4(nan_bytes(x.x), nan_bytes(x.y), nan_bytes(x.z), nan_bytes(x.w));
+      if (__any((nan.x | nan.y | nan.z | nan.w) != 0)) {
+        x = make_uint4(x.x & ~nan.x, x.y & ~nan.y, x.z & ~nan.z, x.w & ~nan.w);
+        // columns that see a NaN value: count them by a product of ones (0x38 is 1.0 in e4m3, 0x3c00 in f16)
+        const uint4 lo4 = codes_f16(nan.x & 0x38383838u, nan.y & 0x38383838u, 1.f);
+        const uint4 hi4 = codes_f16(nan.z & 0x38383838u, nan.w & 0x38383838u, 1.f);
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) {
+          const uint32_t see = live_bits(hi[nb] - tok0) & ~live_bits(lo[nb] - tok0);
+          f32x4 n = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int s = 0; s < 2; ++s) {
+            uint32_t o[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const uint32_t m = see >> (8 * s + 2 * e);
+              o[e] = (m & 1 ? 0x3c00u : 0u) | (m & 2 ? 0x3c000000u : 0u);
+            }
+            n = mfma16_f16(s ? hi4 : lo4, make_uint4(o[0], o[1], o[2], o[3]), n);
+          }
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (n[e] > 0.f) acc[nb][dt][e] = __uint_as_float(0x7fc00000u);
+        }
+      }
+      add(dt, x, vs, pf);
+    }
+  }
+
+  __device__ __forceinline__ void finish() {
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) {
+      l[nb] = groups_sum(l[nb]);
+      if (!mixed) Ml[nb] = M[nb];
+    }
   }
 };
 
-// Joins the partials of slots slot0, slot0 + step, ... (count of them, at
-// most kMaxGroup), all columns below ncols: into slot0 again, or, `last`,
-// into the output.  Called by the whole workgroup; every partial is complete.
-template <int D, int CB, bool F32>
-__device__ __forceinline__ void join(const AttendArgs &a, const Work &w, int h, int slot0, int step, int count, int ncols,
-                                     bool last, float *lds) {
-  float *lm = lds, *ll = lds + kMaxGroup * CB;
-  __syncthreads();
-  for (int i = threadIdx.x; i < count * ncols; i += 256) {
-    const int k = i / ncols, col = i - k * ncols;
-    const Slot<D, CB> s(a, slot0 + k * step);
-    lm[k * CB + col] = __hip_atomic_load(s.p + CB * D + col, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    ll[k * CB + col] = __hip_atomic_load(s.p + CB * D + CB + col, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+// Pages of 16 tiles, lane 4 i + k for 16-token group k of tile i (`step`
+// tiles after the one before): the group's index among all groups of the
+// pool, and the page's exponent bytes, with bit 16 where there is a page.
+struct PageInfo {
+  int group, ex;
+  // The lane's page of the tiles from `tile` to `end`, or -1; then what is known of it.
+  static __device__ __forceinline__ int page(const KvDev &kv, int seq, int tile, int step, int end, int lane) {
+    const int t = tile + (lane >> 2) * step, tok = t * kTile + 16 * (lane & 3);
+    return t < end && tok < kv_cap(kv) ? page_of(kv, seq, tok >> kv.page_shift) : -1;
   }
-  __syncthreads();
-  for (int i = threadIdx.x; i < ncols * (D / 4); i += 256) {
-    const int col = i / (D / 4), d = (i % (D / 4)) * 4;
-    float M = -INFINITY, l = 0.f;
-    for (int k = 0; k < count; ++k) M = fmaxf(M, lm[k * CB + col]);
-    const float base = M == -INFINITY ? 0.f : M;
-    f32x4 sum = {0.f, 0.f, 0.f, 0.f};
-    for (int k0 = 0; k0 < count; k0 += 8) {
-      f32x4 v[8];
-#pragma unroll
-      for (int k = 0; k < 8; ++k)  // past the end: the last again, with no weight
-        v[k] = ld16_coherent(Slot<D, CB>(a, slot0 + min(k0 + k, count - 1) * step).sums(), (uint32_t)(col * D + d) * 4, 0);
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        if (k0 + k >= count) break;
-        const float f = __builtin_amdgcn_exp2f(lm[(k0 + k) * CB + col] - base);
-        l += f * ll[(k0 + k) * CB + col];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) sum[e] += f * v[k][e];
-      }
-    }
-    if (last) {
-      const int c = w.block * CB + col, row = w.s.row0 + c / a.G, head = h * a.G + c % a.G;
-      const float r = denominator(l);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) sum[e] *= r;
-      store_out<F32>(a, row, head, D, d, sum);
-      if (d == 0) store_lse(a, row, head, M, l);
-    } else {
-      // every thread reads and writes its own elements of slot0; M and l are in LDS
-      const Slot<D, CB> s(a, slot0);
-      st16_coherent(s.sums(), (uint32_t)(col * D + d) * 4, 0, sum);
-      if (d == 0) s.put_ml(col, M, l);
+  __device__ __forceinline__ void set(const KvDev &kv, int h, int page, int tile, int step, int lane) {
+    const int tok = (tile + (lane >> 2) * step) * kTile + 16 * (lane & 3);
+    group = 0;
+    ex = 127 | 127 << 8;
+    if (page >= 0) {
+      const size_t ph = (size_t)page * kv.H + h;
+      ex = kv.ke[ph] | (kv.ve[ph] << 8) | 0x10000;
+      group = (int)((ph << (kv.page_shift - 4)) + ((tok & ((1 << kv.page_shift) - 1)) >> 4));
     }
   }
-}
-
-// One arrival at counter `c` of `of`: whether it is the last, which leaves
-// the counter at zero.  The workgroup's stores are complete before it counts.
-__device__ __forceinline__ bool arrive(unsigned *c, unsigned of, unsigned *lds) {
-  wait_vmcnt<0>();
-  asm volatile("" ::: "memory");
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    const unsigned got = __hip_atomic_fetch_add(c, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    if (got == of - 1) __hip_atomic_store(c, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    *lds = got;
+  __device__ __forceinline__ void load(const KvDev &kv, int seq, int h, int tile, int step, int end, int lane) {
+    set(kv, h, page(kv, seq, tile, step, end, lane), tile, step, lane);
   }
-  __syncthreads();
-  const bool last = *lds == of - 1;
-  __syncthreads();
-  return last;
-}
+};
 
-// ---------------------------------------------------------------- kernel
+// ---------------------------------------------------------------- kernels
+// LDS of the wide form: stages of a tile, each its 4 groups of K and 4 of V.
+// Groups lie 64 bytes more than their 16 D apart, so that the keys of four
+// groups that a wave reads together fall into different banks.
+template <int D>
+struct Stage {
+  static constexpr int kPitch = 16 * D + 64, kBytes = 8 * kPitch, kCount = D > 128 ? 2 : 3;
+  static constexpr int kDma = 2 * (D / 64);  // instructions of a wave (its group's K and V) a stage
+};
+
 template <int D, int NB, bool F32, bool WIDE>
-__global__ __launch_bounds__(256) void attend_kernel(AttendArgs a) {
+__global__ __launch_bounds__(256, attend_per_cu(D, WIDE)) void attend_kernel(AttendArgs a) {
   constexpr int CW = 16 * NB;             // columns of a wave
   constexpr int CB = WIDE ? 4 * CW : CW;  // columns of a unit
-  constexpr int NI = D / 64, NS = D / 32, ND = D / 16, NT = F32 ? 3 : 1;
-  constexpr int kMergeBytes = WIDE ? 0 : 4 * ND * 64 * 16, kJoinBytes = kMaxGroup * CB * 8;
-  __shared__ __attribute__((aligned(16))) char smem[kMergeBytes > kJoinBytes ? kMergeBytes : kJoinBytes];
-  __shared__ float wave_ml[4][2][CW];
-  __shared__ unsigned arrived;
+  constexpr int ND = D / 16;
+  static_assert(WIDE || NB == 1, "the narrow form holds 16 columns");
+  __shared__ __attribute__((aligned(16))) char smem[WIDE ? Stage<D>::kBytes * Stage<D>::kCount : 4 * ND * 64 * 16];
+  __shared__ float wave_ml[WIDE ? 1 : 4][3][16];
 
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int h = blockIdx.x % a.kv.H;
+  const int H = a.kv.H, h = blockIdx.x % H;
   Work w;
-  if (!find_work<CB>(a, blockIdx.x / a.kv.H, lane, &w)) return;
+  int all_slots;
+  const bool found = find_work<CB>(a, blockIdx.x / H, lane, &w, &all_slots);
+  if (blockIdx.x == 0 && tid == 0) *a.used = all_slots * H;
+  if (!found) return;
   const int cap = kv_cap(a.kv), n_cols = min(CB, w.s.rows * a.G - w.block * CB);
   const int r = lane & 15, g = lane >> 4;
 
@@ -320,360 +520,282 @@ __global__ __launch_bounds__(256) void attend_kernel(AttendArgs a) {
   const int hi_u = max(min(w.s.start + j_last + 1, cap), 0);
   const int lo_u = a.window ? max(w.s.start + j_first + 1 - a.window, 0) : 0;
   const int tile0 = lo_u / kTile, tiles = hi_u > lo_u ? (hi_u + kTile - 1) / kTile - tile0 : 0;
-  int ta = tile0 + (int)((long long)tiles * w.chunk / w.nc);
-  int tb = tile0 + (int)((long long)tiles * (w.chunk + 1) / w.nc);
+  const int ta = tile0 + (int)((long long)tiles * w.chunk / w.nc);
+  const int tb = tile0 + (int)((long long)tiles * (w.chunk + 1) / w.nc);
 
-  // this wave's columns, and the tokens that all of them see
+  // this wave's columns, the tokens that all of them see and those that any does
   const int c0 = w.block * CB + (WIDE ? wave * CW : 0);
   const int c1 = min(c0 + CW, w.s.rows * a.G);
-  int j0 = j_first, j1 = j_last;
-  if constexpr (WIDE) {
-    j0 = c0 / a.G;
-    j1 = (c1 - 1) / a.G;
-    if (c0 < c1) {
-      tb = min(tb, (max(min(w.s.start + j1 + 1, cap), 0) + kTile - 1) / kTile);
-      if (a.window) ta = max(ta, max(w.s.start + j0 + 1 - a.window, 0) / kTile);
-    } else {
-      tb = ta;
-    }
-  } else {
-    ta += wave;
-  }
-  constexpr int step = WIDE ? 1 : 4;
-  const int hi_all = w.s.start + j0 + 1, lo_all = a.window ? w.s.start + j1 + 1 - a.window : 0;
+  const int j0 = WIDE ? c0 / a.G : j_first, j1 = WIDE ? (c1 - 1) / a.G : j_last;
+  const int hi_all = min(w.s.start + j0 + 1, cap), lo_all = a.window ? w.s.start + j1 + 1 - a.window : 0;
+  Columns<D, NB, F32> cols;
+  PageInfo info;
 
-  int hi_c[NB], lo_c[NB];
-  uint4 q[NB][NS][NT];
-#pragma unroll
-  for (int nb = 0; nb < NB; ++nb) {
-    const int c = c0 + nb * 16 + r;
-    const bool ok = c < c1;
-    const int j = ok ? c / a.G : 0;
-    hi_c[nb] = ok ? w.s.start + j + 1 : 0;
-    lo_c[nb] = ok && a.window ? w.s.start + j + 1 - a.window : 0;
-    const size_t at = (size_t)(w.s.row0 + j) * a.q_stride + (h * a.G + (ok ? c - j * a.G : 0)) * D;
-#pragma unroll
-    for (int s = 0; s < NS; ++s) {
-      const int d = 16 * (4 * (s >> 1) + g) + 8 * (s & 1);
-      if constexpr (F32) {
-        float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-        if (ok) {
-          const uint4 u = ldg16((const float *)a.q + at + d), v = ldg16((const float *)a.q + at + d + 4);
-          x[0] = __uint_as_float(u.x); x[1] = __uint_as_float(u.y); x[2] = __uint_as_float(u.z); x[3] = __uint_as_float(u.w);
-          x[4] = __uint_as_float(v.x); x[5] = __uint_as_float(v.y); x[6] = __uint_as_float(v.z); x[7] = __uint_as_float(v.w);
-        }
-        split3(x, q[nb][s]);
-      } else {
-        q[nb][s][0] = ok ? ldg16((const u16 *)a.q + at + d) : z4();
-      }
-    }
-  }
-
-  f32x4 acc[NB][ND];
-  float M[NB], l[NB];
-#pragma unroll
-  for (int nb = 0; nb < NB; ++nb) {
-    M[nb] = -INFINITY;
-    l[nb] = 0.f;
-#pragma unroll
-    for (int dt = 0; dt < ND; ++dt) acc[nb][dt] = f32x4{0.f, 0.f, 0.f, 0.f};
-  }
-
-  // Pages of the wave's next 16 tiles, lane 4 i + k for 16-token group k of
-  // tile i: the group's index among all groups of the pool, and the page's
-  // exponent bytes, with bit 16 where there is a page.
-  int gidx = 0, ex = 0;
-  auto load_info = [&](int tile) {
-    const int t = tile + (lane >> 2) * step, tok = t * kTile + 16 * (lane & 3);
-    gidx = 0;
-    ex = 127 | 127 << 8;
-    if (t < tb && tok < cap) {
-      const int page = page_of(a.kv, w.seq, tok >> a.kv.page_shift);
-      if (page >= 0) {
-        const size_t ph = (size_t)page * a.kv.H + h;
-        ex = max((int)a.kv.ke[ph], 1) | (a.kv.ve[ph] << 8) | 0x10000;
-        gidx = (int)((ph << (a.kv.page_shift - 4)) + ((tok & ((1 << a.kv.page_shift) - 1)) >> 4));
-      }
-    }
-  };
-  uint4 kr[4][NI], vr[ND];
-  auto load_k = [&](int i) {
-    const uint8_t *p = a.kv.k + (size_t)(unsigned)__shfl(gidx, 4 * i + (r >> 2), 64) * (16 * D) + g * 64 + (r & 3) * 16;
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-#pragma unroll
-      for (int n = 0; n < NI; ++n) kr[j][n] = ldg16(p + j * (4 * D) + n * 256);
-  };
-  auto load_v = [&](int i) {
-    const uint8_t *p = a.kv.v + (size_t)(unsigned)__shfl(gidx, 4 * i + g, 64) * (16 * D) + r * 16;
-#pragma unroll
-    for (int dt = 0; dt < ND; ++dt) vr[dt] = ldg16(p + dt * 256);
-  };
-
-  int bi = 0;  // the tile's place among the 16 whose pages are known
-  if (ta < tb) {
-    load_info(ta);
-    load_k(0);
-    load_v(0);
-  }
-  for (int t = ta; t < tb; t += step) {
-    const int my_ex = __shfl(ex, 4 * bi + g, 64);
-    // scores: lane (column r, g) gets tokens 16 g + 4 j + i of the tile
-    f32x4 S[NB][4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-#pragma unroll
-      for (int nb = 0; nb < NB; ++nb) S[nb][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int s = 0; s < NS; ++s) {
-        const uint4 &x = kr[j][s >> 1];
-        const uint4 kf = s & 1 ? codes_bf16(x.z, x.w) : codes_bf16(x.x, x.y);
-#pragma unroll
-        for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-          for (int n = 0; n < NT; ++n) S[nb][j] = mfma16(kf, q[nb][s][NT - 1 - n], S[nb][j]);
-      }
-    }
-    const bool more = t + step < tb;
-    if (more) {
-      if (++bi == 16) {
-        load_info(t + step);
-        bi = 0;
-      }
-      load_k(bi);
-    }
-
-    const int tok0 = t * kTile + 16 * g;
-    const bool masked = t * kTile < lo_all || (t + 1) * kTile > min(hi_all, cap) || __any(!(my_ex >> 16));
-    bool poison = false;  // a NaN value that some of the columns do not see
-    if (masked) {
-      const bool page = my_ex >> 16;
-#pragma unroll
-      for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int tok = tok0 + 4 * j + i;
-            if (!page || tok >= hi_c[nb] || tok < lo_c[nb]) S[nb][j][i] = -INFINITY;
-          }
-    }
-    const float ve = (float)(((my_ex >> 8) & 255) - 127);
-    const float cs = a.scale * __uint_as_float((uint32_t)(my_ex & 255) << 23);
-    const float inv = __uint_as_float((uint32_t)(254 - min((my_ex >> 8) & 255, 253)) << 23);
-    uint4 pf[NB][2][NT];
-    float alpha[NB];
-    bool grew = false;
-#pragma unroll
-    for (int nb = 0; nb < NB; ++nb) {
-      float mx = S[nb][0][0];
+  if constexpr (!WIDE) {
+    info.load(a.kv, w.seq, h, ta + wave, 4, tb, lane);
+    cols.load(a, w, h, c0, c1, r, g);
+    uint4 kr[4][D / 64], vr[ND];
+    auto load_k = [&](int i) {
+      const uint8_t *p = a.kv.k + (size_t)(unsigned)__shfl(info.group, 4 * i + (r >> 2), 64) * (16 * D) + g * 64 + (r & 3) * 16;
 #pragma unroll
       for (int j = 0; j < 4; ++j)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) mx = fmaxf(mx, S[nb][j][i]);
-      const float top = groups_max(fmaf(mx, cs, ve));
-      const float Mn = fmaxf(M[nb], top);
-      const float base = Mn == -INFINITY ? 0.f : Mn;
-      alpha[nb] = __builtin_amdgcn_exp2f(M[nb] - base);
-      grew |= Mn > M[nb];
-      M[nb] = Mn;
-      const float b = ve - base;
-      float sum = 0.f;
+        for (int n = 0; n < D / 64; ++n) kr[j][n] = ldg16(p + j * (4 * D) + n * 256);
+    };
+    auto load_v = [&](int i) {
+      const uint8_t *p = a.kv.v + (size_t)(unsigned)__shfl(info.group, 4 * i + g, 64) * (16 * D) + r * 16;
 #pragma unroll
-      for (int s = 0; s < 2; ++s) {
-        float p[8];
+      for (int dt = 0; dt < ND; ++dt) vr[dt] = ldg16(p + dt * 256);
+    };
+    int i = 0;  // the tile's place among the 16 whose pages are known
+    if (ta + wave < tb) {
+      load_k(0);
+      load_v(0);
+    }
+    for (int t = ta + wave; t < tb; t += 4) {
+      const int kinfo = __shfl(info.ex, 4 * i + (r >> 2), 64), vinfo = __shfl(info.ex, 4 * i + g, 64);
+      const bool more = t + 4 < tb;
+      cols.tile(
+          t * kTile, kinfo, vinfo, a.scale, lo_all, hi_all, lo_u, hi_u, g, [&](int j, int n) { return kr[j][n]; },
+          [&](int dt) { return vr[dt]; },
+          [&] {
+            if (!more) return;
+            if (++i == 16) {
+              info.load(a.kv, w.seq, h, t + 4, 4, tb, lane);
+              i = 0;
+            }
+            load_k(i);
+          });
+      if (more) load_v(i);
+    }
+  } else {
+    using St = Stage<D>;
+    constexpr int N = St::kCount;
+    const uint32_t base = lds_addr(smem);
+    // wave k brings group k of the tile
+    auto bring = [&](int groups, int i, int stage) {
+      const size_t at = (size_t)(unsigned)__builtin_amdgcn_readlane(groups, 4 * i + wave) * (16 * D) + lane * 16;
+      const uint32_t to = base + stage * St::kBytes + wave * St::kPitch;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          p[e] = __builtin_amdgcn_exp2f(fmaf(S[nb][2 * s + (e >> 2)][e & 3], cs, b));
-          sum += p[e];
-        }
-        if constexpr (F32) split3(p, pf[nb][s]);
-        else pf[nb][s][0] = make_uint4(pack_f16(p[0], p[1]), pack_f16(p[2], p[3]), pack_f16(p[4], p[5]), pack_f16(p[6], p[7]));
+      for (int n = 0; n < D / 64; ++n) dma16(a.kv.k + at + n * 1024, to + n * 1024);
+#pragma unroll
+      for (int n = 0; n < D / 64; ++n) dma16(a.kv.v + at + n * 1024, to + 4 * St::kPitch + n * 1024);
+    };
+    info.load(a.kv, w.seq, h, ta, 1, tb, lane);
+    cols.load(a, w, h, c0, c1, r, g);
+#pragma unroll
+    for (int k = 0; k < N - 1; ++k)
+      if (ta + k < tb) bring(info.group, k, k);
+    const int wave_lo = a.window ? max(w.s.start + j0 + 1 - a.window, 0) : 0;
+    const int wave_hi = c0 < c1 ? min(w.s.start + j1 + 1, cap) : 0;
+    PageInfo later = info;  // of the next 16 tiles
+    int later_page = -1, i = 0, stage = 0;
+    for (int t = ta; t < tb; ++t) {
+      // this wave's part of the tile is here, then everybody's; nobody reads the tile before any more
+      if (N == 3 && t + 1 < tb) wait_vmcnt<St::kDma>();
+      else wait_vmcnt<0>();
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+      block_barrier();
+      if (i == 16) {
+        info = later;
+        i = 0;
       }
-      l[nb] = l[nb] * alpha[nb] + sum * inv;
-    }
-    if (__any(grew)) {
-#pragma unroll
-      for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-        for (int dt = 0; dt < ND; ++dt)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) acc[nb][dt][e] *= alpha[nb];
-    }
-    if (masked) {
-      // tokens that no column sees may hold anything: their bytes become
-      // zeros, and so do NaN codes, which would reach the columns that do
-      // not see them too
-      const bool page = my_ex >> 16;
-      uint32_t keep[4], any_nan = 0;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) keep[i] = page ? live_bytes(tok0 + 4 * i, lo_u, hi_u) : 0u;
-#pragma unroll
-      for (int dt = 0; dt < ND; ++dt) {
-        vr[dt].x &= keep[0];
-        vr[dt].y &= keep[1];
-        vr[dt].z &= keep[2];
-        vr[dt].w &= keep[3];
-        any_nan |= nan_bytes(vr[dt].x) | nan_bytes(vr[dt].y) | nan_bytes(vr[dt].z) | nan_bytes(vr[dt].w);
+      // what waits for the page table does so here, where only the next tile is in flight
+      if (i == 4) later_page = PageInfo::page(a.kv, w.seq, t + 12, 1, tb, lane);
+      if (i == 8) later.set(a.kv, h, later_page, t + 8, 1, lane);
+      if (t + N - 1 < tb)
+        bring(i + N - 1 < 16 ? info.group : later.group, (i + N - 1) & 15, stage == 0 ? N - 1 : stage - 1);
+      if (t * kTile < wave_hi && (t + 1) * kTile > wave_lo) {
+        const char *kp = smem + stage * St::kBytes + (r >> 2) * St::kPitch + g * 64 + (r & 3) * 16;
+        const char *vp = smem + stage * St::kBytes + (4 + g) * St::kPitch + r * 16;
+        cols.tile(
+            t * kTile, __shfl(info.ex, 4 * i + (r >> 2), 64), __shfl(info.ex, 4 * i + g, 64), a.scale, lo_all, hi_all, lo_u, hi_u,
+            g, [&](int j, int n) { return *(const uint4 *)(kp + j * (4 * D) + n * 256); },
+            [&](int dt) { return *(const uint4 *)(vp + dt * 256); }, [] {});
       }
-      poison = __any(any_nan != 0);
+      ++i;
+      stage = stage == N - 1 ? 0 : stage + 1;
     }
-    if (poison) {
-      // columns that see a NaN value: count them by a product of ones
-      uint4 see[NB][2];
-#pragma unroll
-      for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-        for (int s = 0; s < 2; ++s) {
-          uint32_t o[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int t0 = tok0 + 8 * s + 2 * e;
-            o[e] = (t0 < hi_c[nb] && t0 >= lo_c[nb] ? 0x3c00u : 0u) |
-                   (t0 + 1 < hi_c[nb] && t0 + 1 >= lo_c[nb] ? 0x3c000000u : 0u);
-          }
-          see[nb][s] = make_uint4(o[0], o[1], o[2], o[3]);
-        }
-#pragma unroll
-      for (int dt = 0; dt < ND; ++dt) {
-        const uint4 x = vr[dt];
-        const uint4 nan = make_uint4(nan_bytes(x.x), nan_bytes(x.y), nan_bytes(x.z), nan_bytes(x.w));
-        vr[dt] = make_uint4(x.x & ~nan.x, x.y & ~nan.y, x.z & ~nan.z, x.w & ~nan.w);
-        // 0x38 is 1.0 in e4m3
-        const uint4 lo = codes_f16(nan.x & 0x38383838u, nan.y & 0x38383838u);
-        const uint4 hi = codes_f16(nan.z & 0x38383838u, nan.w & 0x38383838u);
-#pragma unroll
-        for (int nb = 0; nb < NB; ++nb) {
-          f32x4 n = mfma16_f16(lo, see[nb][0], f32x4{0.f, 0.f, 0.f, 0.f});
-          n = mfma16_f16(hi, see[nb][1], n);
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if (n[e] > 0.f) acc[nb][dt][e] = __uint_as_float(0x7fc00000u);
-        }
-      }
-    }
-#pragma unroll
-    for (int dt = 0; dt < ND; ++dt) {
-#pragma unroll
-      for (int s = 0; s < 2; ++s) {
-        const uint32_t lo = s ? vr[dt].z : vr[dt].x, hi = s ? vr[dt].w : vr[dt].y;
-        if constexpr (F32) {
-          const uint4 vf = codes_bf16(lo, hi);
-#pragma unroll
-          for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-            for (int n = 0; n < 3; ++n) acc[nb][dt] = mfma16(vf, pf[nb][s][2 - n], acc[nb][dt]);
-        } else {
-          const uint4 vf = codes_f16(lo, hi);
-#pragma unroll
-          for (int nb = 0; nb < NB; ++nb) acc[nb][dt] = mfma16_f16(vf, pf[nb][s][0], acc[nb][dt]);
-        }
-      }
-    }
-    if (more) load_v(bi);
   }
-#pragma unroll
-  for (int nb = 0; nb < NB; ++nb) l[nb] = groups_sum(l[nb]);
+  cols.finish();
 
   const bool split = w.nc > 1;
-  const Slot<D, CB> slot(a, split ? (w.slot + w.chunk) * a.kv.H + h : 0);
+  const int slot = split ? (w.slot + w.chunk) * H + h : 0;
+  float *part = a.part + (size_t)slot * CB * (D + 3), *ml = part + CB * D;
+  if (split && tid == 0) {
+    const AttendRecord rec = {w.slot * H + h, H, w.nc, w.chunk, n_cols, w.s.row0, w.block * CB, h};
+    a.records[slot] = rec;
+  }
+  // four dims of a column of the unit, from its sums or divided by them
+  auto put = [&](int col, int d, f32x4 v, float M, float Ml, float l) {
+    if (split) {
+      *(float4 *)(part + col * D + d) = make_float4(v[0], v[1], v[2], v[3]);
+    } else {
+      const int c = w.block * CB + col, row = w.s.row0 + c / a.G, head = h * a.G + c % a.G;
+      const float f = final_scale<F32>(M, Ml, l);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] *= f;
+      store_out<F32>(a.out, (size_t)row * a.out_stride + head * D + d, v);
+    }
+  };
+  auto put_ml = [&](int col, float M, float Ml, float l) {
+    if (split) {
+      ml[col] = M;
+      ml[CB + col] = Ml;
+      ml[2 * CB + col] = l;
+    } else if (a.lse) {
+      const int c = w.block * CB + col, row = w.s.row0 + c / a.G, head = h * a.G + c % a.G;
+      a.lse[(size_t)row * a.heads + head] = lse_of(Ml, l);
+    }
+  };
   if constexpr (WIDE) {
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) {
       const int c = c0 + nb * 16 + r, col = c - w.block * CB;
       if (c >= c1) continue;
-      const int row = w.s.row0 + c / a.G, head = h * a.G + c % a.G;
-      const float rl = denominator(l[nb]);
 #pragma unroll
-      for (int dt = 0; dt < ND; ++dt) {
-        f32x4 v = acc[nb][dt];
-        if (split) {
-          st16_coherent(slot.sums(), (uint32_t)(col * D + 16 * dt + 4 * g) * 4, 0, v);
-        } else {
-#pragma unroll
-          for (int e = 0; e < 4; ++e) v[e] *= rl;
-          store_out<F32>(a, row, head, D, 16 * dt + 4 * g, v);
-        }
-      }
-      if (g == 0) {
-        if (split) slot.put_ml(col, M[nb], l[nb]);
-        else store_lse(a, row, head, M[nb], l[nb]);
-      }
+      for (int dt = 0; dt < ND; ++dt) put(col, 16 * dt + 4 * g, cols.acc[nb][dt], cols.M[nb], cols.Ml[nb], cols.l[nb]);
+      if (g == 0) put_ml(col, cols.M[nb], cols.Ml[nb], cols.l[nb]);
     }
   } else {
     // the four waves' sums, each scaled to the common maximum, through LDS
     if (g == 0) {
-#pragma unroll
-      for (int nb = 0; nb < NB; ++nb) {
-        wave_ml[wave][0][nb * 16 + r] = M[nb];
-        wave_ml[wave][1][nb * 16 + r] = l[nb];
-      }
+      wave_ml[wave][0][r] = cols.M[0];
+      wave_ml[wave][1][r] = cols.Ml[0];
+      wave_ml[wave][2][r] = cols.l[0];
     }
     __syncthreads();
+    float M = kNone, Ml = kNone, l = 0.f;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      M = fmaxf(M, wave_ml[k][0][r]);
+      Ml = fmaxf(Ml, wave_ml[k][1][r]);
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) l += wave_ml[k][2][r] * __builtin_amdgcn_exp2f(wave_ml[k][1][r] - Ml);
+    const float f = __builtin_amdgcn_exp2f(cols.M[0] - M);
     f32x4 *box = (f32x4 *)smem;  // [wave][dt][lane]
 #pragma unroll
-    for (int nb = 0; nb < NB; ++nb) {
-      float Mx = -INFINITY;
+    for (int dt = 0; dt < ND; ++dt) {
+      f32x4 v = cols.acc[0][dt];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) Mx = fmaxf(Mx, wave_ml[k][0][nb * 16 + r]);
-      const float base = Mx == -INFINITY ? 0.f : Mx;
-      float lx = 0.f;
-#pragma unroll
-      for (int k = 0; k < 4; ++k) lx += wave_ml[k][1][nb * 16 + r] * __builtin_amdgcn_exp2f(wave_ml[k][0][nb * 16 + r] - base);
-      const float f = __builtin_amdgcn_exp2f(M[nb] - base);
-#pragma unroll
-      for (int dt = 0; dt < ND; ++dt) {
-        f32x4 v = acc[nb][dt];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] *= f;
-        box[(wave * ND + dt) * 64 + lane] = v;
-      }
-      __syncthreads();
-      const int c = c0 + nb * 16 + r, col = c - w.block * CB;
-      if (c < c1) {
-        const int row = w.s.row0 + c / a.G, head = h * a.G + c % a.G;
-        const float rl = denominator(lx);
-#pragma unroll
-        for (int k = 0; k < ND / 4; ++k) {
-          const int dt = wave * (ND / 4) + k;
-          f32x4 v = box[dt * 64 + lane];
-#pragma unroll
-          for (int o = 1; o < 4; ++o) {
-            const f32x4 u = box[(o * ND + dt) * 64 + lane];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) v[e] += u[e];
-          }
-          if (split) {
-            st16_coherent(slot.sums(), (uint32_t)(col * D + 16 * dt + 4 * g) * 4, 0, v);
-          } else {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) v[e] *= rl;
-            store_out<F32>(a, row, head, D, 16 * dt + 4 * g, v);
-          }
-        }
-        if (wave == 0 && g == 0) {
-          if (split) slot.put_ml(col, Mx, lx);
-          else store_lse(a, row, head, Mx, lx);
-        }
-      }
-      if (nb + 1 < NB) __syncthreads();
+      for (int e = 0; e < 4; ++e) v[e] *= f;
+      box[(wave * ND + dt) * 64 + lane] = v;
     }
+    __syncthreads();
+    const int col = r;
+    if (col >= n_cols) return;
+#pragma unroll
+    for (int k = 0; k < ND / 4; ++k) {
+      const int dt = wave * (ND / 4) + k;
+      f32x4 v = box[dt * 64 + lane];
+#pragma unroll
+      for (int o = 1; o < 4; ++o) {
+        const f32x4 u = box[(o * ND + dt) * 64 + lane];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] += u[e];
+      }
+      put(col, 16 * dt + 4 * g, v, M, Ml, l);
+    }
+    if (wave == 0 && g == 0) put_ml(col, M, Ml, l);
   }
-  if (!split) return;
-
-  // groups of gs chunks, then the unit's groups
-  int gs = 1;
-  while (gs * gs < w.nc) ++gs;
-  const int H = a.kv.H, groups = (w.nc + gs - 1) / gs, gi = w.chunk / gs;
-  const int in_group = min(gs, w.nc - gi * gs), slot_g = (w.slot + gi * gs) * H + h;
-  if (!arrive(a.cnt + slot_g, in_group, &arrived)) return;
-  join<D, CB, F32>(a, w, h, slot_g, H, in_group, n_cols, groups == 1, (float *)smem);
-  if (groups == 1) return;
-  if (!arrive(a.cnt + kAttendSlots + w.slot * H + h, groups, &arrived)) return;
-  join<D, CB, F32>(a, w, h, w.slot * H + h, gs * H, groups, n_cols, true, (float *)smem);
 }
 
-// ---------------------------------------------------------------- launcher
+// Joins the chunks of split units.  A unit of nc chunks has nc slots, and
+// the kParts workgroups of each take the columns k kParts + y, and every (nc
+// kParts)-th after it: the columns are spread like the chunks were.  A
+// column's dims go over D / 4 threads; the workgroup's groups of that many
+// share a column's chunks where those are many, and take a column each where
+// they are few.
+constexpr int kParts = 1;
+template <int D, bool F32>
+__global__ __launch_bounds__(256) void attend_join_kernel(AttendJoin a) {
+  constexpr int L = D / 4, kGroups = 256 / L;
+  __shared__ f32x4 sums[256];
+  __shared__ float ml[kGroups][3];
+  const AttendJoin::Form f = a.form[blockIdx.z];
+  if ((int)blockIdx.x >= *f.used) return;
+  const AttendRecord rec = f.records[blockIdx.x];
+  const int tid = threadIdx.x, group = tid / L, d = tid % L * 4;
+  const size_t floats = (size_t)f.cb * (D + 3);
+  int share = 1;  // groups to a column: eight chunks at a time each
+  while (share < kGroups && 8 * share < rec.nc) share *= 2;
+  const int abreast = kGroups / share, sub = group % share;
+  for (int c0 = rec.k * kParts + blockIdx.y; c0 < rec.n_cols; c0 += rec.nc * kParts * abreast) {
+    const int col = c0 + group / share * rec.nc * kParts;
+    const bool live = col < rec.n_cols;
+    float M = kNone, Ml = kNone, l = 0.f;
+    f32x4 sum = {0.f, 0.f, 0.f, 0.f};
+    for (int i0 = sub; live && i0 < rec.nc; i0 += 8 * share) {
+      f32x4 v[8];
+      float m[8], n[8], o[8];
+      float Mx = M, Mlx = Ml;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {  // past the end: the first again, with no weight
+        const int at = i0 + i * share;
+        const float *p = f.part + (size_t)(rec.slot0 + (at < rec.nc ? at : i0) * rec.step) * floats;
+        v[i] = *(const f32x4 *)(p + col * D + d);
+        p += f.cb * D + col;
+        m[i] = p[0];
+        n[i] = p[f.cb];
+        o[i] = p[2 * f.cb];
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        Mx = fmaxf(Mx, m[i]);
+        Mlx = fmaxf(Mlx, n[i]);
+      }
+      const float s = __builtin_amdgcn_exp2f(M - Mx);
+      l *= __builtin_amdgcn_exp2f(Ml - Mlx);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) sum[e] *= s;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        if (i0 + i * share >= rec.nc) continue;
+        const float t = __builtin_amdgcn_exp2f(m[i] - Mx);
+        l += o[i] * __builtin_amdgcn_exp2f(n[i] - Mlx);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sum[e] += t * v[i][e];
+      }
+      M = Mx;
+      Ml = Mlx;
+    }
+    if (share > 1) {
+      __syncthreads();
+      sums[tid] = sum;
+      if (tid % L == 0) {
+        ml[group][0] = M;
+        ml[group][1] = Ml;
+        ml[group][2] = l;
+      }
+      __syncthreads();
+      if (sub != 0 || !live) continue;
+      for (int i = 1; i < share; ++i) {
+        M = fmaxf(M, ml[group + i][0]);
+        Ml = fmaxf(Ml, ml[group + i][1]);
+      }
+      l = 0.f;
+      sum = f32x4{0.f, 0.f, 0.f, 0.f};
+      for (int i = 0; i < share; ++i) {
+        const float t = __builtin_amdgcn_exp2f(ml[group + i][0] - M);
+        l += ml[group + i][2] * __builtin_amdgcn_exp2f(ml[group + i][1] - Ml);
+        const f32x4 v = sums[tid + i * L];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sum[e] += t * v[e];
+      }
+    } else if (!live) {
+      continue;
+    }
+    const int c = rec.col0 + col, row = rec.row0 + c / a.G, head = rec.h * a.G + c % a.G;
+    const float t = final_scale<F32>(M, Ml, l);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) sum[e] *= t;
+    store_out<F32>(a.out, (size_t)row * a.out_stride + head * D + d, sum);
+    if (d == 0 && a.lse) a.lse[(size_t)row * a.heads + head] = lse_of(Ml, l);
+  }
+}
+
+// ---------------------------------------------------------------- launchers
 template <int D, int NB, bool F32, bool WIDE>
 static void go(const AttendArgs &a, hipStream_t st) {
   constexpr int CB = (WIDE ? 64 : 16) * NB;
@@ -681,23 +803,28 @@ static void go(const AttendArgs &a, hipStream_t st) {
   const long long blocks = s + ((long long)a.kv.n * a.G - s) / CB;  // sum of ceil(cols / CB) over s sequences at most
   hipLaunchKernelGGL((attend_kernel<D, NB, F32, WIDE>), dim3((unsigned)((a.per_head + blocks) * a.kv.H)), dim3(256), 0, st, a);
 }
-// Column blocks of a wave that its registers hold (accumulators 4 D / 16 and
-// the tile's codes D / 2 of them), at most.
 template <int D>
-static hipError_t go_dim(const AttendArgs &a, int dtype, int nb, bool wide, hipStream_t st) {
-  if (dtype == 0) go<D, 1, true, false>(a, st);
-  else if (wide) go<D, attend_wide_nb(D), false, true>(a, st);
-  else if (nb == 1 || D > 128) go<D, 1, false, false>(a, st);
-  else if constexpr (D <= 128) {
-    if (nb == 2) go<D, 2, false, false>(a, st);
-    else go<D, 3, false, false>(a, st);
-  }
+static void go_dim(const AttendArgs &a, int dtype, int nb, bool wide, hipStream_t st) {
+  if (dtype == 0) wide ? go<D, 1, true, true>(a, st) : go<D, 1, true, false>(a, st);
+  else if (!wide) go<D, 1, false, false>(a, st);
+  else if (nb == 1 || D > 128) go<D, 1, false, true>(a, st);
+  else if constexpr (D <= 128) go<D, 2, false, true>(a, st);
+}
+hipError_t launch_attend(const AttendArgs &a, int dim, int dtype, int nb, bool wide, hipStream_t st) {
+  dim == 64 ? go_dim<64>(a, dtype, nb, wide, st)
+            : dim == 128 ? go_dim<128>(a, dtype, nb, wide, st) : go_dim<256>(a, dtype, nb, wide, st);
   return hipGetLastError();
 }
 
-hipError_t launch_attend(const AttendArgs &a, int dim, int dtype, int nb, bool wide, hipStream_t st) {
-  return dim == 64 ? go_dim<64>(a, dtype, nb, wide, st)
-         : dim == 128 ? go_dim<128>(a, dtype, nb, wide, st) : go_dim<256>(a, dtype, nb, wide, st);
+template <int D>
+static void join_dim(const AttendJoin &a, int dtype, int forms, hipStream_t st) {
+  const dim3 grid(kAttendSlots, kParts, forms);
+  if (dtype == 0) hipLaunchKernelGGL((attend_join_kernel<D, true>), grid, dim3(256), 0, st, a);
+  else hipLaunchKernelGGL((attend_join_kernel<D, false>), grid, dim3(256), 0, st, a);
+}
+hipError_t launch_attend_join(const AttendJoin &a, int dim, int dtype, int forms, hipStream_t st) {
+  dim == 64 ? join_dim<64>(a, dtype, forms, st) : dim == 128 ? join_dim<128>(a, dtype, forms, st) : join_dim<256>(a, dtype, forms, st);
+  return hipGetLastError();
 }
 
 }  // namespace lora

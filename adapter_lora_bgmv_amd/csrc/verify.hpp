@@ -69,6 +69,12 @@ hipError_t launch_kv_read(const KvDev &kv, int dim, int dtype, void *k, int k_st
                           hipStream_t st);
 
 // The attention over the cache (k_attend.hip).
+// A chunk of a split unit leaves [CB][D] sums, then M, Ml and l per column,
+// and this record, by which the join knows the unit.
+struct AttendRecord {
+  int slot0, step, nc, k;     // the unit's slots are slot0 + i step, this is the k-th of nc
+  int n_cols, row0, col0, h;  // its columns, the sequence's first row, the unit's first column, the head
+};
 struct AttendArgs {
   KvDev kv;
   const void *q;  // [n][q_stride], head h at h D
@@ -81,20 +87,39 @@ struct AttendArgs {
   int window;     // 0: none
   int cols_lo, cols_hi;  // takes the sequences whose rows x G lie in (cols_lo, cols_hi]
   int per_head;   // workgroups per key/value head that the tiles are spread over
-  float *part;    // partial results of split units, kAttendSlots slots
-  unsigned *cnt;  // [2][kAttendSlots] arrivals of a group of chunks and of a unit's groups, zero between calls
+  int min_tiles;  // of a chunk: fewer are not split
+  AttendRecord *records;  // [kAttendSlots] of split units' chunks
+  int *used;              // slots in use, written by the call
+  float *part;            // their partial results
 };
-// Workgroups that a launch's tiles are spread over, and the partial slots
-// that takes: a unit is split into nc > 1 chunks only where its tiles exceed
-// a chunk's, so the split units' chunks are fewer than twice as many.
-constexpr int kAttendTarget = 512;
-constexpr int kAttendSlots = 2 * kAttendTarget;
-// Columns (row, query head of the group) of a unit: 16 nb where the waves
-// share out the tiles, 64 nb where they share out the columns (wide).
-constexpr int attend_wide_nb(int dim) { return dim > 128 ? 1 : 2; }
-constexpr int attend_max_nb(int dim) { return dim > 128 ? 1 : 3; }
-constexpr int kAttendNarrowCols = 64;  // sequences of more columns take the wide form (bf16)
+// Workgroups of a CU that a form's registers allow, those that a launch's
+// tiles are spread over (one round of the card), and the partial slots that
+// takes: a unit is split into nc > 1 chunks only where its tiles exceed a
+// chunk's, so the split units' chunks are fewer than twice as many.
+constexpr int attend_per_cu(int dim, bool wide) { return !wide && dim > 128 ? 1 : 2; }
+constexpr int attend_target(int dim, bool wide) { return 256 * attend_per_cu(dim, wide); }
+constexpr int kAttendSlots = 2 * 512;
+// Tiles that are worth a chunk of their own.
+constexpr int kAttendMinTilesNarrow = 16, kAttendMinTilesWide = 4;
+constexpr int kAttendNarrowCols = 16;  // of a unit of the narrow form; sequences of more take the wide one
+// Columns (row, query head of the group) of a wide unit: 64 nb.
+constexpr int attend_wide_nb(int dim, int dtype) { return dtype == 0 || dim > 128 ? 1 : 2; }
 hipError_t launch_attend(const AttendArgs &a, int dim, int dtype, int nb, bool wide, hipStream_t st);
+
+// The join of split units, of one or both forms.
+struct AttendJoin {
+  struct Form {
+    const AttendRecord *records;
+    const int *used;
+    const float *part;
+    int cb;  // columns of a slot
+  } form[2];
+  void *out;
+  int out_stride;
+  float *lse;
+  int heads, G;
+};
+hipError_t launch_attend_join(const AttendJoin &a, int dim, int dtype, int forms, hipStream_t st);
 
 // Scores of given tokens over rows of logits (k_score.hip).
 constexpr int kScoreThreads = 256;

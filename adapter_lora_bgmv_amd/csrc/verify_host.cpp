@@ -98,15 +98,15 @@ int timed(const char *what, hipStream_t st, F launch) {
   return e;
 }
 
-// Which forms an attention call launches.  Short sequences (up to
-// kAttendNarrowCols columns) take the form whose waves share out the tiles,
-// longer ones, in bf16, the wide form.  max_rows bounds every sequence's
-// rows and with n also from below; where it leaves one form, that form takes
-// every sequence, so that a wrong bound costs time only.
+// Which forms an attention call launches.  Sequences of up to
+// kAttendNarrowCols columns take the narrow form, others the wide one.
+// max_rows bounds every sequence's rows and with n also from below; where it
+// leaves one form, that form takes every sequence, so that a wrong bound
+// costs time only.
 struct AttendPlan {
-  bool narrow, wide;
-  int nb;  // column blocks of the narrow form
-  size_t counters, total;
+  bool narrow, wide, split;  // split: a unit may be cut into chunks
+  int nb;                    // 64 nb columns of a wide unit
+  size_t records, wide_part, total;  // offsets in the workspace; the narrow form's partials lie last
 };
 AttendPlan attend_plan(const lora_kv_cache *c, const lora_kv_seqs *s, int32_t dtype, uint32_t n_heads, uint32_t n) {
   AttendPlan p{};
@@ -114,15 +114,16 @@ AttendPlan attend_plan(const lora_kv_cache *c, const lora_kv_seqs *s, int32_t dt
   const uint64_t most = s->max_rows ? std::min(s->max_rows, n) : n;
   const uint64_t others = (uint64_t)(s->n_seqs ? s->n_seqs - 1 : 0) * most;
   const uint64_t least = n > others ? n - others : 0;
-  p.wide = dtype == LORA_BF16 && most * G > (uint64_t)kAttendNarrowCols;
+  p.wide = most * G > (uint64_t)kAttendNarrowCols;
   p.narrow = !p.wide || least * G <= (uint64_t)kAttendNarrowCols;
-  // beside the wide form the short sequences are mostly single rows
-  const uint64_t cols = p.wide ? G : most * G;
-  p.nb = dtype == LORA_BF16 ? (int)std::min<uint64_t>((cols + 15) / 16, (uint64_t)attend_max_nb((int)c->head_dim)) : 1;
-  p.nb = std::max(p.nb, 1);
-  const size_t cb = std::max(p.narrow ? 16 * p.nb : 0, p.wide ? 64 * attend_wide_nb((int)c->head_dim) : 0);
-  p.counters = up256(2 * (size_t)kAttendSlots * 4);
-  p.total = p.counters + up256((size_t)kAttendSlots * cb * (c->head_dim + 2) * 4);
+  p.nb = most * G > 64 ? attend_wide_nb((int)c->head_dim, dtype) : 1;
+  // a table that holds no more tiles than a chunk's least splits nothing
+  const uint64_t tiles = ((uint64_t)s->max_pages * c->page_tokens + 63) / 64;
+  p.split = tiles > (uint64_t)(p.wide ? kAttendMinTilesWide : kAttendMinTilesNarrow);
+  p.records = 256;
+  p.wide_part = p.records + 2 * up256(kAttendSlots * sizeof(AttendRecord));
+  const size_t column = (size_t)kAttendSlots * (c->head_dim + 3) * 4;
+  p.total = p.wide_part + (p.wide ? up256(column * 64 * p.nb) : 0) + (p.narrow ? up256(column * 16) : 0);
   return p;
 }
 
@@ -206,22 +207,40 @@ int lora_kv_attend(const lora_kv_cache *cache, const lora_kv_seqs *seqs, int32_t
   a.G = (int)(n_heads / cache->n_kv_heads);
   a.scale = (float)((double)scale * 1.4426950408889634);
   a.window = (int)window;
-  a.per_head = std::max(1, kAttendTarget / a.kv.H);
-  a.cnt = (unsigned *)workspace;
-  a.part = (float *)((char *)workspace + p.counters);
+  AttendJoin j{};
+  j.out = out;
+  j.out_stride = a.out_stride;
+  j.lse = lse;
+  j.heads = a.heads;
+  j.G = a.G;
+  char *ws = (char *)workspace;
+  int forms = 0;
+  float *part = (float *)(ws + p.wide_part);
+  auto form = [&](bool wide, int cb, int min_tiles) {
+    a.used = (int *)ws + forms;
+    a.records = (AttendRecord *)(ws + p.records + forms * up256(kAttendSlots * sizeof(AttendRecord)));
+    a.part = part;
+    a.min_tiles = min_tiles;
+    a.per_head = std::max(1, attend_target((int)cache->head_dim, wide) / a.kv.H);
+    j.form[forms++] = {a.records, a.used, part, cb};
+    part += up256((size_t)kAttendSlots * cb * (cache->head_dim + 3) * 4) / 4;
+  };
   hipStream_t st = (hipStream_t)stream;
   return timed(what, st, [&] {
     hipError_t e = hipSuccess;
     if (p.wide) {  // the long rows first: the short ones fill in behind them
       a.cols_lo = p.narrow ? kAttendNarrowCols : 0;
       a.cols_hi = INT_MAX;
+      form(true, 64 * p.nb, kAttendMinTilesWide);
       e = launch_attend(a, (int)cache->head_dim, dtype, p.nb, true, st);
     }
     if (p.narrow && e == hipSuccess) {
       a.cols_lo = 0;
       a.cols_hi = p.wide ? kAttendNarrowCols : INT_MAX;
+      form(false, 16, kAttendMinTilesNarrow);
       e = launch_attend(a, (int)cache->head_dim, dtype, p.nb, false, st);
     }
+    if (p.split && e == hipSuccess) e = launch_attend_join(j, (int)cache->head_dim, dtype, forms, st);
     return e;
   });
 }
