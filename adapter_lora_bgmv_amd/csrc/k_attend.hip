@@ -112,10 +112,16 @@ __device__ __forceinline__ void split3(const float x[8], uint4 t[3]) {
   }
 }
 
-// Bytes that hold a NaN code, 0xff each.
-__device__ __forceinline__ uint32_t nan_bytes(uint32_t w) {
-  const uint32_t f = ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
-  return (f >> 7) * 0xffu;
+// Bit 7 of the bytes that hold a NaN code (and other bits that mean nothing);
+// those bytes, 0xff each.
+__device__ __forceinline__ uint32_t has_nan(uint32_t w) { return (w & 0x7f7f7f7fu) + 0x01010101u; }
+__device__ __forceinline__ uint32_t nan_bytes(uint32_t w) { return ((has_nan(w) & 0x80808080u) >> 7) * 0xffu; }
+
+// The lane's number, computed where it is asked for.
+__device__ __forceinline__ int lane_again() {
+  int l;
+  asm volatile("v_mbcnt_lo_u32_b32 %0, -1, 0\n\tv_mbcnt_hi_u32_b32 %0, -1, %0" : "=v"(l));
+  return l;
 }
 
 // The lowest n of 16 bits, 0 <= n <= 16 once clamped.
@@ -135,7 +141,7 @@ struct Work {
 
 template <int CB>
 __device__ __forceinline__ int seq_blocks(const AttendArgs &a, const SeqDev &s) {
-  const int cols = s.rows * a.G;
+  const int cols = s.rows * a.G.d;
   return cols > a.cols_lo && cols <= a.cols_hi ? (cols + CB - 1) / CB : 0;
 }
 // Tiles that a unit of the sequence sees at most; 1 where it sees none (its rows are written as zeros).
@@ -145,7 +151,7 @@ __device__ __forceinline__ int unit_tiles(const AttendArgs &a, const SeqDev &s, 
   if (hi <= lo) return 1;
   const int all = (hi + kTile - 1) / kTile - lo / kTile;
   // tokens under a window: its own and one more for every further row of the unit
-  return a.window ? min(all, (int)(((long long)a.window + CB / a.G + kTile) / kTile) + 1) : all;
+  return a.window ? min(all, (int)(((long long)a.window + CB + kTile) / kTile) + 1) : all;
 }
 
 // Item u of a head's list: units in order, each with its chunks.  Every wave
@@ -164,8 +170,11 @@ __device__ __forceinline__ bool find_work(const AttendArgs &a, int u, int lane, 
   }
 #pragma unroll
   for (int off = 32; off > 0; off >>= 1) total += __shfl_xor(total, off, 64);
-  const long long len = (total + a.per_head - 1) / a.per_head;
-  const int c = (int)min(max(len, (long long)a.min_tiles), 1ll << 30);  // tiles of a chunk at most
+  // tiles of a chunk at most (few tiles, the common case, need no 64-bit division)
+  int c = a.min_tiles;
+  if (total > (long long)c * a.per_head)
+    c = total < 1ll << 31 ? (int)(((unsigned)total + a.per_head - 1) / (unsigned)a.per_head)
+                          : (int)min((total + a.per_head - 1) / a.per_head, 1ll << 30);
   int items = 0, slots = 0;
   for (int i = i0; i < i1; ++i) {
     const SeqDev s = i == i0 ? first : load_seq(a.kv, i);
@@ -233,15 +242,55 @@ __device__ __forceinline__ float lse_of(float Ml, float l) {
   return l == 0.f ? -INFINITY : 0.6931471805599453f * (Ml - kTop + __builtin_amdgcn_logf(l));
 }
 
+// ---------------------------------------------------------------- pages
+// Pages of 16 tiles, lane 4 i + k for 16-token group k of tile i (`step`
+// tiles after the one before): the group's index among all groups of the
+// pool, and the page's exponent bytes (those of group 0 where there is no
+// page, which nothing is made of).
+struct PageInfo {
+  int group, ke, ve;
+  unsigned long long there;  // a bit a lane: it has a page
+  // The lane's page of the tiles from `tile` to `end`, or -1; then what is known of it.
+  static __device__ __forceinline__ int page(const KvDev &kv, int seq, int tile, int step, int end, int lane) {
+    const int t = tile + (lane >> 2) * step, tok = t * kTile + 16 * (lane & 3);
+    return t < end && tok < kv_cap(kv) ? page_of(kv, seq, tok >> kv.page_shift) : -1;
+  }
+  __device__ __forceinline__ void set(const KvDev &kv, int h, int page, int tile, int step, int lane) {
+    const int tok = (tile + (lane >> 2) * step) * kTile + 16 * (lane & 3);
+    const size_t ph = page >= 0 ? (size_t)page * kv.H + h : 0;
+    ke = kv.ke[ph];
+    ve = kv.ve[ph];
+    group = page >= 0 ? (int)((ph << (kv.page_shift - 4)) + ((tok & ((1 << kv.page_shift) - 1)) >> 4)) : 0;
+    there = __ballot(page >= 0);
+  }
+  __device__ __forceinline__ void load(const KvDev &kv, int seq, int h, int tile, int step, int end, int lane) {
+    set(kv, h, page(kv, seq, tile, step, end, lane), tile, step, lane);
+  }
+  // Whether tile i has all its pages and lies within the tokens that every column sees.
+  __device__ __forceinline__ bool whole(int i, int tile, int lo_all, int hi_all) const {
+    return (there >> (4 * i) & 15) == 15 && tile * kTile >= lo_all && (tile + 1) * kTile <= hi_all;
+  }
+  // Tile i's exponent bytes: of the keys' group that the lane loads (r / 4),
+  // of the values of group g, and whether group g has a page.
+  struct Tile {
+    int ke, ve;
+    bool page;
+  };
+  __device__ __forceinline__ Tile tile(int i, int r, int g) const {
+    return {__shfl(ke, 4 * i + (r >> 2), 64), __shfl(ve, 4 * i + g, 64), (bool)(there >> (4 * i + g) & 1)};
+  }
+};
+
 // ---------------------------------------------------------------- a wave's columns
 template <int D, int NB, bool F32>
 struct Columns {
+  static_assert(NB <= 2, "the masked form takes one or two blocks");
   static constexpr int NS = D / 32, ND = D / 16, NT = F32 ? 3 : 1;
   uint4 q[NB][NS][NT];
   f32x4 acc[NB][ND];
   // sums run against 2^(M - kTop), the denominators l against 2^(Ml - kTop); Ml is M unless `mixed`
   float M[NB], Ml[NB], l[NB];
-  int hi[NB], lo[NB];  // a column sees the tokens [lo, hi)
+  int hi[NB];  // a column sees the tokens [hi - window, hi), or [0, hi)
   bool mixed;
 
   // Columns [c0, c1) of the sequence.
@@ -251,10 +300,9 @@ struct Columns {
     for (int nb = 0; nb < NB; ++nb) {
       const int c = c0 + nb * 16 + r;
       const bool ok = c < c1;
-      const int j = ok ? c / a.G : 0;
+      const int j = ok ? a.G.div(c) : 0;
       hi[nb] = ok ? w.s.start + j + 1 : 0;
-      lo[nb] = ok && a.window ? w.s.start + j + 1 - a.window : 0;
-      const size_t at = (size_t)(w.s.row0 + j) * a.q_stride + (h * a.G + (ok ? c - j * a.G : 0)) * D;
+      const size_t at = (size_t)(w.s.row0 + j) * a.q_stride + (h * a.G.d + (ok ? c - j * a.G.d : 0)) * D;
 #pragma unroll
       for (int s = 0; s < NS; ++s) {
         const int d = 16 * (4 * (s >> 1) + g) + 8 * (s & 1);
@@ -277,90 +325,150 @@ struct Columns {
     }
   }
 
-  // The weights of one tile's scores S, as operands; the sums so far are
-  // rescaled where the maximum moves.  `rest` is what the lane's value
-  // exponent leaves over (0 unless MIXED).
-  template <bool MIXED>
-  __device__ __forceinline__ void weigh(const f32x4 (&S)[NB][4], float cs, float rest, uint4 (&pf)[NB][2][NT]) {
-    float top[NB], topl[NB];
-    bool far = false;
+  // The largest of the lane's scores of a column.
+  __device__ __forceinline__ static float largest(const f32x4 (&S)[4]) {
+    float mx = S[0][0];
 #pragma unroll
-    for (int nb = 0; nb < NB; ++nb) {
-      float mx = S[nb][0][0];
+    for (int j = 0; j < 4; ++j)
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) mx = fmaxf(mx, S[nb][j][i]);
-      topl[nb] = mx * cs;
-      top[nb] = MIXED ? topl[nb] + rest : topl[nb];
-      far |= top[nb] > M[nb] + kLag;
-      if (MIXED) far |= topl[nb] > Ml[nb] + kLag;
-    }
-    if (__any(far)) {
-#pragma unroll
-      for (int nb = 0; nb < NB; ++nb) {
-        const float Mn = fmaxf(M[nb], groups_max(top[nb])), f = __builtin_amdgcn_exp2f(M[nb] - Mn);
-        M[nb] = Mn;
-        if (MIXED) {
-          const float Mln = fmaxf(Ml[nb], groups_max(topl[nb]));
-          l[nb] *= __builtin_amdgcn_exp2f(Ml[nb] - Mln);
-          Ml[nb] = Mln;
-        } else {
-          l[nb] *= f;
-        }
-#pragma unroll
-        for (int dt = 0; dt < ND; ++dt)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) acc[nb][dt][e] *= f;
-      }
-    }
-#pragma unroll
-    for (int nb = 0; nb < NB; ++nb) {
-      const float b = kTop - M[nb] + (MIXED ? rest : 0.f), bl = kTop - Ml[nb];
-#pragma unroll
-      for (int s = 0; s < 2; ++s) {
-        float p[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float x = S[nb][2 * s + (e >> 2)][e & 3];
-          p[e] = __builtin_amdgcn_exp2f(fmaf(x, cs, b));
-          l[nb] += MIXED ? __builtin_amdgcn_exp2f(fmaf(x, cs, bl)) : p[e];
-        }
-        if constexpr (F32) split3(p, pf[nb][s]);
-        else pf[nb][s][0] = make_uint4(pack_f16(p[0], p[1]), pack_f16(p[2], p[3]), pack_f16(p[4], p[5]), pack_f16(p[6], p[7]));
-      }
-    }
+      for (int e = 0; e < 4; ++e) mx = fmaxf(mx, S[j][e]);
+    return mx;
   }
 
-  // sums += weights x sixteen dims' codes of the tile
-  __device__ __forceinline__ void add(int dt, const uint4 &x, float scale, const uint4 (&pf)[NB][2][NT]) {
+  // The weights p = 2^(S cs + b) of a column's scores as operands, and their sum.
+  __device__ __forceinline__ static float weigh(const f32x4 (&S)[4], float cs, float b, uint4 (&pf)[2][NT]) {
+    float sum = 0.f;
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      float p[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        p[e] = __builtin_amdgcn_exp2f(fmaf(S[2 * s + (e >> 2)][e & 3], cs, b));
+        sum += p[e];
+      }
+      if constexpr (F32) split3(p, pf[s]);
+      else pf[s][0] = make_uint4(pack_f16(p[0], p[1]), pack_f16(p[2], p[3]), pack_f16(p[4], p[5]), pack_f16(p[6], p[7]));
+    }
+    return sum;
+  }
+
+  // sums of those blocks += weights x sixteen dims' codes of the tile
+  template <int B0, int BN>
+  __device__ __forceinline__ void add(int dt, const uint4 &x, float scale, const uint4 (&pf)[BN][2][NT]) {
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
       const uint32_t lo = s ? x.z : x.x, hi = s ? x.w : x.y;
       if constexpr (F32) {
         const uint4 vf = codes_bf16(lo, hi, scale);
 #pragma unroll
-        for (int nb = 0; nb < NB; ++nb)
+        for (int i = 0; i < BN; ++i)
 #pragma unroll
-          for (int n = 0; n < 3; ++n) acc[nb][dt] = mfma16(vf, pf[nb][s][2 - n], acc[nb][dt]);
+          for (int n = 0; n < 3; ++n) acc[B0 + i][dt] = mfma16(vf, pf[i][s][2 - n], acc[B0 + i][dt]);
       } else {
         const uint4 vf = codes_f16(lo, hi, scale);
 #pragma unroll
-        for (int nb = 0; nb < NB; ++nb) acc[nb][dt] = mfma16_f16(vf, pf[nb][s][0], acc[nb][dt]);
+        for (int i = 0; i < BN; ++i) acc[B0 + i][dt] = mfma16_f16(vf, pf[i][s][0], acc[B0 + i][dt]);
       }
     }
   }
 
-  // One tile, from token tok.  kinfo is the record (PageInfo) of the group
-  // whose keys the lane loads (r / 4), vinfo of group g; kf(j, n) gives 16
-  // bytes of keys, vf(dt) 16 bytes of values; after_keys runs once the keys
-  // are used up.  [lo_all, hi_all) are the tokens that all columns see,
-  // [lo_any, hi_any) those that any column of the workgroup does.
+  // A tile's scores S of column block B0 where masks, rests (what the lane's
+  // value exponent leaves over) or the maximum matter.
+  template <int B0, typename V>
+  __device__ __forceinline__ void careful(f32x4 (&S)[NB][4], int tok0, bool page, bool apart, int window, float cs, float rest,
+                                          float vs, int lo_any, int hi_any, V vf) {
+    // of the lane's tokens, those that its column sees
+    const int first = window && hi[B0] > window ? hi[B0] - window : 0;
+    const uint32_t see = page ? live_bits(hi[B0] - tok0) & ~live_bits(first - tok0) : 0u;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t m = (uint32_t)((int32_t)(see << (31 - 4 * j - i)) >> 31);
+        S[B0][j][i] = __uint_as_float((__float_as_uint(S[B0][j][i]) & m) | (0xff800000u & ~m));
+      }
+    const float topl = largest(S[B0]) * cs, top = topl + rest;
+    if (__any(top > M[B0] + kLag || topl > Ml[B0] + kLag)) {
+      const float Mn = fmaxf(M[B0], groups_max(top)), Mln = fmaxf(Ml[B0], groups_max(topl));
+      const float f = __builtin_amdgcn_exp2f(M[B0] - Mn);
+      l[B0] *= __builtin_amdgcn_exp2f(Ml[B0] - Mln);
+      M[B0] = Mn;
+      Ml[B0] = Mln;
+#pragma unroll
+      for (int dt = 0; dt < ND; ++dt) acc[B0][dt] *= f;
+    }
+    uint4 pf[1][2][NT];
+    const float sum = weigh(S[B0], cs, kTop - M[B0] + rest, pf[0]);
+    if (mixed) {
+      const float bl = kTop - Ml[B0];
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) l[B0] += __builtin_amdgcn_exp2f(fmaf(S[B0][j][e], cs, bl));
+    } else {
+      l[B0] += sum;
+    }
+    // tokens that no column sees may hold anything: their bytes become zeros
+    uint32_t keep[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) keep[i] = page ? live_bytes(tok0 + 4 * i, lo_any, hi_any) : 0u;
+    auto kept = [&](int dt) {
+      const uint4 x = vf(dt);
+      return make_uint4(x.x & keep[0], x.y & keep[1], x.z & keep[2], x.w & keep[3]);
+    };
+    // and so must NaN codes that some of the columns do not see
+    bool nans = false;
+    if (apart) {
+      uint32_t any = 0;
+#pragma unroll
+      for (int dt = 0; dt < ND; ++dt) {
+        const uint4 x = kept(dt);
+        any |= has_nan(x.x) | has_nan(x.y) | has_nan(x.z) | has_nan(x.w);
+      }
+      nans = __any((any & 0x80808080u) != 0);
+    }
+    if (__builtin_expect(!nans, 1)) {
+#pragma unroll
+      for (int dt = 0; dt < ND; ++dt) add<B0, 1>(dt, kept(dt), vs, pf);
+      return;
+    }
+#pragma unroll
+    for (int dt = 0; dt < ND; ++dt) {
+      uint4 x = kept(dt);
+      const uint4 nan = make_uint4(nan_bytes(x.x), nan_bytes(x.y), nan_bytes(x.z), nan_bytes(x.w));
+      x = make_uint4(x.x & ~nan.x, x.y & ~nan.y, x.z & ~nan.z, x.w & ~nan.w);
+      // columns that see a NaN value: count them by a product of ones (0x38 is 1.0 in e4m3, 0x3c00 in f16)
+      f32x4 n = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        uint32_t o[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const uint32_t m = see >> (8 * s + 2 * e);
+          o[e] = (m & 1 ? 0x3c00u : 0u) | (m & 2 ? 0x3c000000u : 0u);
+        }
+        n = mfma16_f16(codes_f16((s ? nan.z : nan.x) & 0x38383838u, (s ? nan.w : nan.y) & 0x38383838u, 1.f),
+                       make_uint4(o[0], o[1], o[2], o[3]), n);
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (n[e] > 0.f) acc[B0][dt][e] = __uint_as_float(0x7fc00000u);
+      add<B0, 1>(dt, x, vs, pf);
+    }
+  }
+
+  // One tile, from token tok; kf(j, n) gives 16 bytes of keys, vf(dt) 16
+  // bytes of values; after_keys runs once the keys are used up.  `whole`: every column sees every token of the tile;
+  // `apart`: some columns may see tokens of it that others do not.
+  // [lo_any, hi_any) are the tokens that any column of the workgroup sees.
   template <typename K, typename V, typename F>
-  __device__ __forceinline__ void tile(int tok, int kinfo, int vinfo, float cs, int lo_all, int hi_all, int lo_any, int hi_any,
+  __device__ __forceinline__ void tile(int tok, PageInfo::Tile info, bool whole, bool apart, int window, float cs, int lo_any, int hi_any,
                                        int g, K kf, V vf, F after_keys) {
     using X = ValueExp<F32>;
-    const float ks = __uint_as_float((uint32_t)(kinfo & 255) << 23);
+    const float ks = __uint_as_float((uint32_t)info.ke << 23);
+    const int ve = info.ve, vc = min(max(ve, X::kLo), X::kHi);
+    const float vs = __uint_as_float((uint32_t)(vc + X::kAdd) << 23);
+    const bool rests = __any(ve != vc);
     // scores: lane (column r, g) gets tokens 16 g + 4 j + i of the tile
     f32x4 S[NB][4];
 #pragma unroll
@@ -382,74 +490,55 @@ struct Columns {
     }
     after_keys();
 
-    const int tok0 = tok + 16 * g;
-    const bool page = vinfo >> 16;
-    const bool masked = tok < lo_all || tok + kTile > hi_all || __any(!page);
-    if (masked) {
+    bool plain = whole && !rests && !mixed;
+    if (__builtin_expect(plain, 1)) {
+      float top[NB];
+      bool far = false, old = false;
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb) {
-        const uint32_t see = page ? live_bits(hi[nb] - tok0) & ~live_bits(lo[nb] - tok0) : 0u;
+        top[nb] = largest(S[nb]) * cs;
+        far |= top[nb] > M[nb] + kLag;
+        old |= top[nb] > M[nb] + kLag && M[nb] != kNone;
+      }
+      if (__builtin_expect(__any(far), 0)) {
+        plain = !__any(old);  // first maxima: nothing to rescale
+        if (plain)
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const uint32_t m = (uint32_t)((int32_t)(see << (31 - 4 * j - i)) >> 31);
-            S[nb][j][i] = __uint_as_float((__float_as_uint(S[nb][j][i]) & m) | (0xff800000u & ~m));
-          }
+          for (int nb = 0; nb < NB; ++nb) M[nb] = M[nb] == kNone ? fmaxf(kNone, groups_max(top[nb])) : M[nb];
       }
     }
-    const int ve = (vinfo >> 8) & 255, vc = min(max(ve, X::kLo), X::kHi);
-    const float vs = __uint_as_float((uint32_t)(vc + X::kAdd) << 23);
-    uint4 pf[NB][2][NT];
-    if (!mixed && __any(ve != vc)) {
-      mixed = true;
+    if (__builtin_expect(plain, 1)) {
+      uint4 pf[NB][2][NT];
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb) l[nb] += weigh(S[nb], cs, kTop - M[nb], pf[nb]);
+      uint4 next = vf(0);
+#pragma unroll
+      for (int dt = 0; dt < ND; ++dt) {
+        const uint4 now = next;
+        if (dt + 1 < ND) next = vf(dt + 1);
+        add<0, NB>(dt, now, vs, pf);
+      }
+      return;
+    }
+    // masks, rests and maxima that moved, one block after the other; with no rest so far M and Ml move together
+    if (!mixed) {
+      mixed = rests;
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb) Ml[nb] = M[nb];
     }
-    if (mixed) weigh<true>(S, cs, (float)(ve - vc), pf);
-    else weigh<false>(S, cs, 0.f, pf);
-    if (!masked) {
+    careful<0>(S, tok + 16 * g, info.page, apart, window, cs, (float)(ve - vc), vs, lo_any, hi_any, vf);
+    if constexpr (NB == 2) careful<1>(S, tok + 16 * g, info.page, apart, window, cs, (float)(ve - vc), vs, lo_any, hi_any, vf);
+  }
+
+  // Waits for q here rather than at its first use, which is in the loop.
+  __device__ __forceinline__ void arrive() {
 #pragma unroll
-      for (int dt = 0; dt < ND; ++dt) add(dt, vf(dt), vs, pf);
-      return;
-    }
-    // tokens that no column sees may hold anything: their bytes become
-    // zeros, and so do NaN codes, which would reach the columns that do
-    // not see them too
-    uint32_t keep[4];
+    for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) keep[i] = page ? live_bytes(tok0 + 4 * i, lo_any, hi_any) : 0u;
+      for (int s = 0; s < NS; ++s)
 #pragma unroll
-    for (int dt = 0; dt < ND; ++dt) {
-      uint4 x = vf(dt);
-      x = make_uint4(x.x & keep[0], x.y & keep[1], x.z & keep[2], x.w & keep[3]);
-      const uint4 nan = make_uint4(nan_bytes(x.x), nan_bytes(x.y), nan_bytes(x.z), nan_bytes(x.w));
-      if (__any((nan.x | nan.y | nan.z | nan.w) != 0)) {
-        x = make_uint4(x.x & ~nan.x, x.y & ~nan.y, x.z & ~nan.z, x.w & ~nan.w);
-        // columns that see a NaN value: count them by a product of ones (0x38 is 1.0 in e4m3, 0x3c00 in f16)
-        const uint4 lo4 = codes_f16(nan.x & 0x38383838u, nan.y & 0x38383838u, 1.f);
-        const uint4 hi4 = codes_f16(nan.z & 0x38383838u, nan.w & 0x38383838u, 1.f);
-#pragma unroll
-        for (int nb = 0; nb < NB; ++nb) {
-          const uint32_t see = live_bits(hi[nb] - tok0) & ~live_bits(lo[nb] - tok0);
-          f32x4 n = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-          for (int s = 0; s < 2; ++s) {
-            uint32_t o[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const uint32_t m = see >> (8 * s + 2 * e);
-              o[e] = (m & 1 ? 0x3c00u : 0u) | (m & 2 ? 0x3c000000u : 0u);
-            }
-            n = mfma16_f16(s ? hi4 : lo4, make_uint4(o[0], o[1], o[2], o[3]), n);
-          }
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if (n[e] > 0.f) acc[nb][dt][e] = __uint_as_float(0x7fc00000u);
-        }
-      }
-      add(dt, x, vs, pf);
-    }
+        for (int t = 0; t < NT; ++t)
+          asm volatile("" : "+v"(q[nb][s][t].x), "+v"(q[nb][s][t].y), "+v"(q[nb][s][t].z), "+v"(q[nb][s][t].w));
   }
 
   __device__ __forceinline__ void finish() {
@@ -458,31 +547,6 @@ struct Columns {
       l[nb] = groups_sum(l[nb]);
       if (!mixed) Ml[nb] = M[nb];
     }
-  }
-};
-
-// Pages of 16 tiles, lane 4 i + k for 16-token group k of tile i (`step`
-// tiles after the one before): the group's index among all groups of the
-// pool, and the page's exponent bytes, with bit 16 where there is a page.
-struct PageInfo {
-  int group, ex;
-  // The lane's page of the tiles from `tile` to `end`, or -1; then what is known of it.
-  static __device__ __forceinline__ int page(const KvDev &kv, int seq, int tile, int step, int end, int lane) {
-    const int t = tile + (lane >> 2) * step, tok = t * kTile + 16 * (lane & 3);
-    return t < end && tok < kv_cap(kv) ? page_of(kv, seq, tok >> kv.page_shift) : -1;
-  }
-  __device__ __forceinline__ void set(const KvDev &kv, int h, int page, int tile, int step, int lane) {
-    const int tok = (tile + (lane >> 2) * step) * kTile + 16 * (lane & 3);
-    group = 0;
-    ex = 127 | 127 << 8;
-    if (page >= 0) {
-      const size_t ph = (size_t)page * kv.H + h;
-      ex = kv.ke[ph] | (kv.ve[ph] << 8) | 0x10000;
-      group = (int)((ph << (kv.page_shift - 4)) + ((tok & ((1 << kv.page_shift) - 1)) >> 4));
-    }
-  }
-  __device__ __forceinline__ void load(const KvDev &kv, int seq, int h, int tile, int step, int end, int lane) {
-    set(kv, h, page(kv, seq, tile, step, end, lane), tile, step, lane);
   }
 };
 
@@ -497,7 +561,7 @@ struct Stage {
 };
 
 template <int D, int NB, bool F32, bool WIDE>
-__global__ __launch_bounds__(256, attend_per_cu(D, WIDE)) void attend_kernel(AttendArgs a) {
+__global__ __launch_bounds__(256, attend_per_cu(D, F32, WIDE)) void attend_kernel(AttendArgs a) {
   constexpr int CW = 16 * NB;             // columns of a wave
   constexpr int CB = WIDE ? 4 * CW : CW;  // columns of a unit
   constexpr int ND = D / 16;
@@ -506,34 +570,39 @@ __global__ __launch_bounds__(256, attend_per_cu(D, WIDE)) void attend_kernel(Att
   __shared__ float wave_ml[WIDE ? 1 : 4][3][16];
 
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int H = a.kv.H, h = blockIdx.x % H;
+  const int H = a.kv.H, item = a.H.div(blockIdx.x), h = blockIdx.x - item * H;
   Work w;
   int all_slots;
-  const bool found = find_work<CB>(a, blockIdx.x / H, lane, &w, &all_slots);
+  const bool found = find_work<CB>(a, item, lane, &w, &all_slots);
   if (blockIdx.x == 0 && tid == 0) *a.used = all_slots * H;
   if (!found) return;
-  const int cap = kv_cap(a.kv), n_cols = min(CB, w.s.rows * a.G - w.block * CB);
+  const int cap = kv_cap(a.kv), n_cols = min(CB, w.s.rows * a.G.d - w.block * CB);
   const int r = lane & 15, g = lane >> 4;
 
   // the tokens that the unit's columns see, [lo_u, hi_u), and this chunk's tiles of them
-  const int j_first = (w.block * CB) / a.G, j_last = (w.block * CB + n_cols - 1) / a.G;
+  const int j_first = a.G.div(w.block * CB), j_last = a.G.div(w.block * CB + n_cols - 1);
   const int hi_u = max(min(w.s.start + j_last + 1, cap), 0);
   const int lo_u = a.window ? max(w.s.start + j_first + 1 - a.window, 0) : 0;
   const int tile0 = lo_u / kTile, tiles = hi_u > lo_u ? (hi_u + kTile - 1) / kTile - tile0 : 0;
-  const int ta = tile0 + (int)((long long)tiles * w.chunk / w.nc);
-  const int tb = tile0 + (int)((long long)tiles * (w.chunk + 1) / w.nc);
+  int ta = tile0, tb = tile0 + tiles;
+  if (w.nc > 1) {  // the first tiles % nc chunks take one more
+    const int each = tiles / w.nc, more = tiles - each * w.nc;
+    ta += w.chunk * each + min(w.chunk, more);
+    tb = ta + each + (w.chunk < more);
+  }
 
   // this wave's columns, the tokens that all of them see and those that any does
   const int c0 = w.block * CB + (WIDE ? wave * CW : 0);
-  const int c1 = min(c0 + CW, w.s.rows * a.G);
-  const int j0 = WIDE ? c0 / a.G : j_first, j1 = WIDE ? (c1 - 1) / a.G : j_last;
+  const int c1 = min(c0 + CW, w.s.rows * a.G.d);
+  const int j0 = WIDE ? a.G.div(c0) : j_first, j1 = WIDE ? a.G.div(max(c1 - 1, 0)) : j_last;
   const int hi_all = min(w.s.start + j0 + 1, cap), lo_all = a.window ? w.s.start + j1 + 1 - a.window : 0;
+  auto apart = [&](int t) { return (t * kTile < lo_all || (t + 1) * kTile > hi_all) && j_first != j_last; };
   Columns<D, NB, F32> cols;
   PageInfo info;
 
   if constexpr (!WIDE) {
-    info.load(a.kv, w.seq, h, ta + wave, 4, tb, lane);
     cols.load(a, w, h, c0, c1, r, g);
+    info.load(a.kv, w.seq, h, ta + wave, 4, tb, lane);
     uint4 kr[4][D / 64], vr[ND];
     auto load_k = [&](int i) {
       const uint8_t *p = a.kv.k + (size_t)(unsigned)__shfl(info.group, 4 * i + (r >> 2), 64) * (16 * D) + g * 64 + (r & 3) * 16;
@@ -553,10 +622,11 @@ __global__ __launch_bounds__(256, attend_per_cu(D, WIDE)) void attend_kernel(Att
       load_v(0);
     }
     for (int t = ta + wave; t < tb; t += 4) {
-      const int kinfo = __shfl(info.ex, 4 * i + (r >> 2), 64), vinfo = __shfl(info.ex, 4 * i + g, 64);
+      const PageInfo::Tile pages = info.tile(i, r, g);
       const bool more = t + 4 < tb;
       cols.tile(
-          t * kTile, kinfo, vinfo, a.scale, lo_all, hi_all, lo_u, hi_u, g, [&](int j, int n) { return kr[j][n]; },
+          t * kTile, pages, info.whole(i, t, lo_all, hi_all), apart(t), a.window, a.scale, lo_u, hi_u, g,
+          [&](int j, int n) { return kr[j][n]; },
           [&](int dt) { return vr[dt]; },
           [&] {
             if (!more) return;
@@ -581,8 +651,9 @@ __global__ __launch_bounds__(256, attend_per_cu(D, WIDE)) void attend_kernel(Att
 #pragma unroll
       for (int n = 0; n < D / 64; ++n) dma16(a.kv.v + at + n * 1024, to + 4 * St::kPitch + n * 1024);
     };
-    info.load(a.kv, w.seq, h, ta, 1, tb, lane);
     cols.load(a, w, h, c0, c1, r, g);
+    info.load(a.kv, w.seq, h, ta, 1, tb, lane);
+    cols.arrive();
 #pragma unroll
     for (int k = 0; k < N - 1; ++k)
       if (ta + k < tb) bring(info.group, k, k);
@@ -606,11 +677,13 @@ __global__ __launch_bounds__(256, attend_per_cu(D, WIDE)) void attend_kernel(Att
       if (t + N - 1 < tb)
         bring(i + N - 1 < 16 ? info.group : later.group, (i + N - 1) & 15, stage == 0 ? N - 1 : stage - 1);
       if (t * kTile < wave_hi && (t + 1) * kTile > wave_lo) {
+        // the lane's places anew: the registers that would hold them are wanted
+        const int again = lane_again(), r = again & 15, g = again >> 4;
         const char *kp = smem + stage * St::kBytes + (r >> 2) * St::kPitch + g * 64 + (r & 3) * 16;
         const char *vp = smem + stage * St::kBytes + (4 + g) * St::kPitch + r * 16;
         cols.tile(
-            t * kTile, __shfl(info.ex, 4 * i + (r >> 2), 64), __shfl(info.ex, 4 * i + g, 64), a.scale, lo_all, hi_all, lo_u, hi_u,
-            g, [&](int j, int n) { return *(const uint4 *)(kp + j * (4 * D) + n * 256); },
+            t * kTile, info.tile(i, r, g), info.whole(i, t, lo_all, hi_all), apart(t), a.window, a.scale, lo_u, hi_u, g,
+            [&](int j, int n) { return *(const uint4 *)(kp + j * (4 * D) + n * 256); },
             [&](int dt) { return *(const uint4 *)(vp + dt * 256); }, [] {});
       }
       ++i;
@@ -631,7 +704,7 @@ __global__ __launch_bounds__(256, attend_per_cu(D, WIDE)) void attend_kernel(Att
     if (split) {
       *(float4 *)(part + col * D + d) = make_float4(v[0], v[1], v[2], v[3]);
     } else {
-      const int c = w.block * CB + col, row = w.s.row0 + c / a.G, head = h * a.G + c % a.G;
+      const int c = w.block * CB + col, j = a.G.div(c), row = w.s.row0 + j, head = h * a.G.d + c - j * a.G.d;
       const float f = final_scale<F32>(M, Ml, l);
 #pragma unroll
       for (int e = 0; e < 4; ++e) v[e] *= f;
@@ -644,7 +717,7 @@ __global__ __launch_bounds__(256, attend_per_cu(D, WIDE)) void attend_kernel(Att
       ml[CB + col] = Ml;
       ml[2 * CB + col] = l;
     } else if (a.lse) {
-      const int c = w.block * CB + col, row = w.s.row0 + c / a.G, head = h * a.G + c % a.G;
+      const int c = w.block * CB + col, j = a.G.div(c), row = w.s.row0 + j, head = h * a.G.d + c - j * a.G.d;
       a.lse[(size_t)row * a.heads + head] = lse_of(Ml, l);
     }
   };
@@ -702,38 +775,38 @@ __global__ __launch_bounds__(256, attend_per_cu(D, WIDE)) void attend_kernel(Att
 }
 
 // Joins the chunks of split units.  A unit of nc chunks has nc slots, and
-// the kParts workgroups of each take the columns k kParts + y, and every (nc
-// kParts)-th after it: the columns are spread like the chunks were.  A
-// column's dims go over D / 4 threads; the workgroup's groups of that many
-// share a column's chunks where those are many, and take a column each where
-// they are few.
-constexpr int kParts = 1;
+// the k-th slot's workgroup takes the items k, k + nc, .. of the unit, an
+// item being 64 dims of a column: the items are spread like the chunks were.
+// The workgroup's 16 groups of 16 threads share an item's chunks where those
+// are many, and take an item each where they are few.
 template <int D, bool F32>
 __global__ __launch_bounds__(256) void attend_join_kernel(AttendJoin a) {
-  constexpr int L = D / 4, kGroups = 256 / L;
+  constexpr int kGroups = 16, kParts = D / 64;
   __shared__ f32x4 sums[256];
   __shared__ float ml[kGroups][3];
   const AttendJoin::Form f = a.form[blockIdx.z];
-  if ((int)blockIdx.x >= *f.used) return;
-  const AttendRecord rec = f.records[blockIdx.x];
-  const int tid = threadIdx.x, group = tid / L, d = tid % L * 4;
+  const int used = *f.used;
+  const AttendRecord rec = f.records[blockIdx.x];  // in one round trip with `used`
+  if ((int)blockIdx.x >= used) return;
+  const int tid = threadIdx.x, group = tid >> 4, lane = tid & 15;
   const size_t floats = (size_t)f.cb * (D + 3);
-  int share = 1;  // groups to a column: eight chunks at a time each
+  int share = 1;  // groups to an item: eight chunks at a time each
   while (share < kGroups && 8 * share < rec.nc) share *= 2;
-  const int abreast = kGroups / share, sub = group % share;
-  for (int c0 = rec.k * kParts + blockIdx.y; c0 < rec.n_cols; c0 += rec.nc * kParts * abreast) {
-    const int col = c0 + group / share * rec.nc * kParts;
-    const bool live = col < rec.n_cols;
+  const int abreast = kGroups / share, sub = group & (share - 1);
+  const int items = rec.n_cols * kParts;
+  for (int i0 = rec.k; i0 < items; i0 += rec.nc * abreast) {
+    const int item = i0 + group / share * rec.nc, col = item / kParts, d = item % kParts * 64 + lane * 4;
+    const bool live = item < items;
     float M = kNone, Ml = kNone, l = 0.f;
     f32x4 sum = {0.f, 0.f, 0.f, 0.f};
-    for (int i0 = sub; live && i0 < rec.nc; i0 += 8 * share) {
+    for (int i1 = sub; live && i1 < rec.nc; i1 += 8 * share) {
       f32x4 v[8];
       float m[8], n[8], o[8];
       float Mx = M, Mlx = Ml;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {  // past the end: the first again, with no weight
-        const int at = i0 + i * share;
-        const float *p = f.part + (size_t)(rec.slot0 + (at < rec.nc ? at : i0) * rec.step) * floats;
+        const int at = i1 + i * share;
+        const float *p = f.part + (size_t)(rec.slot0 + (at < rec.nc ? at : i1) * rec.step) * floats;
         v[i] = *(const f32x4 *)(p + col * D + d);
         p += f.cb * D + col;
         m[i] = p[0];
@@ -751,7 +824,7 @@ __global__ __launch_bounds__(256) void attend_join_kernel(AttendJoin a) {
       for (int e = 0; e < 4; ++e) sum[e] *= s;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        if (i0 + i * share >= rec.nc) continue;
+        if (i1 + i * share >= rec.nc) continue;
         const float t = __builtin_amdgcn_exp2f(m[i] - Mx);
         l += o[i] * __builtin_amdgcn_exp2f(n[i] - Mlx);
 #pragma unroll
@@ -763,7 +836,7 @@ __global__ __launch_bounds__(256) void attend_join_kernel(AttendJoin a) {
     if (share > 1) {
       __syncthreads();
       sums[tid] = sum;
-      if (tid % L == 0) {
+      if (lane == 0) {
         ml[group][0] = M;
         ml[group][1] = Ml;
         ml[group][2] = l;
@@ -779,14 +852,14 @@ __global__ __launch_bounds__(256) void attend_join_kernel(AttendJoin a) {
       for (int i = 0; i < share; ++i) {
         const float t = __builtin_amdgcn_exp2f(ml[group + i][0] - M);
         l += ml[group + i][2] * __builtin_amdgcn_exp2f(ml[group + i][1] - Ml);
-        const f32x4 v = sums[tid + i * L];
+        const f32x4 v = sums[tid + i * 16];
 #pragma unroll
         for (int e = 0; e < 4; ++e) sum[e] += t * v[e];
       }
     } else if (!live) {
       continue;
     }
-    const int c = rec.col0 + col, row = rec.row0 + c / a.G, head = rec.h * a.G + c % a.G;
+    const int c = rec.col0 + col, j = a.G.div(c), row = rec.row0 + j, head = rec.h * a.G.d + c - j * a.G.d;
     const float t = final_scale<F32>(M, Ml, l);
 #pragma unroll
     for (int e = 0; e < 4; ++e) sum[e] *= t;
@@ -800,7 +873,7 @@ template <int D, int NB, bool F32, bool WIDE>
 static void go(const AttendArgs &a, hipStream_t st) {
   constexpr int CB = (WIDE ? 64 : 16) * NB;
   const int s = a.kv.n < a.kv.n_seqs ? a.kv.n : a.kv.n_seqs;
-  const long long blocks = s + ((long long)a.kv.n * a.G - s) / CB;  // sum of ceil(cols / CB) over s sequences at most
+  const long long blocks = s + ((long long)a.kv.n * a.G.d - s) / CB;  // sum of ceil(cols / CB) over s sequences at most
   hipLaunchKernelGGL((attend_kernel<D, NB, F32, WIDE>), dim3((unsigned)((a.per_head + blocks) * a.kv.H)), dim3(256), 0, st, a);
 }
 template <int D>
@@ -818,7 +891,7 @@ hipError_t launch_attend(const AttendArgs &a, int dim, int dtype, int nb, bool w
 
 template <int D>
 static void join_dim(const AttendJoin &a, int dtype, int forms, hipStream_t st) {
-  const dim3 grid(kAttendSlots, kParts, forms);
+  const dim3 grid(kAttendSlots, 1, forms);
   if (dtype == 0) hipLaunchKernelGGL((attend_join_kernel<D, true>), grid, dim3(256), 0, st, a);
   else hipLaunchKernelGGL((attend_join_kernel<D, false>), grid, dim3(256), 0, st, a);
 }

@@ -68,6 +68,22 @@ hipError_t launch_kv_write(const KvDev &kv, int dim, int dtype, const void *k, i
 hipError_t launch_kv_read(const KvDev &kv, int dim, int dtype, void *k, int k_stride, void *v, int v_stride,
                           hipStream_t st);
 
+// n / d for 0 <= n < 2^31 and a d of the host's: with 2^(s-1) < d <= 2^s, m =
+// floor(2^(31+s) / d) + 1 exceeds 2^(31+s) / d by a part that stays below 1 / d
+// of a quotient, so that floor(n m / 2^(31+s)) is exact.
+struct FastDiv {
+  int d;
+  uint32_t m;
+  int s;
+  __device__ __forceinline__ int div(int n) const { return s ? (int)(__umulhi((uint32_t)n, m) >> (s - 1)) : n; }
+};
+inline FastDiv fast_div(int d) {
+  FastDiv f{d, 0, 0};
+  while ((1ll << f.s) < d) ++f.s;
+  f.m = (uint32_t)((1ull << (31 + f.s)) / (uint64_t)d + 1);
+  return f;
+}
+
 // The attention over the cache (k_attend.hip).
 // A chunk of a split unit leaves [CB][D] sums, then M, Ml and l per column,
 // and this record, by which the join knows the unit.
@@ -82,7 +98,8 @@ struct AttendArgs {
   void *out;      // [n][out_stride]
   int out_stride;
   float *lse;     // [n][heads] or null
-  int heads, G;   // query heads, and per key/value head
+  int heads;      // query heads
+  FastDiv G, H;   // query heads per key/value head, and those
   float scale;    // softmax scale times log2(e)
   int window;     // 0: none
   int cols_lo, cols_hi;  // takes the sequences whose rows x G lie in (cols_lo, cols_hi]
@@ -96,8 +113,8 @@ struct AttendArgs {
 // tiles are spread over (one round of the card), and the partial slots that
 // takes: a unit is split into nc > 1 chunks only where its tiles exceed a
 // chunk's, so the split units' chunks are fewer than twice as many.
-constexpr int attend_per_cu(int dim, bool wide) { return !wide && dim > 128 ? 1 : 2; }
-constexpr int attend_target(int dim, bool wide) { return 256 * attend_per_cu(dim, wide); }
+constexpr int attend_per_cu(int dim, bool f32, bool wide) { return dim > 128 && (f32 || !wide) ? 1 : 2; }
+constexpr int attend_target(int dim, int dtype, bool wide) { return 256 * attend_per_cu(dim, dtype == 0, wide); }
 constexpr int kAttendSlots = 2 * 512;
 // Tiles that are worth a chunk of their own.
 constexpr int kAttendMinTilesNarrow = 16, kAttendMinTilesWide = 4;
@@ -117,7 +134,8 @@ struct AttendJoin {
   void *out;
   int out_stride;
   float *lse;
-  int heads, G;
+  int heads;
+  FastDiv G;
 };
 hipError_t launch_attend_join(const AttendJoin &a, int dim, int dtype, int forms, hipStream_t st);
 

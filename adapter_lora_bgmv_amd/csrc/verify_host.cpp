@@ -204,7 +204,8 @@ int lora_kv_attend(const lora_kv_cache *cache, const lora_kv_seqs *seqs, int32_t
   a.out_stride = (int)out_row_stride;
   a.lse = lse;
   a.heads = (int)n_heads;
-  a.G = (int)(n_heads / cache->n_kv_heads);
+  a.G = fast_div((int)(n_heads / cache->n_kv_heads));
+  a.H = fast_div(a.kv.H);
   a.scale = (float)((double)scale * 1.4426950408889634);
   a.window = (int)window;
   AttendJoin j{};
@@ -221,7 +222,7 @@ int lora_kv_attend(const lora_kv_cache *cache, const lora_kv_seqs *seqs, int32_t
     a.records = (AttendRecord *)(ws + p.records + forms * up256(kAttendSlots * sizeof(AttendRecord)));
     a.part = part;
     a.min_tiles = min_tiles;
-    a.per_head = std::max(1, attend_target((int)cache->head_dim, wide) / a.kv.H);
+    a.per_head = std::max(1, attend_target((int)cache->head_dim, dtype, wide) / a.kv.H);
     j.form[forms++] = {a.records, a.used, part, cb};
     part += up256((size_t)kAttendSlots * cb * (cache->head_dim + 3) * 4) / 4;
   };
