@@ -26,9 +26,9 @@
 // the true one by 2^kLag: only a tile that exceeds it looks across lanes and
 // rescales the sums, which after a few tiles is rare.
 //
-// Rounding: bf16 calls take q as it is and round the weights, 2^10 at the
+// Rounding: bf16 calls take q as it is and round the weights, 2^8 at the
 // running maximum, to f16 (2^-12, an eighth of the output's own half step;
-// weights down to 2^-34 of the largest count); f32 calls split q and the
+// weights down to 2^-32 of the largest count); f32 calls split q and the
 // weights into three bf16 terms (24 bits) and take three products of each.
 // Scores, sums and outputs accumulate in f32.
 //
@@ -47,8 +47,8 @@
 namespace lora {
 
 constexpr int kTile = 64;    // tokens
-constexpr float kLag = 5.f;  // log2 of how far the running maximum may lag
-constexpr float kTop = 10.f; // log2 of the weight at the running maximum: with the lag 2^15, in f16's range
+constexpr float kLag = 7.f;  // log2 of how far the running maximum may lag
+constexpr float kTop = 8.f;  // log2 of the weight at the running maximum: with the lag 2^15, in f16's range
 constexpr float kNone = -3e38f;  // the maximum of a column that saw nothing yet
 
 // max / sum over the four lane groups l / 16 that hold a column's tokens.
@@ -64,6 +64,9 @@ __device__ __forceinline__ float groups_sum(float x) {
   auto s = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
   return __uint_as_float(s[0]) + __uint_as_float(s[1]);
 }
+
+// 2^(e - 127).
+__device__ __forceinline__ float scale_of(int e) { return __uint_as_float((uint32_t)e << 23); }
 
 // Eight codes (two dwords) times a power of two as a matrix operand.
 __device__ __forceinline__ uint4 codes_bf16(uint32_t lo, uint32_t hi, float scale) {
@@ -126,6 +129,12 @@ __device__ __forceinline__ int lane_again() {
 
 // The lowest n of 16 bits, 0 <= n <= 16 once clamped.
 __device__ __forceinline__ uint32_t live_bits(int n) { return (1u << min(max(n, 0), 16)) - 1u; }
+
+// Of the 16 tokens from tok0, those that a column sees whose last token is hi - 1.
+__device__ __forceinline__ uint32_t sees(int hi, int window, int tok0) {
+  const int first = window && hi > window ? hi - window : 0;
+  return live_bits(hi - tok0) & ~live_bits(first - tok0);
+}
 
 // Bytes of four tokens from t0 that lie in [lo, hi).
 __device__ __forceinline__ uint32_t live_bytes(int t0, int lo, int hi) {
@@ -372,22 +381,82 @@ struct Columns {
     }
   }
 
-  // A tile's scores S of column block B0 where masks, rests (what the lane's
-  // value exponent leaves over) or the maximum matter.
+  // Scores of the column blocks [B0, B0 + BN): lane (column r, g) gets tokens
+  // 16 g + 4 j + i of the tile; kf(j, n) gives 16 bytes of keys.
+  template <int B0, int BN, typename K>
+  __device__ __forceinline__ void score(f32x4 (&S)[BN][4], float scale, K kf) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+#pragma unroll
+      for (int i = 0; i < BN; ++i) S[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int n = 0; n < D / 64; ++n) {
+        const uint4 x = kf(j, n);
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+          const uint4 kk = s ? codes_bf16(x.z, x.w, scale) : codes_bf16(x.x, x.y, scale);
+#pragma unroll
+          for (int i = 0; i < BN; ++i)
+#pragma unroll
+            for (int t = 0; t < NT; ++t) S[i][j] = mfma16(kk, q[B0 + i][2 * n + s][NT - 1 - t], S[i][j]);
+        }
+      }
+    }
+  }
+
+  // The rest of a tile that every column sees all of, from its scores and
+  // values vf(dt); false, and nothing changed, where something unusual sends
+  // it through `careful`.
+  template <typename V>
+  __device__ __forceinline__ bool plain(const f32x4 (&S)[NB][4], PageInfo::Tile info, float cs, V vf) {
+    using X = ValueExp<F32>;
+    if (__builtin_expect(mixed || __any(info.ve < X::kLo || info.ve > X::kHi), 0)) return false;
+    float top[NB];
+    bool far = false, old = false;
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) {
+      top[nb] = largest(S[nb]) * cs;
+      far |= top[nb] > M[nb] + kLag;
+      old |= top[nb] > M[nb] + kLag && M[nb] != kNone;
+    }
+    if (__builtin_expect(__any(far), 0)) {
+      if (__any(old)) return false;
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb) M[nb] = M[nb] == kNone ? fmaxf(kNone, groups_max(top[nb])) : M[nb];  // the first: nothing to rescale
+    }
+    uint4 pf[NB][2][NT];
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) l[nb] += weigh(S[nb], cs, kTop - M[nb], pf[nb]);
+    const float vs = scale_of(info.ve + X::kAdd);
+    uint4 next = vf(0);
+#pragma unroll
+    for (int dt = 0; dt < ND; ++dt) {
+      const uint4 now = next;
+      if (dt + 1 < ND) next = vf(dt + 1);
+      add<0, NB>(dt, now, vs, pf);
+    }
+    return true;
+  }
+
+  // The rest of any tile, from token tok0 of the lane, for column block B0:
+  // masks, missing pages, value exponents out of the operand's range, maxima
+  // that moved, NaN codes.  [lo_any, hi_any) are the tokens that any column
+  // of the workgroup sees.
   template <int B0, typename V>
-  __device__ __forceinline__ void careful(f32x4 (&S)[NB][4], int tok0, bool page, bool apart, int window, float cs, float rest,
-                                          float vs, int lo_any, int hi_any, V vf) {
-    // of the lane's tokens, those that its column sees
-    const int first = window && hi[B0] > window ? hi[B0] - window : 0;
-    const uint32_t see = page ? live_bits(hi[B0] - tok0) & ~live_bits(first - tok0) : 0u;
+  __device__ __forceinline__ void careful(f32x4 (&S)[1][4], int tok0, PageInfo::Tile info, int window, float cs, int lo_any,
+                                          int hi_any, V vf) {
+    using X = ValueExp<F32>;
+    const int vc = min(max(info.ve, X::kLo), X::kHi);
+    const float rest = (float)(info.ve - vc), vs = scale_of(vc + X::kAdd);
+    const uint32_t see = info.page ? sees(hi[B0], window, tok0) : 0u;
 #pragma unroll
     for (int j = 0; j < 4; ++j)
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const uint32_t m = (uint32_t)((int32_t)(see << (31 - 4 * j - i)) >> 31);
-        S[B0][j][i] = __uint_as_float((__float_as_uint(S[B0][j][i]) & m) | (0xff800000u & ~m));
+        S[0][j][i] = __uint_as_float((__float_as_uint(S[0][j][i]) & m) | (0xff800000u & ~m));
       }
-    const float topl = largest(S[B0]) * cs, top = topl + rest;
+    const float topl = largest(S[0]) * cs, top = topl + rest;
     if (__any(top > M[B0] + kLag || topl > Ml[B0] + kLag)) {
       const float Mn = fmaxf(M[B0], groups_max(top)), Mln = fmaxf(Ml[B0], groups_max(topl));
       const float f = __builtin_amdgcn_exp2f(M[B0] - Mn);
@@ -398,43 +467,36 @@ struct Columns {
       for (int dt = 0; dt < ND; ++dt) acc[B0][dt] *= f;
     }
     uint4 pf[1][2][NT];
-    const float sum = weigh(S[B0], cs, kTop - M[B0] + rest, pf[0]);
+    const float sum = weigh(S[0], cs, kTop - M[B0] + rest, pf[0]);
     if (mixed) {
       const float bl = kTop - Ml[B0];
 #pragma unroll
       for (int j = 0; j < 4; ++j)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) l[B0] += __builtin_amdgcn_exp2f(fmaf(S[B0][j][e], cs, bl));
+        for (int e = 0; e < 4; ++e) l[B0] += __builtin_amdgcn_exp2f(fmaf(S[0][j][e], cs, bl));
     } else {
       l[B0] += sum;
     }
-    // tokens that no column sees may hold anything: their bytes become zeros
-    uint32_t keep[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) keep[i] = page ? live_bytes(tok0 + 4 * i, lo_any, hi_any) : 0u;
-    auto kept = [&](int dt) {
-      const uint4 x = vf(dt);
-      return make_uint4(x.x & keep[0], x.y & keep[1], x.z & keep[2], x.w & keep[3]);
-    };
-    // and so must NaN codes that some of the columns do not see
-    bool nans = false;
-    if (apart) {
-      uint32_t any = 0;
-#pragma unroll
-      for (int dt = 0; dt < ND; ++dt) {
-        const uint4 x = kept(dt);
-        any |= has_nan(x.x) | has_nan(x.y) | has_nan(x.z) | has_nan(x.w);
-      }
-      nans = __any((any & 0x80808080u) != 0);
-    }
-    if (__builtin_expect(!nans, 1)) {
-#pragma unroll
-      for (int dt = 0; dt < ND; ++dt) add<B0, 1>(dt, kept(dt), vs, pf);
-      return;
-    }
+    // a NaN code, even where nothing is seen, would reach every column
+    uint32_t any = 0;
 #pragma unroll
     for (int dt = 0; dt < ND; ++dt) {
-      uint4 x = kept(dt);
+      const uint4 x = vf(dt);
+      any |= has_nan(x.x) | has_nan(x.y) | has_nan(x.z) | has_nan(x.w);
+    }
+    asm volatile("" ::: "memory");  // read anew: held, the values would take the registers of the sums
+    if (__builtin_expect(!__any((any & 0x80808080u) != 0), 1)) {
+#pragma unroll
+      for (int dt = 0; dt < ND; ++dt) add<B0, 1>(dt, vf(dt), vs, pf);
+      return;
+    }
+    uint32_t keep[4];  // bytes of tokens that some column sees
+#pragma unroll
+    for (int i = 0; i < 4; ++i) keep[i] = info.page ? live_bytes(tok0 + 4 * i, lo_any, hi_any) : 0u;
+#pragma unroll
+    for (int dt = 0; dt < ND; ++dt) {
+      uint4 x = vf(dt);
+      x = make_uint4(x.x & keep[0], x.y & keep[1], x.z & keep[2], x.w & keep[3]);
       const uint4 nan = make_uint4(nan_bytes(x.x), nan_bytes(x.y), nan_bytes(x.z), nan_bytes(x.w));
       x = make_uint4(x.x & ~nan.x, x.y & ~nan.y, x.z & ~nan.z, x.w & ~nan.w);
       // columns that see a NaN value: count them by a product of ones (0x38 is 1.0 in e4m3, 0x3c00 in f16)
@@ -456,78 +518,12 @@ struct Columns {
       add<B0, 1>(dt, x, vs, pf);
     }
   }
-
-  // One tile, from token tok; kf(j, n) gives 16 bytes of keys, vf(dt) 16
-  // bytes of values; after_keys runs once the keys are used up.  `whole`: every column sees every token of the tile;
-  // `apart`: some columns may see tokens of it that others do not.
-  // [lo_any, hi_any) are the tokens that any column of the workgroup sees.
-  template <typename K, typename V, typename F>
-  __device__ __forceinline__ void tile(int tok, PageInfo::Tile info, bool whole, bool apart, int window, float cs, int lo_any, int hi_any,
-                                       int g, K kf, V vf, F after_keys) {
-    using X = ValueExp<F32>;
-    const float ks = __uint_as_float((uint32_t)info.ke << 23);
-    const int ve = info.ve, vc = min(max(ve, X::kLo), X::kHi);
-    const float vs = __uint_as_float((uint32_t)(vc + X::kAdd) << 23);
-    const bool rests = __any(ve != vc);
-    // scores: lane (column r, g) gets tokens 16 g + 4 j + i of the tile
-    f32x4 S[NB][4];
+  // Before a careful tile: with no rest so far M and Ml move together.
+  __device__ __forceinline__ void meet(PageInfo::Tile info) {
+    if (mixed) return;
+    mixed = __any(info.ve < ValueExp<F32>::kLo || info.ve > ValueExp<F32>::kHi);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-#pragma unroll
-      for (int nb = 0; nb < NB; ++nb) S[nb][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int n = 0; n < D / 64; ++n) {
-        const uint4 x = kf(j, n);
-#pragma unroll
-        for (int s = 0; s < 2; ++s) {
-          const uint4 kk = s ? codes_bf16(x.z, x.w, ks) : codes_bf16(x.x, x.y, ks);
-#pragma unroll
-          for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-            for (int t = 0; t < NT; ++t) S[nb][j] = mfma16(kk, q[nb][2 * n + s][NT - 1 - t], S[nb][j]);
-        }
-      }
-    }
-    after_keys();
-
-    bool plain = whole && !rests && !mixed;
-    if (__builtin_expect(plain, 1)) {
-      float top[NB];
-      bool far = false, old = false;
-#pragma unroll
-      for (int nb = 0; nb < NB; ++nb) {
-        top[nb] = largest(S[nb]) * cs;
-        far |= top[nb] > M[nb] + kLag;
-        old |= top[nb] > M[nb] + kLag && M[nb] != kNone;
-      }
-      if (__builtin_expect(__any(far), 0)) {
-        plain = !__any(old);  // first maxima: nothing to rescale
-        if (plain)
-#pragma unroll
-          for (int nb = 0; nb < NB; ++nb) M[nb] = M[nb] == kNone ? fmaxf(kNone, groups_max(top[nb])) : M[nb];
-      }
-    }
-    if (__builtin_expect(plain, 1)) {
-      uint4 pf[NB][2][NT];
-#pragma unroll
-      for (int nb = 0; nb < NB; ++nb) l[nb] += weigh(S[nb], cs, kTop - M[nb], pf[nb]);
-      uint4 next = vf(0);
-#pragma unroll
-      for (int dt = 0; dt < ND; ++dt) {
-        const uint4 now = next;
-        if (dt + 1 < ND) next = vf(dt + 1);
-        add<0, NB>(dt, now, vs, pf);
-      }
-      return;
-    }
-    // masks, rests and maxima that moved, one block after the other; with no rest so far M and Ml move together
-    if (!mixed) {
-      mixed = rests;
-#pragma unroll
-      for (int nb = 0; nb < NB; ++nb) Ml[nb] = M[nb];
-    }
-    careful<0>(S, tok + 16 * g, info.page, apart, window, cs, (float)(ve - vc), vs, lo_any, hi_any, vf);
-    if constexpr (NB == 2) careful<1>(S, tok + 16 * g, info.page, apart, window, cs, (float)(ve - vc), vs, lo_any, hi_any, vf);
+    for (int nb = 0; nb < NB; ++nb) Ml[nb] = M[nb];
   }
 
   // Waits for q here rather than at its first use, which is in the loop.
@@ -596,7 +592,6 @@ __global__ __launch_bounds__(256, attend_per_cu(D, F32, WIDE)) void attend_kerne
   const int c1 = min(c0 + CW, w.s.rows * a.G.d);
   const int j0 = WIDE ? a.G.div(c0) : j_first, j1 = WIDE ? a.G.div(max(c1 - 1, 0)) : j_last;
   const int hi_all = min(w.s.start + j0 + 1, cap), lo_all = a.window ? w.s.start + j1 + 1 - a.window : 0;
-  auto apart = [&](int t) { return (t * kTile < lo_all || (t + 1) * kTile > hi_all) && j_first != j_last; };
   Columns<D, NB, F32> cols;
   PageInfo info;
 
@@ -622,21 +617,24 @@ __global__ __launch_bounds__(256, attend_per_cu(D, F32, WIDE)) void attend_kerne
       load_v(0);
     }
     for (int t = ta + wave; t < tb; t += 4) {
+      auto kf = [&](int j, int n) { return kr[j][n]; };
+      auto vf = [&](int dt) { return vr[dt]; };
       const PageInfo::Tile pages = info.tile(i, r, g);
-      const bool more = t + 4 < tb;
-      cols.tile(
-          t * kTile, pages, info.whole(i, t, lo_all, hi_all), apart(t), a.window, a.scale, lo_u, hi_u, g,
-          [&](int j, int n) { return kr[j][n]; },
-          [&](int dt) { return vr[dt]; },
-          [&] {
-            if (!more) return;
-            if (++i == 16) {
-              info.load(a.kv, w.seq, h, t + 4, 4, tb, lane);
-              i = 0;
-            }
-            load_k(i);
-          });
-      if (more) load_v(i);
+      const bool whole = info.whole(i, t, lo_all, hi_all);
+      f32x4 S[1][4];
+      cols.template score<0, 1>(S, scale_of(pages.ke), kf);
+      if (t + 4 < tb) {
+        if (++i == 16) {
+          info.load(a.kv, w.seq, h, t + 4, 4, tb, lane);
+          i = 0;
+        }
+        load_k(i);
+      }
+      if (!whole || !cols.plain(S, pages, a.scale, vf)) {
+        cols.meet(pages);
+        cols.template careful<0>(S, t * kTile + 16 * g, pages, a.window, a.scale, lo_u, hi_u, vf);
+      }
+      if (t + 4 < tb) load_v(i);
     }
   } else {
     using St = Stage<D>;
@@ -681,10 +679,26 @@ __global__ __launch_bounds__(256, attend_per_cu(D, F32, WIDE)) void attend_kerne
         const int again = lane_again(), r = again & 15, g = again >> 4;
         const char *kp = smem + stage * St::kBytes + (r >> 2) * St::kPitch + g * 64 + (r & 3) * 16;
         const char *vp = smem + stage * St::kBytes + (4 + g) * St::kPitch + r * 16;
-        cols.tile(
-            t * kTile, info.tile(i, r, g), info.whole(i, t, lo_all, hi_all), apart(t), a.window, a.scale, lo_u, hi_u, g,
-            [&](int j, int n) { return *(const uint4 *)(kp + j * (4 * D) + n * 256); },
-            [&](int dt) { return *(const uint4 *)(vp + dt * 256); }, [] {});
+        auto kf = [&](int j, int n) { return *(const uint4 *)(kp + j * (4 * D) + n * 256); };
+        auto vf = [&](int dt) { return *(const uint4 *)(vp + dt * 256); };
+        const PageInfo::Tile pages = info.tile(i, r, g);
+        bool done = info.whole(i, t, lo_all, hi_all);
+        if (__builtin_expect(done, 1)) {
+          f32x4 S[NB][4];
+          cols.template score<0, NB>(S, scale_of(pages.ke), kf);
+          done = cols.plain(S, pages, a.scale, vf);
+        }
+        if (__builtin_expect(!done, 0)) {  // one block after the other, for the registers
+          cols.meet(pages);
+          f32x4 S[1][4];
+          cols.template score<0, 1>(S, scale_of(pages.ke), kf);
+          cols.template careful<0>(S, t * kTile + 16 * g, pages, a.window, a.scale, lo_u, hi_u, vf);
+          if constexpr (NB == 2) {
+            asm volatile("" ::: "memory");
+            cols.template score<1, 1>(S, scale_of(pages.ke), kf);
+            cols.template careful<1>(S, t * kTile + 16 * g, pages, a.window, a.scale, lo_u, hi_u, vf);
+          }
+        }
       }
       ++i;
       stage = stage == N - 1 ? 0 : stage + 1;
