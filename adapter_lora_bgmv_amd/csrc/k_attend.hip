@@ -68,22 +68,24 @@ __device__ __forceinline__ float groups_sum(float x) {
 // 2^(e - 127).
 __device__ __forceinline__ float scale_of(int e) { return __uint_as_float((uint32_t)e << 23); }
 
-// Eight codes (two dwords) times a power of two as a matrix operand.
+// Four codes, and eight, times a power of two as parts of a matrix operand.
+__device__ __forceinline__ uint2 pair_bf16(uint32_t w, float scale) {
+  const bf16x2 a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, scale, false);
+  const bf16x2 b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, scale, true);
+  return make_uint2(__builtin_bit_cast(uint32_t, a), __builtin_bit_cast(uint32_t, b));
+}
+__device__ __forceinline__ uint2 pair_f16(uint32_t w, float scale) {
+  const f16x2 a = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, scale, false);
+  const f16x2 b = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, scale, true);
+  return make_uint2(__builtin_bit_cast(uint32_t, a), __builtin_bit_cast(uint32_t, b));
+}
 __device__ __forceinline__ uint4 codes_bf16(uint32_t lo, uint32_t hi, float scale) {
-  const bf16x2 a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, scale, false);
-  const bf16x2 b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, scale, true);
-  const bf16x2 c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, scale, false);
-  const bf16x2 d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, scale, true);
-  return make_uint4(__builtin_bit_cast(uint32_t, a), __builtin_bit_cast(uint32_t, b), __builtin_bit_cast(uint32_t, c),
-                    __builtin_bit_cast(uint32_t, d));
+  const uint2 a = pair_bf16(lo, scale), b = pair_bf16(hi, scale);
+  return make_uint4(a.x, a.y, b.x, b.y);
 }
 __device__ __forceinline__ uint4 codes_f16(uint32_t lo, uint32_t hi, float scale) {
-  const f16x2 a = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, scale, false);
-  const f16x2 b = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, scale, true);
-  const f16x2 c = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, scale, false);
-  const f16x2 d = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, scale, true);
-  return make_uint4(__builtin_bit_cast(uint32_t, a), __builtin_bit_cast(uint32_t, b), __builtin_bit_cast(uint32_t, c),
-                    __builtin_bit_cast(uint32_t, d));
+  const uint2 a = pair_f16(lo, scale), b = pair_f16(hi, scale);
+  return make_uint4(a.x, a.y, b.x, b.y);
 }
 __device__ __forceinline__ f32x4 mfma16_f16(uint4 a, uint4 b, f32x4 c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
@@ -334,6 +336,8 @@ struct Columns {
     }
   }
 
+  static __device__ __forceinline__ uint32_t &word(uint4 &v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
+
   // The largest of the lane's scores of a column.
   __device__ __forceinline__ static float largest(const f32x4 (&S)[4]) {
     float mx = S[0][0];
@@ -406,9 +410,13 @@ struct Columns {
 
   // The rest of a tile that every column sees all of, from its scores and
   // values vf(dt); false, and nothing changed, where something unusual sends
-  // it through `careful`.
-  template <typename V>
-  __device__ __forceinline__ bool plain(const f32x4 (&S)[NB][4], PageInfo::Tile info, float cs, V vf) {
+  // it through `careful`.  AHEAD: the next tile's scores, from its keys
+  // kf(j, n) under `scale`, take the place of S.  In one wave the matrix
+  // products hide the conversions and exponentials between them, so those
+  // scores are computed among this tile's weights and the order is asked for:
+  // one product, then its share of the rest.
+  template <bool AHEAD, typename V, typename K>
+  __device__ __forceinline__ bool plain(f32x4 (&S)[NB][4], PageInfo::Tile info, float cs, V vf, float scale, K kf) {
     using X = ValueExp<F32>;
     if (__builtin_expect(mixed || __any(info.ve < X::kLo || info.ve > X::kHi), 0)) return false;
     float top[NB];
@@ -424,16 +432,107 @@ struct Columns {
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb) M[nb] = M[nb] == kNone ? fmaxf(kNone, groups_max(top[nb])) : M[nb];  // the first: nothing to rescale
     }
-    uint4 pf[NB][2][NT];
-#pragma unroll
-    for (int nb = 0; nb < NB; ++nb) l[nb] += weigh(S[nb], cs, kTop - M[nb], pf[nb]);
     const float vs = scale_of(info.ve + X::kAdd);
-    uint4 next = vf(0);
+    uint4 pf[NB][2][NT];
+    if constexpr (!AHEAD) {
 #pragma unroll
-    for (int dt = 0; dt < ND; ++dt) {
-      const uint4 now = next;
-      if (dt + 1 < ND) next = vf(dt + 1);
-      add<0, NB>(dt, now, vs, pf);
+      for (int nb = 0; nb < NB; ++nb) l[nb] += weigh(S[nb], cs, kTop - M[nb], pf[nb]);
+      uint4 next = vf(0);
+#pragma unroll
+      for (int dt = 0; dt < ND; ++dt) {
+        const uint4 now = next;
+        if (dt + 1 < ND) next = vf(dt + 1);
+        add<0, NB>(dt, now, vs, pf);
+      }
+    } else if constexpr (F32) {
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb) l[nb] += weigh(S[nb], cs, kTop - M[nb], pf[nb]);
+      score<0, NB>(S, scale, kf);
+#pragma unroll
+      for (int dt = 0; dt < ND; ++dt) add<0, NB>(dt, vf(dt), vs, pf);
+    } else {
+      // step k: a 32-dim half of a key fragment against every column block,
+      // with kEach weights of each block and the conversion of the next half
+      constexpr int kFrags = 4 * (D / 64), kSteps = 2 * kFrags, kEach = 16 / kSteps;
+      uint4 x[3] = {kf(0, 0), kf(1 / (D / 64), 1 % (D / 64)), z4()};
+      f32x4 T[NB][4];
+      float f[NB], p[NB][16], b[NB];
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb) {
+        b[nb] = kTop - M[nb];
+        f[nb] = fmaf(S[nb][0][0], cs, b[nb]);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) T[nb][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+      }
+      uint4 cur = codes_bf16(x[0].x, x[0].y, scale);
+#pragma unroll
+      for (int k = 0; k < kSteps; ++k) {
+        const int m = k / 2, j = m / (D / 64), n = m % (D / 64);
+        if (k % 2 == 0) {  // two fragments ahead; the values follow the keys
+          if (m + 2 < kFrags) x[(m + 2) % 3] = kf((m + 2) / (D / 64), (m + 2) % (D / 64));
+          else x[(m + 2) % 3] = vf(m + 2 - kFrags);
+        }
+        const uint4 &y = x[((k + 1) / 2) % 3];
+        uint4 after = z4();
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) {
+          __builtin_amdgcn_sched_barrier(0);
+          T[nb][j] = mfma16(cur, q[nb][2 * n + k % 2][0], T[nb][j]);
+          if (nb == 0) {
+            const uint32_t w = k % 2 ? y.x : y.z;
+            const uint2 c = k + 1 < kSteps ? pair_bf16(w, scale) : pair_f16(w, vs);
+            after.x = c.x;
+            after.y = c.y;
+          }
+          if (nb == NB - 1) {
+            const uint32_t w = k % 2 ? y.y : y.w;
+            const uint2 c = k + 1 < kSteps ? pair_bf16(w, scale) : pair_f16(w, vs);
+            after.z = c.x;
+            after.w = c.y;
+          }
+#pragma unroll
+          for (int i = 0; i < kEach; ++i) {
+            const int e = k * kEach + i;
+            p[nb][e] = __builtin_amdgcn_exp2f(f[nb]);
+            if (e + 1 < 16) f[nb] = fmaf(S[nb][(e + 1) >> 2][(e + 1) & 3], cs, b[nb]);
+            if (e > 0) l[nb] += p[nb][e - 1];
+            if (e >= 2 && e % 2 == 0) word(pf[nb][(e - 2) / 8][0], (e - 2) / 2 % 4) = pack_f16(p[nb][e - 2], p[nb][e - 1]);
+          }
+        }
+        cur = after;
+      }
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb) {
+        l[nb] += p[nb][15];
+        pf[nb][1][0].w = pack_f16(p[nb][14], p[nb][15]);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) S[nb][j] = T[nb][j];
+      }
+      // step k: half of sixteen dims' values against every block's weights
+#pragma unroll
+      for (int k = 0; k < 2 * ND; ++k) {
+        const int dt = k / 2, m = kFrags + dt;
+        if (k % 2 == 0 && dt + 2 < ND) x[(m + 2) % 3] = vf(dt + 2);
+        const uint4 &y = x[(kFrags + (k + 1) / 2) % 3];
+        uint4 after = z4();
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) {
+          __builtin_amdgcn_sched_barrier(0);
+          acc[nb][dt] = mfma16_f16(cur, pf[nb][k % 2][0], acc[nb][dt]);
+          if (k + 1 == 2 * ND) continue;
+          if (nb == 0) {
+            const uint2 c = pair_f16(k % 2 ? y.x : y.z, vs);
+            after.x = c.x;
+            after.y = c.y;
+          }
+          if (nb == NB - 1) {
+            const uint2 c = pair_f16(k % 2 ? y.y : y.w, vs);
+            after.z = c.x;
+            after.w = c.y;
+          }
+        }
+        cur = after;
+      }
     }
     return true;
   }
@@ -548,11 +647,16 @@ struct Columns {
 
 // ---------------------------------------------------------------- kernels
 // LDS of the wide form: stages of a tile, each its 4 groups of K and 4 of V.
-// Groups lie 64 bytes more than their 16 D apart, so that the keys of four
-// groups that a wave reads together fall into different banks.
+// A 16-byte read serves 16 lanes at a time, in sets that take two of the four
+// token quads r / 4 from lanes g = 0 and the other two from g = 1 (and so for
+// 2 and 3): free of conflicts where a lane's 64-byte place modulo 256 is its
+// quad's alone.  V lies so by itself.  K's 64-byte units (quad j, chunk c) of
+// group q are put at unit 4 c + (j + q) % 4: the DMA's lanes fetch them from
+// where they are (conflicts 3.3 -> 0 cycles a read).
 template <int D>
 struct Stage {
-  static constexpr int kPitch = 16 * D + 64, kBytes = 8 * kPitch, kCount = D > 128 ? 2 : 3;
+  static constexpr int kPitch = 16 * D, kBytes = 8 * kPitch, kCount = D > 128 ? 2 : 4;
+  static constexpr bool kAhead = kCount == 4;  // a tile's scores are computed during the one before
   static constexpr int kDma = 2 * (D / 64);  // instructions of a wave (its group's K and V) a stage
 };
 
@@ -630,7 +734,7 @@ __global__ __launch_bounds__(256, attend_per_cu(D, F32, WIDE)) void attend_kerne
         }
         load_k(i);
       }
-      if (!whole || !cols.plain(S, pages, a.scale, vf)) {
+      if (!whole || !cols.template plain<false>(S, pages, a.scale, vf, 0.f, kf)) {
         cols.meet(pages);
         cols.template careful<0>(S, t * kTile + 16 * g, pages, a.window, a.scale, lo_u, hi_u, vf);
       }
@@ -640,14 +744,15 @@ __global__ __launch_bounds__(256, attend_per_cu(D, F32, WIDE)) void attend_kerne
     using St = Stage<D>;
     constexpr int N = St::kCount;
     const uint32_t base = lds_addr(smem);
-    // wave k brings group k of the tile
+    // wave k brings group k of the tile; lane l's unit is 4 c + l / 4 % 4 of 4 c .. 4 c + 3, c = 4 n + l / 16
+    const int from_k = ((((lane >> 2) - wave) & 3) * (D / 16) + (lane >> 4)) * 64 + (lane & 3) * 16;
     auto bring = [&](int groups, int i, int stage) {
-      const size_t at = (size_t)(unsigned)__builtin_amdgcn_readlane(groups, 4 * i + wave) * (16 * D) + lane * 16;
+      const size_t at = (size_t)(unsigned)__builtin_amdgcn_readlane(groups, 4 * i + wave) * (16 * D);
       const uint32_t to = base + stage * St::kBytes + wave * St::kPitch;
 #pragma unroll
-      for (int n = 0; n < D / 64; ++n) dma16(a.kv.k + at + n * 1024, to + n * 1024);
+      for (int n = 0; n < D / 64; ++n) dma16(a.kv.k + at + from_k + n * 256, to + n * 1024);
 #pragma unroll
-      for (int n = 0; n < D / 64; ++n) dma16(a.kv.v + at + n * 1024, to + 4 * St::kPitch + n * 1024);
+      for (int n = 0; n < D / 64; ++n) dma16(a.kv.v + at + lane * 16 + n * 1024, to + 4 * St::kPitch + n * 1024);
     };
     cols.load(a, w, h, c0, c1, r, g);
     info.load(a.kv, w.seq, h, ta, 1, tb, lane);
@@ -659,9 +764,13 @@ __global__ __launch_bounds__(256, attend_per_cu(D, F32, WIDE)) void attend_kerne
     const int wave_hi = c0 < c1 ? min(w.s.start + j1 + 1, cap) : 0;
     PageInfo later = info;  // of the next 16 tiles
     int later_page = -1, i = 0, stage = 0;
+    f32x4 S[NB][4];
+    bool ahead = false;  // S holds the tile's scores
+
     for (int t = ta; t < tb; ++t) {
-      // this wave's part of the tile is here, then everybody's; nobody reads the tile before any more
-      if (N == 3 && t + 1 < tb) wait_vmcnt<St::kDma>();
+      // this wave's part of the tile (of the next one too, where its keys are
+      // read) is here, then everybody's; nobody reads the tile before any more
+      if (N == 4 && t + 2 < tb) wait_vmcnt<St::kDma>();
       else wait_vmcnt<0>();
       asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
       block_barrier();
@@ -677,18 +786,26 @@ __global__ __launch_bounds__(256, attend_per_cu(D, F32, WIDE)) void attend_kerne
       if (t * kTile < wave_hi && (t + 1) * kTile > wave_lo) {
         // the lane's places anew: the registers that would hold them are wanted
         const int again = lane_again(), r = again & 15, g = again >> 4;
-        const char *kp = smem + stage * St::kBytes + (r >> 2) * St::kPitch + g * 64 + (r & 3) * 16;
+        const char *kp = smem + stage * St::kBytes + (r >> 2) * St::kPitch + g * 256 + (r & 3) * 16;
         const char *vp = smem + stage * St::kBytes + (4 + g) * St::kPitch + r * 16;
-        auto kf = [&](int j, int n) { return *(const uint4 *)(kp + j * (4 * D) + n * 256); };
+        auto kf = [&](int j, int n) { return *(const uint4 *)(kp + (((r >> 2) + j) & 3) * 64 + n * 1024); };
         auto vf = [&](int dt) { return *(const uint4 *)(vp + dt * 256); };
         const PageInfo::Tile pages = info.tile(i, r, g);
         bool done = info.whole(i, t, lo_all, hi_all);
         if (__builtin_expect(done, 1)) {
-          f32x4 S[NB][4];
-          cols.template score<0, NB>(S, scale_of(pages.ke), kf);
-          done = cols.plain(S, pages, a.scale, vf);
+          if (!ahead) cols.template score<0, NB>(S, scale_of(pages.ke), kf);
+          if (St::kAhead && t + 1 < tb) {
+            const char *np = smem + (stage == N - 1 ? 0 : stage + 1) * St::kBytes + (kp - smem - stage * St::kBytes);
+            auto nf = [&](int j, int n) { return *(const uint4 *)(np + (((r >> 2) + j) & 3) * 64 + n * 1024); };
+            const int nk = __shfl(i == 15 ? later.ke : info.ke, 4 * ((i + 1) & 15) + (r >> 2), 64);
+            done = cols.template plain<true>(S, pages, a.scale, vf, scale_of(nk), nf);
+            ahead = done;
+          } else {
+            done = cols.template plain<false>(S, pages, a.scale, vf, 0.f, kf);
+          }
         }
         if (__builtin_expect(!done, 0)) {  // one block after the other, for the registers
+          ahead = false;
           cols.meet(pages);
           f32x4 S[1][4];
           cols.template score<0, 1>(S, scale_of(pages.ke), kf);
