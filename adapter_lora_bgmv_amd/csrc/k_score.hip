@@ -16,12 +16,14 @@
 // above the complement of the index, all of them different.  Of the 64
 // lanes' maxima a wave finds (by ballots, bit after bit) a value that `top`
 // of them reach: no smaller logit can be among the `top`.  A lane whose batch
-// reaches it puts what does on a list in LDS, and the wave's value is found
-// anew; after a few batches that is rare.  At the end the list shrinks to
-// what reaches the largest of the four waves' values, and an entry's place is
-// the number of larger keys.  Where the list overflows (equal or rising
-// logits) the chunk is read again for what reaches the final value, and where
-// even that is too much, once for every place.
+// reaches it puts the batch's maximum and number on a list in LDS, and the
+// wave's value is found anew; after a few batches that is rare.  At the end
+// the batches on the list whose maximum reaches the largest of the four
+// waves' values are read again (they are few: 32 logits each), and an entry's
+// place among what reaches it is the number of larger keys.  Where a list
+// overflows (equal or rising logits) the whole chunk is read again for what
+// reaches the final value, and where even that is too much, once for every
+// place.
 //
 // A row of several chunks leaves a record of each in the workspace; the last
 // chunk to arrive joins them, the lists by the same selection.
@@ -94,12 +96,13 @@ __device__ __forceinline__ uint32_t kth_floor(uint32_t key, int k) {
 
 struct ScoreLds {
   u64 list[kScoreList], kept[kScoreList];
+  uint32_t pick[kScoreList];
   u64 top[kScoreMaxTop];
   u64 red[4];
   float m[4], s[4], sx[4];
   uint32_t floor[4];
   int above[4];
-  int count, kept_count;
+  int count, kept_count, picks;
   unsigned arrived;
 };
 
@@ -111,20 +114,16 @@ __device__ __forceinline__ void put(u64 *list, int *count, u64 key) {
 
 // The `k` largest keys into lds.top, in order (0 where there are fewer).
 // `floor`: a value (upper half) that at least k of the keys reach, if there
-// are k.  lds.list holds every key that reaches it, unless lds.count says
-// that it overflowed: then `each(f)` calls f(key) for the thread's keys.
-// Called by the whole workgroup after a barrier; ends with one.
+// are k.  lds.kept holds the lds.kept_count keys that reach it, unless `all`:
+// then each(f) calls f(key) for all of the thread's keys.  Called by the
+// whole workgroup after a barrier; ends with one.
 template <typename Each>
-__device__ __forceinline__ void select_top(int k, uint32_t floor, Each each, ScoreLds &lds) {
+__device__ __forceinline__ void rank_top(int k, uint32_t floor, bool all, Each each, ScoreLds &lds) {
   const int tid = threadIdx.x;
-  const int n = lds.count;
-  if (tid == 0) lds.kept_count = 0;
   if (tid < k) lds.top[tid] = 0;
-  __syncthreads();
-  if (n <= kScoreList) {
-    for (int c = tid; c < n; c += kScoreThreads)
-      if ((uint32_t)(lds.list[c] >> 32) >= floor) put(lds.kept, &lds.kept_count, lds.list[c]);
-  } else {
+  if (all) {
+    if (tid == 0) lds.kept_count = 0;
+    __syncthreads();
     each([&](u64 key) {
       if ((uint32_t)(key >> 32) >= floor) put(lds.kept, &lds.kept_count, key);
     });
@@ -194,7 +193,7 @@ __global__ __launch_bounds__(kScoreThreads) void score_kernel(ScoreArgs a) {
   const int skew = (int)(((uintptr_t)x & 15) / sizeof(T));
   const int begin = chunk * a.batches * (NV * kStride) - skew + tid * VE;  // index of the thread's first element
   const int id = a.ids[row];
-  if (tid == 0) lds.count = 0;
+  if (tid == 0) lds.count = lds.kept_count = lds.picks = 0;
   __syncthreads();
 
   constexpr uint32_t kNegInf = sizeof(T) == 4 ? 0xff800000u : 0xff80ff80u;
@@ -247,16 +246,7 @@ __global__ __launch_bounds__(kScoreThreads) void score_kernel(ScoreArgs a) {
     if (a.top && __any(holds && ordered(mx) >= floor)) {
       // lanes without elements count as lower than any
       floor = max(floor, kth_floor(begin < a.n_vocab ? ordered(m) : 0u, a.top));
-      if (holds && ordered(mx) >= floor) {
-#pragma unroll
-        for (int i = 0; i < NV; ++i)
-#pragma unroll
-          for (int e = 0; e < VE; ++e) {
-            const int at = first + i * kStride + e;
-            const u64 key = key_of(Vec<T>::at(v[i], e), (uint32_t)at);
-            if ((uint32_t)(key >> 32) >= floor && at >= 0 && at < a.n_vocab) put(lds.list, &lds.count, key);
-          }
-      }
+      if (holds && ordered(mx) >= floor) put(lds.list, &lds.count, (u64)ordered(mx) << 32 | (uint32_t)(b * kScoreThreads + tid));
     }
     const float base = m == -INFINITY ? 0.f : m;
 #pragma unroll
@@ -301,7 +291,25 @@ __global__ __launch_bounds__(kScoreThreads) void score_kernel(ScoreArgs a) {
         }
       }
     };
-    select_top(a.top, f, each, lds);
+    __syncthreads();
+    const int listed = lds.count;
+    for (int c = tid; c < min(listed, kScoreList); c += kScoreThreads)
+      if ((uint32_t)(lds.list[c] >> 32) >= f) lds.pick[atomicAdd(&lds.picks, 1)] = (uint32_t)lds.list[c];
+    __syncthreads();
+    const int picks = lds.picks;
+    for (int c = tid / kScoreBatch; c < picks; c += kScoreThreads / kScoreBatch) {
+      const int who = lds.pick[c], i = tid % kScoreBatch;
+      const int at = (chunk * a.batches + who / kScoreThreads) * (NV * kStride) - skew + who % kScoreThreads * VE +
+                     i / VE * kStride + i % VE;
+      if (at >= 0 && at < a.n_vocab) {
+        const u64 key = key_of(Vec<T>::one(x + at), (uint32_t)at);
+        if ((uint32_t)(key >> 32) >= f) put(lds.kept, &lds.kept_count, key);
+      }
+    }
+    __syncthreads();
+    const bool all = listed > kScoreList || lds.kept_count > kScoreList;
+    __syncthreads();  // everybody has read the count before it may be cleared
+    rank_top(a.top, f, all, each, lds);
   } else {
     __syncthreads();
   }
@@ -361,7 +369,7 @@ __global__ __launch_bounds__(kScoreThreads) void score_kernel(ScoreArgs a) {
     const uint32_t f = kth_floor(best, a.top);
     if (lane == 0) lds.floor[wave] = f;
   }
-  if (tid == 0) lds.count = 0;
+  if (tid == 0) lds.kept_count = 0;
   __syncthreads();
   const float M_raw = fmaxf(fmaxf(lds.m[0], lds.m[1]), fmaxf(lds.m[2], lds.m[3]));
   const float M = M_raw == -INFINITY ? 0.f : M_raw;
@@ -388,10 +396,10 @@ __global__ __launch_bounds__(kScoreThreads) void score_kernel(ScoreArgs a) {
     };
     if (best >= f)
       each([&](u64 key) {
-        if ((uint32_t)(key >> 32) >= f) put(lds.list, &lds.count, key);
+        if ((uint32_t)(key >> 32) >= f) put(lds.kept, &lds.kept_count, key);
       });
     __syncthreads();
-    select_top(a.top, f, each, lds);
+    rank_top(a.top, f, false, each, lds);
   } else {
     __syncthreads();
   }
