@@ -179,8 +179,11 @@ __device__ __forceinline__ bool find_work(const AttendArgs &a, int u, int lane, 
     const SeqDev s = i == i0 ? first : load_seq(a.kv, i);
     total += (long long)seq_blocks<CB>(a, s) * unit_tiles<CB>(a, s, cap);
   }
-#pragma unroll
-  for (int off = 32; off > 0; off >>= 1) total += __shfl_xor(total, off, 64);
+  // over the lanes in two parts of 24 and up to 32 bits
+  total = min(total, 1ll << 50);
+  const unsigned low = (unsigned)__builtin_amdgcn_readlane(wave_incl_scan((int)(total & 0xffffff)), 63);
+  const unsigned high = (unsigned)__builtin_amdgcn_readlane(wave_incl_scan((int)(total >> 24)), 63);
+  total = ((long long)high << 24) + low;
   // tiles of a chunk at most (few tiles, the common case, need no 64-bit division)
   int c = a.min_tiles;
   if (total > (long long)c * a.per_head)
@@ -193,9 +196,10 @@ __device__ __forceinline__ bool find_work(const AttendArgs &a, int u, int lane, 
     items += b * nc;
     slots += nc > 1 ? b * nc : 0;
   }
-  const int incl = wave_incl_scan(items, lane), sincl = wave_incl_scan(slots, lane);
+  const int incl = wave_incl_scan(items), sincl = wave_incl_scan(slots);
   *all_slots = __builtin_amdgcn_readlane(sincl, 63);
   int found = -1, block = 0, chunk = 0, nc_of = 1, slot = 0;
+  SeqDev its = first;
   if (u < incl && u >= incl - items) {
     int at = incl - items, sat = sincl - slots;
     for (int i = i0; i < i1; ++i) {
@@ -203,6 +207,7 @@ __device__ __forceinline__ bool find_work(const AttendArgs &a, int u, int lane, 
       const int b = seq_blocks<CB>(a, s), nc = (unit_tiles<CB>(a, s, cap) + c - 1) / c;
       if (u < at + b * nc) {
         found = i;
+        its = s;
         nc_of = nc;
         const int unit = (u - at) / nc;
         chunk = (u - at) - unit * nc;
@@ -222,11 +227,7 @@ __device__ __forceinline__ bool find_work(const AttendArgs &a, int u, int lane, 
   w->chunk = __builtin_amdgcn_readlane(chunk, src);
   w->nc = __builtin_amdgcn_readlane(nc_of, src);
   w->slot = __builtin_amdgcn_readlane(slot, src);
-  w->s = load_seq(a.kv, w->seq);
-  w->s.row0 = __builtin_amdgcn_readfirstlane(w->s.row0);
-  w->s.rows = __builtin_amdgcn_readfirstlane(w->s.rows);
-  w->s.len = __builtin_amdgcn_readfirstlane(w->s.len);
-  w->s.start = __builtin_amdgcn_readfirstlane(w->s.start);
+  w->s = seq_of_lane(its, src);
   return true;
 }
 

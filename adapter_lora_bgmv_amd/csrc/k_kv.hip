@@ -42,15 +42,18 @@ __device__ __forceinline__ int touched(const KvDev &a, const SeqDev &s, int *p0)
 // pages of `per` sequences, one scan over the lanes, and the lane whose share
 // holds u walks it.
 __device__ __forceinline__ bool find_page(const KvDev &a, int u, int lane, SeqDev *s, int *seq, int *page) {
-  const int per = (a.n_seqs + 63) >> 6;
-  int sum = 0, p0;
-  for (int i = lane * per; i < min((lane + 1) * per, a.n_seqs); ++i) sum += touched(a, load_seq(a, i), &p0);
-  const int incl = wave_incl_scan(sum, lane);
+  const int per = (a.n_seqs + 63) >> 6, i0 = lane * per, i1 = min(i0 + per, a.n_seqs);
+  SeqDev its = {0, 0, 0, 0};  // the lane's first sequence, later the one that holds u
+  if (i0 < i1) its = load_seq(a, i0);
+  int p0, sum = i0 < i1 ? touched(a, its, &p0) : 0;
+  for (int i = i0 + 1; i < i1; ++i) sum += touched(a, load_seq(a, i), &p0);
+  const int incl = wave_incl_scan(sum);
   int found = -1, where = 0;
   if (u < incl && u >= incl - sum) {
     int at = incl - sum;
-    for (int i = lane * per; i < (lane + 1) * per; ++i) {
-      const int c = touched(a, load_seq(a, i), &p0);
+    for (int i = i0; i < i1; ++i) {
+      if (i > i0) its = load_seq(a, i);
+      const int c = touched(a, its, &p0);
       if (u < at + c) {
         found = i;
         where = p0 + u - at;
@@ -64,7 +67,7 @@ __device__ __forceinline__ bool find_page(const KvDev &a, int u, int lane, SeqDe
   const int src = __ffsll(who) - 1;
   *seq = __builtin_amdgcn_readlane(found, src);
   *page = __builtin_amdgcn_readlane(where, src);
-  *s = load_seq(a, *seq);
+  *s = seq_of_lane(its, src);
   return true;
 }
 
@@ -267,6 +270,24 @@ __device__ __forceinline__ void store_row4<float>(float *p, uint32_t w, float sc
   *(float4 *)p = make_float4(a[0] * scale, a[1] * scale, b[0] * scale, b[1] * scale);
 }
 
+// Sixteen values of a row, 16 bytes at a time.
+template <typename T>
+__device__ __forceinline__ void store_row16(T *p, const uint32_t w[4], float scale) {
+  if constexpr (sizeof(T) == 2) {
+    uint32_t o[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      o[2 * i] = __builtin_bit_cast(uint32_t, (bf16x2)__builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w[i], scale, false));
+      o[2 * i + 1] = __builtin_bit_cast(uint32_t, (bf16x2)__builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w[i], scale, true));
+    }
+    ((uint4 *)p)[0] = make_uint4(o[0], o[1], o[2], o[3]);
+    ((uint4 *)p)[1] = make_uint4(o[4], o[5], o[6], o[7]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) store_row4<T>(p + 4 * i, w[i], scale);
+  }
+}
+
 // Grid as in the write.  Every product is exact: e4m3 times a power of two in
 // the range of the exponent bytes is a bf16 number.
 template <typename T, int D, int IT>
@@ -308,9 +329,7 @@ __global__ __launch_bounds__(kKvThreads) void kv_read_kernel(KvDev a, T *krows, 
     if (!is_v) {
       const int t = it / (D / 16), c = it % (D / 16);
       if (t < t0 || t >= t1) continue;
-      T *p = dst + (size_t)(row0 + t) * stride + c * 16;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) store_row4<T>(p + 4 * i, r[i], scale);
+      store_row16<T>(dst + (size_t)(row0 + t) * stride + c * 16, r, scale);
     } else {
       const int q = (it & 3) + 4 * (it / D), db = (it >> 2) % (D / 4);
       transpose4(r);

@@ -48,13 +48,21 @@ __device__ __forceinline__ int page_of(const KvDev &a, int i, int p) {
   return (unsigned)id < (unsigned)a.n_pages ? id : -1;
 }
 
-__device__ __forceinline__ int wave_incl_scan(int v, int lane) {
-#pragma unroll
-  for (int off = 1; off < 64; off <<= 1) {
-    const int o = __shfl_up(v, off, 64);
-    if (lane >= off) v += o;
-  }
+// Sums over the lanes up to and including this one, in registers: within rows
+// of 16 lanes, then the last lanes of rows 0 and 2 over rows 1 and 3, then
+// lane 31 over rows 2 and 3.
+__device__ __forceinline__ int wave_incl_scan(int v) {
+  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xf, 0xf, false);  // row_shr:1
+  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xf, 0xf, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xf, 0xf, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xf, 0xf, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xa, 0xf, false);  // row_bcast:15
+  v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xc, 0xf, false);  // row_bcast:31
   return v;
+}
+__device__ __forceinline__ SeqDev seq_of_lane(const SeqDev &s, int lane) {
+  return {__builtin_amdgcn_readlane(s.row0, lane), __builtin_amdgcn_readlane(s.rows, lane),
+          __builtin_amdgcn_readlane(s.len, lane), __builtin_amdgcn_readlane(s.start, lane)};
 }
 
 // The e4m3 byte pair conversions (gfx950).
