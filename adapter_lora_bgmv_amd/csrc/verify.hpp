@@ -113,23 +113,27 @@ struct AttendArgs {
   int cols_lo, cols_hi;  // takes the sequences whose rows x G lie in (cols_lo, cols_hi]
   int per_head;   // workgroups per key/value head that the tiles are spread over
   int min_tiles;  // of a chunk: fewer are not split
-  AttendRecord *records;  // [kAttendSlots] of split units' chunks
+  AttendRecord *records;  // of split units' chunks
   int *used;              // slots in use, written by the call
   float *part;            // their partial results
 };
+// The forms of the attention, by the columns (row, query head of the group)
+// that a sequence brings: narrow up to 16, wide above, and many, with units of
+// 256, where bf16 calls may bring more than 64.
+enum AttendForm { kNarrow, kWide, kMany };
+constexpr int kAttendNarrowCols = 16, kAttendWideCols = 64, kAttendManyCols = 256;
+constexpr int attend_cols(AttendForm f) { return f == kNarrow ? kAttendNarrowCols : f == kWide ? kAttendWideCols : kAttendManyCols; }
 // Workgroups of a CU that a form's registers allow, those that a launch's
 // tiles are spread over (one round of the card), and the partial slots that
 // takes: a unit is split into nc > 1 chunks only where its tiles exceed a
 // chunk's, so the split units' chunks are fewer than twice as many.
-constexpr int attend_per_cu(int dim, bool f32, bool wide) { return dim > 128 && (f32 || !wide) ? 1 : 2; }
-constexpr int attend_target(int dim, int dtype, bool wide) { return 256 * attend_per_cu(dim, dtype == 0, wide); }
-constexpr int kAttendSlots = 2 * 512;
+constexpr int attend_per_cu(int dim, bool f32, AttendForm f) { return f == kMany || (dim > 128 && (f32 || f == kNarrow)) ? 1 : 2; }
+constexpr int attend_target(int dim, int dtype, AttendForm f) { return 256 * attend_per_cu(dim, dtype == 0, f); }
+constexpr int attend_slots(int dim, int dtype, AttendForm f) { return 2 * attend_target(dim, dtype, f); }
 // Tiles that are worth a chunk of their own.
-constexpr int kAttendMinTilesNarrow = 16, kAttendMinTilesWide = 4;
-constexpr int kAttendNarrowCols = 16;  // of a unit of the narrow form; sequences of more take the wide one
-// Columns (row, query head of the group) of a wide unit: 64 nb.
-constexpr int attend_wide_nb(int dim, int dtype) { return dtype == 0 || dim > 128 ? 1 : 2; }
-hipError_t launch_attend(const AttendArgs &a, int dim, int dtype, int nb, bool wide, hipStream_t st);
+constexpr int attend_min_tiles(AttendForm f) { return f == kNarrow ? 16 : 4; }
+hipError_t launch_attend(const AttendArgs &a, int dim, int dtype, AttendForm f, hipStream_t st);
+hipError_t launch_attend_many(const AttendArgs &a, int dim, hipStream_t st);
 
 // The join of split units, of one or both forms.
 struct AttendJoin {
@@ -137,7 +141,7 @@ struct AttendJoin {
     const AttendRecord *records;
     const int *used;
     const float *part;
-    int cb;  // columns of a slot
+    int slots, cb;  // slots at most, and the columns of each
   } form[2];
   void *out;
   int out_stride;

@@ -99,31 +99,43 @@ int timed(const char *what, hipStream_t st, F launch) {
 }
 
 // Which forms an attention call launches.  Sequences of up to
-// kAttendNarrowCols columns take the narrow form, others the wide one.
-// max_rows bounds every sequence's rows and with n also from below; where it
-// leaves one form, that form takes every sequence, so that a wrong bound
-// costs time only.
+// kAttendNarrowCols columns take the narrow form, longer ones the wide form
+// or, in bf16 calls whose rows may be many, the form for those.  max_rows
+// bounds every sequence's rows and with n also from below; where it leaves
+// one form, that form takes every sequence, so that a wrong bound costs time
+// only.
 struct AttendPlan {
-  bool narrow, wide, split;  // split: a unit may be cut into chunks
-  int nb;                    // 64 nb columns of a wide unit
-  size_t records, wide_part, total;  // offsets in the workspace; the narrow form's partials lie last
+  struct Part {
+    AttendForm form;
+    size_t records, sums;  // offsets in the workspace, after a place for the slots in use
+    int slots;
+  } part[2];
+  int parts;
+  bool split;  // a unit may be cut into chunks
+  size_t total;
 };
 AttendPlan attend_plan(const lora_kv_cache *c, const lora_kv_seqs *s, int32_t dtype, uint32_t n_heads, uint32_t n) {
   AttendPlan p{};
+  const int dim = (int)c->head_dim;
   const uint64_t G = std::max<uint64_t>(1, n_heads / std::max(1u, c->n_kv_heads));
   const uint64_t most = s->max_rows ? std::min(s->max_rows, n) : n;
   const uint64_t others = (uint64_t)(s->n_seqs ? s->n_seqs - 1 : 0) * most;
   const uint64_t least = n > others ? n - others : 0;
-  p.wide = most * G > (uint64_t)kAttendNarrowCols;
-  p.narrow = !p.wide || least * G <= (uint64_t)kAttendNarrowCols;
-  p.nb = most * G > 64 ? attend_wide_nb((int)c->head_dim, dtype) : 1;
   // a table that holds no more tiles than a chunk's least splits nothing
   const uint64_t tiles = ((uint64_t)s->max_pages * c->page_tokens + 63) / 64;
-  p.split = tiles > (uint64_t)(p.wide ? kAttendMinTilesWide : kAttendMinTilesNarrow);
-  p.records = 256;
-  p.wide_part = p.records + 2 * up256(kAttendSlots * sizeof(AttendRecord));
-  const size_t column = (size_t)kAttendSlots * (c->head_dim + 3) * 4;
-  p.total = p.wide_part + (p.wide ? up256(column * 64 * p.nb) : 0) + (p.narrow ? up256(column * 16) : 0);
+  p.total = 256;
+  auto add = [&](AttendForm f) {
+    AttendPlan::Part &q = p.part[p.parts++];
+    q.form = f;
+    q.slots = attend_slots(dim, dtype, f);
+    q.records = p.total;
+    q.sums = q.records + up256(q.slots * sizeof(AttendRecord));
+    p.total = q.sums + up256((size_t)q.slots * attend_cols(f) * (dim + 3) * 4);
+    p.split |= tiles > (uint64_t)attend_min_tiles(f);
+  };
+  const bool wide = most * G > (uint64_t)kAttendNarrowCols;
+  if (wide) add(dtype == LORA_BF16 && dim <= 128 && most * G > (uint64_t)kAttendWideCols ? kMany : kWide);
+  if (!wide || least * G <= (uint64_t)kAttendNarrowCols) add(kNarrow);
   return p;
 }
 
@@ -215,33 +227,23 @@ int lora_kv_attend(const lora_kv_cache *cache, const lora_kv_seqs *seqs, int32_t
   j.heads = a.heads;
   j.G = a.G;
   char *ws = (char *)workspace;
-  int forms = 0;
-  float *part = (float *)(ws + p.wide_part);
-  auto form = [&](bool wide, int cb, int min_tiles) {
-    a.used = (int *)ws + forms;
-    a.records = (AttendRecord *)(ws + p.records + forms * up256(kAttendSlots * sizeof(AttendRecord)));
-    a.part = part;
-    a.min_tiles = min_tiles;
-    a.per_head = std::max(1, attend_target((int)cache->head_dim, dtype, wide) / a.kv.H);
-    j.form[forms++] = {a.records, a.used, part, cb};
-    part += up256((size_t)kAttendSlots * cb * (cache->head_dim + 3) * 4) / 4;
-  };
   hipStream_t st = (hipStream_t)stream;
   return timed(what, st, [&] {
     hipError_t e = hipSuccess;
-    if (p.wide) {  // the long rows first: the short ones fill in behind them
-      a.cols_lo = p.narrow ? kAttendNarrowCols : 0;
-      a.cols_hi = INT_MAX;
-      form(true, 64 * p.nb, kAttendMinTilesWide);
-      e = launch_attend(a, (int)cache->head_dim, dtype, p.nb, true, st);
+    const int dim = (int)cache->head_dim;
+    for (int i = 0; i < p.parts && e == hipSuccess; ++i) {  // the long rows first: the short ones fill in behind them
+      const AttendPlan::Part &q = p.part[i];
+      a.used = (int *)ws + i;
+      a.records = (AttendRecord *)(ws + q.records);
+      a.part = (float *)(ws + q.sums);
+      a.min_tiles = attend_min_tiles(q.form);
+      a.per_head = std::max(1, attend_target(dim, dtype, q.form) / a.kv.H);
+      a.cols_lo = p.parts > 1 && i == 0 ? kAttendNarrowCols : 0;
+      a.cols_hi = i == 1 ? kAttendNarrowCols : INT_MAX;
+      j.form[i] = {a.records, a.used, a.part, q.slots, attend_cols(q.form)};
+      e = q.form == kMany ? launch_attend_many(a, dim, st) : launch_attend(a, dim, dtype, q.form, st);
     }
-    if (p.narrow && e == hipSuccess) {
-      a.cols_lo = 0;
-      a.cols_hi = p.wide ? kAttendNarrowCols : INT_MAX;
-      form(false, 16, kAttendMinTilesNarrow);
-      e = launch_attend(a, (int)cache->head_dim, dtype, p.nb, false, st);
-    }
-    if (p.split && e == hipSuccess) e = launch_attend_join(j, (int)cache->head_dim, dtype, forms, st);
+    if (p.split && e == hipSuccess) e = launch_attend_join(j, dim, dtype, p.parts, st);
     return e;
   });
 }
