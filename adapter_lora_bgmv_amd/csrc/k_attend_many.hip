@@ -4,18 +4,18 @@
 // of k_attend.hip.  What differs is who converts: there every wave converts
 // the codes of the tile for its own columns, 128 conversions for 64 matrix
 // products, which cost as much as a third of the products.  Here a workgroup
-// is eight waves of 32 columns, each converts an eighth of the tile (a 16-token
-// group of K or of V, loaded straight into registers) and puts it into LDS as
-// bf16 or f16 times the page's scale, once, and all of them read finished
-// operands.  A tile costs a wave 16 conversions for its 64 products, 32
+// is eight waves of 32 columns, each converts an eighth of the tile (halves of
+// a 16-token group of K and of V, loaded straight into registers) and puts it
+// into LDS as bf16 or f16 times the page's scale, once, and all of them read
+// finished operands.  A tile costs a wave 16 conversions for its 64 products, 32
 // exponentials, and 32 LDS reads of 16 bytes a lane, about half of what the
 // LDS can give.
 //
 // The matrix products take longer than all else together, and hide it where
 // one wave alternates them: a step is one operand against both column blocks,
-// with a share of the other work between.  The next tile's scores run among
-// this tile's weights, so K is kept a tile ahead of V: while a tile is worked
-// on, waves 0-3 convert K two tiles ahead and waves 4-7 V one ahead.
+// with a share of the other work between: the next tile's scores run among
+// this tile's weights, and the sums among the conversions of K two tiles ahead
+// and of V one ahead.
 //
 // In LDS a fragment's 16 rows of 16 bytes lie side by side, so that reads and
 // writes are free of bank conflicts.  K: [4 quads j][D/16 chunks c][half s]
@@ -34,7 +34,7 @@ template <int D>
 struct ManyLds {
   static constexpr int kKeys = 8 * D, kValues = 8 * D;  // 16-byte units of a tile
   uint4 k[3][kKeys], v[2][kValues];
-  int info[2][4];  // of the groups of a tile of V: bit 0 it has a page, bit 1 NaN codes, from bit 8 on 256 + rest
+  int info[2][4][2];  // of the groups of a tile, by the halves of V: bit 0 it has a page, bit 1 NaN codes, from bit 8 on 256 + rest
 };
 
 template <int D>
@@ -66,6 +66,15 @@ struct ManyColumns {
     }
   }
 
+  // Waits for q here rather than at its first use, which is in the loop and
+  // would wait for what is on its way there.
+  __device__ __forceinline__ void arrive() {
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+      for (int s = 0; s < NS; ++s) asm volatile("" : "+v"(q[nb][s].x), "+v"(q[nb][s].y), "+v"(q[nb][s].z), "+v"(q[nb][s].w));
+  }
+
   static __device__ __forceinline__ float largest(const f32x4 (&s)[4]) {
     float mx = s[0][0];
 #pragma unroll
@@ -76,15 +85,19 @@ struct ManyColumns {
   }
   static __device__ __forceinline__ uint32_t &word(uint4 &v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
 
-  // Fragment f of a tile's keys, f = (j D/64 + n) 2 + s: quad j, chunks 4 n + g, half s; of its values, f = 2 dt + s.
-  static __device__ __forceinline__ uint4 key(const uint4 *k, int f) {
-    const int s = f & 1, n = (f >> 1) % (D / 64), j = (f >> 1) / (D / 64);
-    return k[((j * (D / 16) + 4 * n) * 2 + s) * 16];
-  }
-  static __device__ __forceinline__ uint4 value(const uint4 *v, int f) { return v[(f & 1) * D + (f >> 1) * 16]; }
+  // Fragment f of a tile's keys: two quads in turn over all parts (chunks 4 n +
+  // g and half s, 2 n + s), then the other two, so that no sum is added to
+  // twice in a row and the scores before make room for those after; of its
+  // values, 16 dims dt and half s.
   static constexpr int kKeyFrags = 8 * (D / 64), kValueFrags = 2 * ND;
-  static __device__ __forceinline__ int quad_of(int f) { return (f >> 1) / (D / 64); }
-  static __device__ __forceinline__ int part_of(int f) { return 2 * ((f >> 1) % (D / 64)) + (f & 1); }
+  static __device__ __forceinline__ int quad_of(int f) { return f / (kKeyFrags / 2) * 2 + f % 2; }
+  static __device__ __forceinline__ int part_of(int f) { return f % (kKeyFrags / 2) / 2; }
+  static __device__ __forceinline__ int dims_of(int f) { return f / 4 * 2 + f % 2; }
+  static __device__ __forceinline__ int half_of(int f) { return f / 2 % 2; }
+  static __device__ __forceinline__ uint4 key(const uint4 *k, int f) {
+    return k[((quad_of(f) * (D / 16) + part_of(f) / 2 * 4) * 2 + part_of(f) % 2) * 16];
+  }
+  static __device__ __forceinline__ uint4 value(const uint4 *v, int f) { return v[half_of(f) * D + dims_of(f) * 16]; }
 
   __device__ __forceinline__ void score(const uint4 *k) {
 #pragma unroll
@@ -103,8 +116,10 @@ struct ManyColumns {
   // unusual in it, from S and values v; false, and nothing changed, where the
   // maximum has to move.  Afterwards S holds the scores of the next tile's
   // keys (after the last tile: of whatever lies there).
-  __device__ __forceinline__ bool plain(float cs, const uint4 *v, const uint4 *next) {
-    constexpr int kAhead = 3;  // fragments on their way from LDS
+  // side(k), k < kValueFrags, is other work for the vector unit.
+  template <typename Side>
+  __device__ __forceinline__ bool plain(float cs, const uint4 *v, const uint4 *next, Side side) {
+    constexpr int kAhead = 6;  // fragments on their way from LDS: a step is 33 cycles, a read 130 and more
     constexpr int kSteps = kKeyFrags, kEach = 16 / kSteps;
     uint4 x[kAhead];
 #pragma unroll
@@ -161,8 +176,9 @@ struct ManyColumns {
       __builtin_amdgcn_sched_barrier(0);
       uint4 &y = x[(kSteps + k) % kAhead];
 #pragma unroll
-      for (int nb = 0; nb < NB; ++nb) acc[nb][k >> 1] = mfma16_f16(y, pf[nb][k & 1], acc[nb][k >> 1]);
+      for (int nb = 0; nb < NB; ++nb) acc[nb][dims_of(k)] = mfma16_f16(y, pf[nb][half_of(k)], acc[nb][dims_of(k)]);
       if (k + kAhead < kValueFrags) y = value(v, k + kAhead);
+      side(k);
     }
     return true;
   }
@@ -210,7 +226,7 @@ struct ManyColumns {
     }
     if (__builtin_expect(!nans, 1)) {
 #pragma unroll
-      for (int f = 0; f < kValueFrags; ++f) acc[B0][f >> 1] = mfma16_f16(value(v, f), pf[f & 1], acc[B0][f >> 1]);
+      for (int f = 0; f < kValueFrags; ++f) acc[B0][dims_of(f)] = mfma16_f16(value(v, f), pf[half_of(f)], acc[B0][dims_of(f)]);
       return;
     }
     // NaN values would reach every column: they become zeros, and the columns
@@ -228,14 +244,14 @@ struct ManyColumns {
       uint32_t o[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const uint32_t m = see >> (8 * (f & 1) + 2 * e);
+        const uint32_t m = see >> (8 * half_of(f) + 2 * e);
         o[e] = (m & 1 ? 0x3c00u : 0u) | (m & 2 ? 0x3c000000u : 0u);
       }
       const f32x4 n = mfma16_f16(one, make_uint4(o[0], o[1], o[2], o[3]), f32x4{0.f, 0.f, 0.f, 0.f});
 #pragma unroll
       for (int e = 0; e < 4; ++e)
-        if (n[e] > 0.f) acc[B0][f >> 1][e] = __uint_as_float(0x7fc00000u);
-      acc[B0][f >> 1] = mfma16_f16(x, pf[f & 1], acc[B0][f >> 1]);
+        if (n[e] > 0.f) acc[B0][dims_of(f)][e] = __uint_as_float(0x7fc00000u);
+      acc[B0][dims_of(f)] = mfma16_f16(x, pf[half_of(f)], acc[B0][dims_of(f)]);
     }
   }
 };
@@ -273,87 +289,103 @@ __global__ __launch_bounds__(kManyThreads, 2) void attend_many_kernel(AttendArgs
   ManyColumns<D> cols;
   cols.load(a, w, h, c0, c1, r, g);
 
-  // This wave's share of the tiles: group q of K, `lead` = 2 tiles ahead, or of V, 1 ahead.
-  const bool keys = wave < 4;
-  const int mine = wave & 3, lead = keys ? 2 : 1;
-  const uint8_t *pool = keys ? a.kv.k : a.kv.v, *exps = keys ? a.kv.ke : a.kv.ve;
-  int first = ta - 64, group = 0, exp = 0;  // lane l's page of tile first + l
+  // This wave's share of the tiles: half of group `mine`, of K two tiles ahead and of V one.
+  constexpr int kLanes = D / 2;  // a 16-byte unit each: 16 dims of a token of K, 16 tokens of a dim of V
+  const int mine = wave >> 1, unit = (wave & 1) * kLanes + (lane & (kLanes - 1));
+  const bool works = kLanes == 64 || lane < kLanes;
+  const int c = (unit >> 2) % (D / 16), x = ((c >> 1) & 1) ^ ((c & 1) * 3);
+  const int to_k = ((unit >> 2) / (D / 16) * (D / 16) + c) * 32 + 4 * (mine ^ x) + (unit & 3), to_v = mine * 2 * D + unit;
+  int first = ta - 64, group = 0, ke = 0, ve = 0;  // lane l's page of tile first + l
   unsigned long long there = 0;
-  uint4 raw[U];
-  int raw_exp = 0;
-  bool raw_there = false;
-  auto fetch = [&](int t) {  // tile t's share, on its way
-    if (t >= tb) return;
-    if (t >= first + 64) {
-      first = t;
-      const int tok = (t + lane) * kTile + 16 * mine;
-      const int page = t + lane < tb && tok < cap ? page_of(a.kv, w.seq, tok >> a.kv.page_shift) : -1;
-      const size_t ph = page >= 0 ? (size_t)page * H + h : 0;
-      exp = exps[ph];
-      group = page >= 0 ? (int)((ph << (a.kv.page_shift - 4)) + ((tok & ((1 << a.kv.page_shift) - 1)) >> 4)) : 0;
-      there = __ballot(page >= 0);
-    }
-    const uint8_t *p = pool + (size_t)(unsigned)__builtin_amdgcn_readlane(group, t - first) * (16 * D) + lane * 16;
-#pragma unroll
-    for (int i = 0; i < U; ++i) raw[i] = ldg16(p + i * 1024);
-    raw_exp = __builtin_amdgcn_readlane(exp, t - first);
-    raw_there = there >> (t - first) & 1;
+  auto pages = [&](int t) {  // the pages of 64 tiles from t on
+    first = t;
+    const int tok = (t + lane) * kTile + 16 * mine;
+    const int page = t + lane < tb && tok < cap ? page_of(a.kv, w.seq, tok >> a.kv.page_shift) : -1;
+    const size_t ph = page >= 0 ? (size_t)page * H + h : 0;
+    ke = a.kv.ke[ph];
+    ve = a.kv.ve[ph];
+    group = page >= 0 ? (int)((ph << (a.kv.page_shift - 4)) + ((tok & ((1 << a.kv.page_shift) - 1)) >> 4)) : 0;
+    there = __ballot(page >= 0);
   };
-  auto convert = [&](int t) {  // what was fetched, into tile t's place
-    if (t >= tb) return;
-    const int i = t - ta;
-    if (keys) {
-      const float scale = scale_of(raw_exp);
-#pragma unroll
-      for (int n = 0; n < U; ++n) {
-        const int u = lane + 64 * n, c = (u >> 2) % (D / 16), j = (u >> 2) / (D / 16);
-        const int x = ((c >> 1) & 1) ^ ((c & 1) * 3);
-        uint4 *to = &lds.k[i % 3][(j * (D / 16) + c) * 32 + 4 * (mine ^ x) + (u & 3)];
-        to[0] = raw_there ? codes_bf16(raw[n].x, raw[n].y, scale) : z4();
-        to[16] = raw_there ? codes_bf16(raw[n].z, raw[n].w, scale) : z4();
-      }
-    } else {
-      using X = ValueExp<false>;
-      const int vc = min(max(raw_exp, X::kLo), X::kHi);
-      const float scale = scale_of(vc + X::kAdd);
-      uint32_t any = 0;
-#pragma unroll
-      for (int n = 0; n < U; ++n) {
-        uint4 *to = &lds.v[i & 1][mine * 2 * D + lane + 64 * n];
-        to[0] = raw_there ? codes_f16(raw[n].x, raw[n].y, scale) : z4();
-        to[D] = raw_there ? codes_f16(raw[n].z, raw[n].w, scale) : z4();
-        any |= has_nan(raw[n].x) | has_nan(raw[n].y) | has_nan(raw[n].z) | has_nan(raw[n].w);
-      }
-      const int nan = raw_there && __any((any & 0x80808080u) != 0) ? 2 : 0;
-      if (lane == 0) lds.info[i & 1][mine] = (int)raw_there | nan | (raw_there ? raw_exp - vc + 256 : 256) << 8;
-    }
+  // What is on its way: a unit of K of tile tk, of V of tile tv, and their exponents.  Past the last tile: it again.
+  uint4 raw_k, raw_v;
+  int exp_k, exp_v, rest_v;
+  uint32_t there_k, there_v;  // all ones, or 0 without a page
+  auto fetch_k = [&](int t) {
+    const int at = min(t, tb - 1) - first;
+    raw_k = ldg16(a.kv.k + (size_t)(unsigned)__builtin_amdgcn_readlane(group, at) * (16 * D) + unit * 16);
+    exp_k = __builtin_amdgcn_readlane(ke, at);
+    there_k = there >> at & 1 ? ~0u : 0u;
   };
-  fetch(ta);
-  convert(ta);
-  fetch(ta + 1);
-  if (keys) {
-    convert(ta + 1);
-    fetch(ta + 2);
-  }
+  auto fetch_v = [&](int t) {
+    const int at = min(t, tb - 1) - first;
+    raw_v = ldg16(a.kv.v + (size_t)(unsigned)__builtin_amdgcn_readlane(group, at) * (16 * D) + unit * 16);
+    const int e = __builtin_amdgcn_readlane(ve, at);
+    there_v = there >> at & 1 ? ~0u : 0u;
+    exp_v = there_v ? min(max(e, ValueExp<false>::kLo), ValueExp<false>::kHi) : 127;
+    rest_v = there_v ? e - exp_v : 0;
+  };
+  // The conversions in parts: half p of the unit of K into a place of three, of V into one of two.
+  auto put_k = [&](int place, int p) {
+    const uint32_t lo = (p ? raw_k.z : raw_k.x) & there_k, hi = (p ? raw_k.w : raw_k.y) & there_k;
+    const uint4 y = codes_bf16(lo, hi, scale_of(exp_k));
+    if (works) lds.k[place][to_k + 16 * p] = y;
+  };
+  auto put_v = [&](int place, int p) {
+    const uint32_t lo = (p ? raw_v.z : raw_v.x) & there_v, hi = (p ? raw_v.w : raw_v.y) & there_v;
+    const uint4 y = codes_f16(lo, hi, scale_of(exp_v + ValueExp<false>::kAdd));
+    if (works) lds.v[place][to_v + D * p] = y;
+  };
+  auto put_info = [&](int place) {
+    const uint32_t any = has_nan(raw_v.x) | has_nan(raw_v.y) | has_nan(raw_v.z) | has_nan(raw_v.w);
+    const int nan = __any((any & there_v & 0x80808080u) != 0) ? 2 : 0;
+    lds.info[place][mine][wave & 1] = (int)(there_v & 1) | nan | (rest_v + 256) << 8;  // the same from every lane
+  };
 
   int kb = 0;
+  if (ta < tb) {
+    pages(ta);
+    fetch_k(ta);
+    fetch_v(ta);
+    put_k(0, 0);
+    put_k(0, 1);
+    fetch_k(ta + 1);
+    put_v(0, 0);
+    put_v(0, 1);
+    put_info(0);
+    fetch_v(ta + 1);
+    put_k(1, 0);
+    put_k(1, 1);
+    fetch_k(ta + 2);
+    cols.arrive();
+  }
   for (int t = ta; t < tb; ++t) {
+    if (t + 3 >= first + 64) pages(t);
     __syncthreads();  // tile t's V and tile t + 1's K are there; nobody reads what is written next
-    const int i = t - ta, kn = kb == 2 ? 0 : kb + 1;
+    const int vb = (t - ta) & 1, kn = kb == 2 ? 0 : kb + 1, kw = kn == 2 ? 0 : kn + 1;
+    auto side = [&](int k) {  // tile t + 2's K, tile t + 1's V, and the fetches after them
+      if (k == 1) put_k(kw, 0);
+      if (k == 2) put_k(kw, 1);
+      if (k == 3) fetch_k(t + 3);
+      if (k == 4) put_v(vb ^ 1, 0);
+      if (k == 5) put_v(vb ^ 1, 1);
+      if (k == 6) put_info(vb ^ 1);
+      if (k == 7) fetch_v(t + 2);
+    };
+    bool done = false;
     if (t * kTile < wave_hi && (t + 1) * kTile > wave_lo) {
       const int again = lane_again(), r = again & 15, g = again >> 4, x = ((g >> 1) & 1) ^ ((g & 1) * 3);
       const int at_k = g * 32 + 4 * ((r >> 2) ^ x) + (r & 3);
-      const uint4 *v = &lds.v[i & 1][g * 2 * D + r];
-      const int info = lds.info[i & 1][g];
-      const bool usual = __all((info & ~2) == (1 | 256 << 8)), nans = __any(info & 2);
-      bool done = usual && !cols.mixed && t * kTile >= lo_all && (t + 1) * kTile <= hi_all;
-      if (__builtin_expect(done, 1)) {
+      const uint4 *v = &lds.v[vb][g * 2 * D + r];
+      const int info = lds.info[vb][g][0] | (lds.info[vb][g][1] & 2);
+      const bool usual = __all((info & ~2) == (1 | 256 << 8));
+      if (__builtin_expect(usual && !cols.mixed && t * kTile >= lo_all && (t + 1) * kTile <= hi_all, 1)) {
         if (!cols.ahead) cols.score(&lds.k[kb][at_k]);
-        done = cols.plain(a.scale, v, &lds.k[kn][at_k]);
-        cols.ahead = done;
+        done = cols.plain(a.scale, v, &lds.k[kn][at_k], side);
       }
+      cols.ahead = done;
       if (__builtin_expect(!done, 0)) {
-        cols.ahead = false;
+        const bool nans = __any(info & 2);
         if (!cols.mixed) {  // with no rest so far M and Ml move together
           cols.mixed = __any(info >> 8 != 256);
           cols.Ml[0] = cols.M[0];
@@ -364,8 +396,10 @@ __global__ __launch_bounds__(kManyThreads, 2) void attend_many_kernel(AttendArgs
         cols.template careful<1>(a.scale, t * kTile + 16 * g, info, nans, a.window, &lds.k[kb][at_k], v);
       }
     }
-    convert(t + lead);
-    fetch(t + lead + 1);
+    if (!done) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) side(k);
+    }
     kb = kn;
   }
 
