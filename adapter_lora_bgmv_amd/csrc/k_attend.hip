@@ -805,13 +805,14 @@ static void go(const AttendArgs &a, hipStream_t st) {
   hipLaunchKernelGGL((attend_kernel<D, NB, F32, WIDE>), dim3((unsigned)((a.per_head + blocks) * a.kv.H)), dim3(256), 0, st, a);
 }
 template <int D>
-static void go_dim(const AttendArgs &a, int dtype, bool wide, hipStream_t st) {
-  if (dtype == 0) wide ? go<D, 1, true, true>(a, st) : go<D, 1, true, false>(a, st);
-  else wide ? go<D, 1, false, true>(a, st) : go<D, 1, false, false>(a, st);
+static void go_dim(const AttendArgs &a, int dtype, AttendForm f, hipStream_t st) {
+  if (f == kNarrow) dtype == 0 ? go<D, 1, true, false>(a, st) : go<D, 1, false, false>(a, st);
+  else if (dtype == 0) go<D, 1, true, true>(a, st);
+  else if (f == kWide || D > 128) go<D, 1, false, true>(a, st);
+  else if constexpr (D <= 128) go<D, 2, false, true>(a, st);
 }
 hipError_t launch_attend(const AttendArgs &a, int dim, int dtype, AttendForm f, hipStream_t st) {
-  const bool wide = f == kWide;
-  dim == 64 ? go_dim<64>(a, dtype, wide, st) : dim == 128 ? go_dim<128>(a, dtype, wide, st) : go_dim<256>(a, dtype, wide, st);
+  dim == 64 ? go_dim<64>(a, dtype, f, st) : dim == 128 ? go_dim<128>(a, dtype, f, st) : go_dim<256>(a, dtype, f, st);
   return hipGetLastError();
 }
 

@@ -118,22 +118,21 @@ struct AttendArgs {
   float *part;            // their partial results
 };
 // The forms of the attention, by the columns (row, query head of the group)
-// that a sequence brings: narrow up to 16, wide above, and many, with units of
-// 256, where bf16 calls may bring more than 64.
-enum AttendForm { kNarrow, kWide, kMany };
-constexpr int kAttendNarrowCols = 16, kAttendWideCols = 64, kAttendManyCols = 256;
-constexpr int attend_cols(AttendForm f) { return f == kNarrow ? kAttendNarrowCols : f == kWide ? kAttendWideCols : kAttendManyCols; }
+// that a sequence brings: narrow up to 16, wide above (units of 64), and wider
+// (128) where bf16 calls of up to 128 dims may bring more than 64.
+enum AttendForm { kNarrow, kWide, kWider };
+constexpr int kAttendNarrowCols = 16, kAttendWideCols = 64;
+constexpr int attend_cols(AttendForm f) { return f == kNarrow ? kAttendNarrowCols : f == kWide ? kAttendWideCols : 128; }
 // Workgroups of a CU that a form's registers allow, those that a launch's
 // tiles are spread over (one round of the card), and the partial slots that
 // takes: a unit is split into nc > 1 chunks only where its tiles exceed a
 // chunk's, so the split units' chunks are fewer than twice as many.
-constexpr int attend_per_cu(int dim, bool f32, AttendForm f) { return f == kMany || (dim > 128 && (f32 || f == kNarrow)) ? 1 : 2; }
+constexpr int attend_per_cu(int dim, bool f32, AttendForm f) { return dim > 128 && (f32 || f == kNarrow) ? 1 : 2; }
 constexpr int attend_target(int dim, int dtype, AttendForm f) { return 256 * attend_per_cu(dim, dtype == 0, f); }
 constexpr int attend_slots(int dim, int dtype, AttendForm f) { return 2 * attend_target(dim, dtype, f); }
 // Tiles that are worth a chunk of their own.
 constexpr int attend_min_tiles(AttendForm f) { return f == kNarrow ? 16 : 4; }
 hipError_t launch_attend(const AttendArgs &a, int dim, int dtype, AttendForm f, hipStream_t st);
-hipError_t launch_attend_many(const AttendArgs &a, int dim, hipStream_t st);
 
 // The join of split units, of one or both forms.
 struct AttendJoin {

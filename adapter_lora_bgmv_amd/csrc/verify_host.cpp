@@ -100,10 +100,9 @@ int timed(const char *what, hipStream_t st, F launch) {
 
 // Which forms an attention call launches.  Sequences of up to
 // kAttendNarrowCols columns take the narrow form, longer ones the wide form
-// or, in bf16 calls whose rows may be many, the form for those.  max_rows
-// bounds every sequence's rows and with n also from below; where it leaves
-// one form, that form takes every sequence, so that a wrong bound costs time
-// only.
+// or its wider units.  max_rows bounds every sequence's rows and with n also
+// from below; where it leaves one form, that form takes every sequence, so
+// that a wrong bound costs time only.
 struct AttendPlan {
   struct Part {
     AttendForm form;
@@ -134,7 +133,7 @@ AttendPlan attend_plan(const lora_kv_cache *c, const lora_kv_seqs *s, int32_t dt
     p.split |= tiles > (uint64_t)attend_min_tiles(f);
   };
   const bool wide = most * G > (uint64_t)kAttendNarrowCols;
-  if (wide) add(dtype == LORA_BF16 && dim <= 128 && most * G > (uint64_t)kAttendWideCols ? kMany : kWide);
+  if (wide) add(dtype == LORA_BF16 && dim <= 128 && most * G > (uint64_t)kAttendWideCols ? kWider : kWide);
   if (!wide || least * G <= (uint64_t)kAttendNarrowCols) add(kNarrow);
   return p;
 }
@@ -241,7 +240,7 @@ int lora_kv_attend(const lora_kv_cache *cache, const lora_kv_seqs *seqs, int32_t
       a.cols_lo = p.parts > 1 && i == 0 ? kAttendNarrowCols : 0;
       a.cols_hi = i == 1 ? kAttendNarrowCols : INT_MAX;
       j.form[i] = {a.records, a.used, a.part, q.slots, attend_cols(q.form)};
-      e = q.form == kMany ? launch_attend_many(a, dim, st) : launch_attend(a, dim, dtype, q.form, st);
+      e = launch_attend(a, dim, dtype, q.form, st);
     }
     if (p.split && e == hipSuccess) e = launch_attend_join(j, dim, dtype, p.parts, st);
     return e;
