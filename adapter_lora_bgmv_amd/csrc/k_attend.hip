@@ -240,12 +240,6 @@ struct Columns {
         if (dt + 1 < ND) next = vf(dt + 1);
         add<0, NB>(dt, now, vs, pf);
       }
-    } else if constexpr (F32) {
-#pragma unroll
-      for (int nb = 0; nb < NB; ++nb) l[nb] += weigh(S[nb], cs, kTop - M[nb], pf[nb]);
-      score<0, NB>(S, scale, kf);
-#pragma unroll
-      for (int dt = 0; dt < ND; ++dt) add<0, NB>(dt, vf(dt), vs, pf);
     } else {
       // step k: a 32-dim half of a key fragment against every column block,
       // with kEach weights of each block and the conversion of the next half
@@ -452,7 +446,6 @@ struct Columns {
 template <int D>
 struct Stage {
   static constexpr int kPitch = 16 * D, kBytes = 8 * kPitch, kCount = D > 128 ? 2 : 4;
-  static constexpr bool kAhead = kCount == 4;  // a tile's scores are computed during the one before
   static constexpr int kDma = 2 * (D / 64);  // instructions of a wave (its group's K and V) a stage
 };
 
@@ -539,6 +532,7 @@ __global__ __launch_bounds__(256, attend_per_cu(D, F32, WIDE ? kWide : kNarrow))
   } else {
     using St = Stage<D>;
     constexpr int N = St::kCount;
+    constexpr bool kAhead = NB == 2;  // a tile's scores are computed during the one before
     const uint32_t base = lds_addr(smem);
     // wave k brings group k of the tile; lane l's unit is 4 c + l / 4 % 4 of 4 c .. 4 c + 3, c = 4 n + l / 16
     const int from_k = ((((lane >> 2) - wave) & 3) * (D / 16) + (lane >> 4)) * 64 + (lane & 3) * 16;
@@ -566,8 +560,7 @@ __global__ __launch_bounds__(256, attend_per_cu(D, F32, WIDE ? kWide : kNarrow))
     for (int t = ta; t < tb; ++t) {
       // this wave's part of the tile (of the next one too, where its keys are
       // read) is here, then everybody's; nobody reads the tile before any more
-      if (N == 4 && t + 2 < tb) wait_vmcnt<St::kDma>();
-      else wait_vmcnt<0>();
+      wait_stages<St::kDma, N - 2>(min(tb - 1 - t, N - 2) - kAhead);
       asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
       block_barrier();
       if (i == 16) {
@@ -590,11 +583,11 @@ __global__ __launch_bounds__(256, attend_per_cu(D, F32, WIDE ? kWide : kNarrow))
         bool done = info.whole(i, t, lo_all, hi_all);
         if (__builtin_expect(done, 1)) {
           if (!ahead) cols.template score<0, NB>(S, scale_of(pages.ke), kf);
-          if (St::kAhead && t + 1 < tb) {
+          if (kAhead && t + 1 < tb) {
             const char *np = smem + (stage == N - 1 ? 0 : stage + 1) * St::kBytes + (kp - smem - stage * St::kBytes);
             auto nf = [&](int j, int n) { return *(const uint4 *)(np + (((r >> 2) + j) & 3) * 64 + n * 1024); };
             const int nk = __shfl(i == 15 ? later.ke : info.ke, 4 * ((i + 1) & 15) + (r >> 2), 64);
-            done = cols.template plain<true>(S, pages, a.scale, vf, scale_of(nk), nf);
+            done = cols.template plain<kAhead>(S, pages, a.scale, vf, scale_of(nk), nf);
             ahead = done;
           } else {
             done = cols.template plain<false>(S, pages, a.scale, vf, 0.f, kf);
