@@ -34,13 +34,24 @@
 //
 // Two forms share the code.  Narrow (up to 16 columns a sequence: decode):
 // each wave of a workgroup takes every fourth tile straight into registers,
-// and the four are joined through LDS.  Wide (more columns): the waves take
-// 16 NB columns each and share the tiles, which LDS-DMA brings in up to two
-// ahead.  In both, the call's tiles are shared out in chunks of equal length
-// over about one round of workgroups, from the lengths in device memory, so
-// long and short sequences balance; a unit (sequence, head, columns) of
-// several chunks leaves its sums in the workspace, and a second kernel joins
-// them.
+// and the four are joined through LDS; a decode batch is bound by HBM (64 rows
+// over 1 to 8192 tokens: 111 us, 4.8 TB/s), one row by latency (701 tokens:
+// 7.7 us).  Wide (more columns): the waves take 16 NB columns each and share
+// the tiles, which LDS-DMA brings in two or three ahead.  With two blocks a
+// wave it is bound by issue: 62 products and 313 other vector instructions a
+// tile (1024 rows over 16 000 tokens: 913 TFLOP/s, matrix unit busy 36 %).
+// Two blocks instead of one halve the conversions a product; three do not fit
+// the registers of two waves a SIMD.
+//
+// The call's tiles are shared out in chunks of equal length over about one
+// round of workgroups, from the lengths in device memory, so long and short
+// sequences balance; a unit (sequence, head, columns) of several chunks leaves
+// its sums in the workspace, and a second kernel joins them (5 us; the last
+// workgroup to arrive took 20 us for 16 chunks of 36 columns, alone).
+//
+// What is rare (masks, missing pages, maxima that moved, NaN codes, rests) is
+// kept out of the main loop, and in the wide form takes one block after the
+// other: inside, it costs copies of all sums and spills, 15 % and more.
 #include <algorithm>
 
 #include "attend.hpp"

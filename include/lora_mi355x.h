@@ -443,8 +443,7 @@ typedef struct lora_kv_cache {
  * page_tokens name no page: such a token is not written, not read back, and
  * seen by no row.  A negative kv_len counts as 0.  Row ranges that leave
  * [0, n) or decrease never make a call touch memory outside its operands,
- * but which rows are processed is then unspecified, and a workspace must be
- * zero-filled again.
+ * but which rows are processed is then unspecified.
  * max_rows is a bound [host] on every sequence's rows (0: none known): it
  * chooses kernels and never changes which rows are processed.
  */
@@ -499,8 +498,8 @@ int lora_kv_read(const lora_kv_cache *cache, const lora_kv_seqs *seqs, int32_t d
  * product with v); out is rounded once.  The order of every sum follows from
  * the call's lengths alone.  workspace [dev] of at least
  * lora_kv_attend_workspace_bytes(...) bytes (a function of the head counts
- * and sizes, dtype, n, n_seqs and max_rows), zero-filled before its first
- * use with these.
+ * and sizes, dtype, n, n_seqs, the page table's width and max_rows), of any
+ * content; calls that may run at the same time need one each.
  */
 size_t lora_kv_attend_workspace_bytes(const lora_kv_cache *cache, const lora_kv_seqs *seqs, int32_t dtype,
                                       uint32_t n_heads, uint32_t n);
