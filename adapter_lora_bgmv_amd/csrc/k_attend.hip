@@ -70,11 +70,11 @@ struct PageInfo {
   unsigned long long there;  // a bit a lane: it has a page
   // The lane's page of the tiles from `tile` to `end`, or -1; then what is known of it.
   static __device__ __forceinline__ int page(const KvDev &kv, int seq, int tile, int step, int end, int lane) {
-    const int t = tile + (lane >> 2) * step, tok = t * kTile + 16 * (lane & 3);
+    const int t = tile + (lane >> 2) * step, tok = (int)((unsigned)t * kTile) + 16 * (lane & 3);
     return t < end && tok < kv_cap(kv) ? page_of(kv, seq, tok >> kv.page_shift) : -1;
   }
   __device__ __forceinline__ void set(const KvDev &kv, int h, int page, int tile, int step, int lane) {
-    const int tok = (tile + (lane >> 2) * step) * kTile + 16 * (lane & 3);
+    const int tok = (int)((unsigned)(tile + (lane >> 2) * step) * kTile) + 16 * (lane & 3);
     const size_t ph = page >= 0 ? (size_t)page * kv.H + h : 0;
     ke = kv.ke[ph];
     ve = kv.ve[ph];
@@ -555,9 +555,11 @@ __global__ __launch_bounds__(256, attend_per_cu(D, F32, WIDE ? kWide : kNarrow))
 #pragma unroll
       for (int n = 0; n < D / 64; ++n) dma16(a.kv.v + at + lane * 16 + n * 1024, to + 4 * St::kPitch + n * 1024);
     };
+    // the page table's round trip beside q's
+    const int page = PageInfo::page(a.kv, w.seq, ta, 1, tb, lane);
     cols.load(a, w, h, c0, c1, r, g);
-    info.load(a.kv, w.seq, h, ta, 1, tb, lane);
     cols.arrive();
+    info.set(a.kv, h, page, ta, 1, lane);
 #pragma unroll
     for (int k = 0; k < N - 1; ++k)
       if (ta + k < tb) bring(info.group, k, k);
@@ -806,7 +808,9 @@ static void go(const AttendArgs &a, hipStream_t st) {
   constexpr int CB = (WIDE ? 64 : 16) * NB;
   const int s = a.kv.n < a.kv.n_seqs ? a.kv.n : a.kv.n_seqs;
   const long long blocks = s + ((long long)a.kv.n * a.G.d - s) / CB;  // sum of ceil(cols / CB) over s sequences at most
-  hipLaunchKernelGGL((attend_kernel<D, NB, F32, WIDE>), dim3((unsigned)((a.per_head + blocks) * a.kv.H)), dim3(256), 0, st, a);
+  // without splits there is a chunk a unit; a narrow launch of few units is
+  // faster with idle workgroups beside them (7.7 us for 8.2 with 512 beside 8)
+  hipLaunchKernelGGL((attend_kernel<D, NB, F32, WIDE>), dim3((unsigned)(((a.split || !WIDE ? a.per_head : 0) + blocks) * a.kv.H)), dim3(256), 0, st, a);
 }
 template <int D>
 static void go_dim(const AttendArgs &a, int dtype, AttendForm f, hipStream_t st) {

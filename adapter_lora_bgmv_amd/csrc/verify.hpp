@@ -113,6 +113,7 @@ struct AttendArgs {
   int cols_lo, cols_hi;  // takes the sequences whose rows x G lie in (cols_lo, cols_hi]
   int per_head;   // workgroups per key/value head that the tiles are spread over
   int min_tiles;  // of a chunk: fewer are not split
+  bool split;     // a unit may have more than that
   AttendRecord *records;  // of split units' chunks
   int *used;              // slots in use, written by the call
   float *part;            // their partial results
@@ -130,8 +131,11 @@ constexpr int attend_cols(AttendForm f) { return f == kNarrow ? kAttendNarrowCol
 constexpr int attend_per_cu(int dim, bool f32, AttendForm f) { return dim > 128 && (f32 || f == kNarrow) ? 1 : 2; }
 constexpr int attend_target(int dim, int dtype, AttendForm f) { return 256 * attend_per_cu(dim, dtype == 0, f); }
 constexpr int attend_slots(int dim, int dtype, AttendForm f) { return 2 * attend_target(dim, dtype, f); }
-// Tiles that are worth a chunk of their own.
-constexpr int attend_min_tiles(AttendForm f) { return f == kNarrow ? 16 : 4; }
+// Tiles that are worth a chunk of their own: four a wave of the narrow form,
+// where fewer cost more in start and join than they save; four of the wide
+// form, whose workgroups wait for memory; eight of the wider, which compute
+// (8 prompts of 512 rows: 52 us split at four and joined, 45 whole).
+constexpr int attend_min_tiles(AttendForm f) { return f == kNarrow ? 16 : f == kWide ? 4 : 8; }
 hipError_t launch_attend(const AttendArgs &a, int dim, int dtype, AttendForm f, hipStream_t st);
 
 // The join of split units, of one or both forms.

@@ -108,9 +108,10 @@ struct AttendPlan {
     AttendForm form;
     size_t records, sums;  // offsets in the workspace, after a place for the slots in use
     int slots;
+    bool split;  // a unit may be cut into chunks
   } part[2];
   int parts;
-  bool split;  // a unit may be cut into chunks
+  bool split;  // of either
   size_t total;
 };
 AttendPlan attend_plan(const lora_kv_cache *c, const lora_kv_seqs *s, int32_t dtype, uint32_t n_heads, uint32_t n) {
@@ -130,7 +131,8 @@ AttendPlan attend_plan(const lora_kv_cache *c, const lora_kv_seqs *s, int32_t dt
     q.records = p.total;
     q.sums = q.records + up256(q.slots * sizeof(AttendRecord));
     p.total = q.sums + up256((size_t)q.slots * attend_cols(f) * (dim + 3) * 4);
-    p.split |= tiles > (uint64_t)attend_min_tiles(f);
+    q.split = tiles > (uint64_t)attend_min_tiles(f);
+    p.split |= q.split;
   };
   const bool wide = most * G > (uint64_t)kAttendNarrowCols;
   if (wide) add(dtype == LORA_BF16 && dim <= 128 && most * G > (uint64_t)kAttendWideCols ? kWider : kWide);
@@ -236,6 +238,7 @@ int lora_kv_attend(const lora_kv_cache *cache, const lora_kv_seqs *seqs, int32_t
       a.records = (AttendRecord *)(ws + q.records);
       a.part = (float *)(ws + q.sums);
       a.min_tiles = attend_min_tiles(q.form);
+      a.split = q.split;
       a.per_head = std::max(1, attend_target(dim, dtype, q.form) / a.kv.H);
       a.cols_lo = p.parts > 1 && i == 0 ? kAttendNarrowCols : 0;
       a.cols_hi = i == 1 ? kAttendNarrowCols : INT_MAX;
