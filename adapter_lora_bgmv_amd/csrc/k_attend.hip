@@ -426,6 +426,37 @@ struct Columns {
     for (int nb = 0; nb < NB; ++nb) Ml[nb] = M[nb];
   }
 
+  // q as operands in LDS, the lane's [NS][NT] in steps of 64, and the scores
+  // from there: the 12 D / 32 registers of three terms are wanted for tiles on
+  // their way (f32, 256 dims: without this the loop spills, and every reload
+  // waits for those tiles).
+  __device__ __forceinline__ void keep(uint4 *mine) const {
+#pragma unroll
+    for (int s = 0; s < NS; ++s)
+#pragma unroll
+      for (int t = 0; t < NT; ++t) mine[(s * NT + t) * 64] = q[0][s][t];
+  }
+  template <typename K>
+  static __device__ __forceinline__ void score_kept(f32x4 (&S)[1][4], float scale, const uint4 *mine, K kf) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) S[0][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int s = 0; s < NS; ++s) {
+      uint4 kk[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint4 x = kf(j, s / 2);
+        kk[j] = s & 1 ? codes_bf16(x.z, x.w, scale) : codes_bf16(x.x, x.y, scale);
+      }
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        const uint4 y = mine[(s * NT + NT - 1 - t) * 64];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) S[0][j] = mfma16(kk[j], y, S[0][j]);
+      }
+    }
+  }
+
   // Waits for q here rather than at its first use, which is in the loop.
   __device__ __forceinline__ void arrive() {
 #pragma unroll
@@ -500,7 +531,10 @@ __global__ __launch_bounds__(256, attend_per_cu(D, F32, WIDE ? kWide : kNarrow))
   PageInfo info;
 
   if constexpr (!WIDE) {
+    constexpr bool kKeep = F32 && D > 64;
+    __shared__ uint4 kept[kKeep ? D / 32 * 3 * 64 : 1];  // the waves' columns are the same
     cols.load(a, w, h, c0, c1, r, g);
+    if constexpr (kKeep) cols.keep(kept + lane);
     info.load(a.kv, w.seq, h, ta + wave, 4, tb, lane);
     uint4 kr[4][D / 64], vr[ND];
     auto load_k = [&](int i) {
@@ -526,7 +560,8 @@ __global__ __launch_bounds__(256, attend_per_cu(D, F32, WIDE ? kWide : kNarrow))
       const PageInfo::Tile pages = info.tile(i, r, g);
       const bool whole = info.whole(i, t, lo_all, hi_all);
       f32x4 S[1][4];
-      cols.template score<0, 1>(S, scale_of(pages.ke), kf);
+      if constexpr (kKeep) cols.score_kept(S, scale_of(pages.ke), kept + lane, kf);
+      else cols.template score<0, 1>(S, scale_of(pages.ke), kf);
       if (t + 4 < tb) {
         if (++i == 16) {
           info.load(a.kv, w.seq, h, t + 4, 4, tb, lane);
