@@ -207,8 +207,7 @@ __global__ __launch_bounds__(kKvThreads) void kv_write_kernel(KvDev a, const T *
     for (int i = 0; i < 4; ++i)
 #pragma unroll
       for (int e = 0; e < 4; ++e) big = max(big, finite_bits(x[j][i].at(e)));
-#pragma unroll
-  for (int off = 32; off > 0; off >>= 1) big = max(big, (uint32_t)__shfl_xor((int)big, off, 64));
+  big = (uint32_t)wave_reduce((int)big, 0, [](int a, int b) { return max(a, b); });  // bits of finite numbers: no sign
   if (lane == 0) wave_max[tid >> 6] = big;
   __syncthreads();
 #pragma unroll

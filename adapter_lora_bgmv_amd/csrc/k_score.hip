@@ -73,14 +73,11 @@ struct Vec<u16> {
 };
 
 __device__ __forceinline__ float wave_sum(float v) {
-#pragma unroll
-  for (int off = 32; off > 0; off >>= 1) v += __shfl_xor(v, off, 64);
-  return v;
+  return __int_as_float(wave_reduce(__float_as_int(v), 0, [](int a, int b) { return __float_as_int(__int_as_float(a) + __int_as_float(b)); }));
 }
 __device__ __forceinline__ float wave_max(float v) {
-#pragma unroll
-  for (int off = 32; off > 0; off >>= 1) v = fmaxf(v, __shfl_xor(v, off, 64));
-  return v;
+  return __int_as_float(wave_reduce(__float_as_int(v), (int)0xff800000u,
+                                    [](int a, int b) { return __float_as_int(fmaxf(__int_as_float(a), __int_as_float(b))); }));
 }
 
 // A lower bound of the k-th largest of the wave's 64 keys: its upper 16 bits.
@@ -378,9 +375,7 @@ __global__ __launch_bounds__(kScoreThreads) void score_kernel(ScoreArgs a) {
   const float f2 = r[0] == -INFINITY && r[1] == 0.f ? 0.f : __builtin_amdgcn_exp2f(by);
   s = wave_sum(r[1] * f2);
   sx = wave_sum((r[2] + (f2 == 0.f ? 0.f : r[1] * by)) * f2);
-  above = __float_as_int(r[3]);
-#pragma unroll
-  for (int off = 32; off > 0; off >>= 1) above += __shfl_xor(above, off, 64);
+  above = wave_reduce(__float_as_int(r[3]), 0, [](int a, int b) { return a + b; });
   __syncthreads();
   if (lane == 0) {
     lds.s[wave] = s;

@@ -60,6 +60,17 @@ __device__ __forceinline__ int wave_incl_scan(int v) {
   v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xc, 0xf, false);  // row_bcast:31
   return v;
 }
+// Over the whole wave, the same way: f(v, what the other lane has, or `none`), lane 63's at the end.
+template <typename F>
+__device__ __forceinline__ int wave_reduce(int v, int none, F f) {
+  v = f(v, __builtin_amdgcn_update_dpp(none, v, 0x111, 0xf, 0xf, false));
+  v = f(v, __builtin_amdgcn_update_dpp(none, v, 0x112, 0xf, 0xf, false));
+  v = f(v, __builtin_amdgcn_update_dpp(none, v, 0x114, 0xf, 0xf, false));
+  v = f(v, __builtin_amdgcn_update_dpp(none, v, 0x118, 0xf, 0xf, false));
+  v = f(v, __builtin_amdgcn_update_dpp(none, v, 0x142, 0xa, 0xf, false));
+  v = f(v, __builtin_amdgcn_update_dpp(none, v, 0x143, 0xc, 0xf, false));
+  return __builtin_amdgcn_readlane(v, 63);
+}
 __device__ __forceinline__ SeqDev seq_of_lane(const SeqDev &s, int lane) {
   return {__builtin_amdgcn_readlane(s.row0, lane), __builtin_amdgcn_readlane(s.rows, lane),
           __builtin_amdgcn_readlane(s.len, lane), __builtin_amdgcn_readlane(s.start, lane)};
