@@ -28,9 +28,9 @@
 // A row of several chunks leaves a record of each in the workspace; the last
 // chunk to arrive joins them, the lists by the same selection.
 //
-// HBM bounds large calls (4096 rows of 32000 bf16 logits: 59 us, 4.5 TB/s) and
+// HBM bounds large calls (4096 rows of 32000 bf16 logits: 58 us, 4.5 TB/s) and
 // the exponentials and compares follow closely, 14 vector instructions a
-// logit; latency bounds small ones (36 rows of 131071: 19 us).
+// logit; latency bounds small ones (36 rows of 131071: 18 us).
 #include <algorithm>
 
 #include "common.hpp"

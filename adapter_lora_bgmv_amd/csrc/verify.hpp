@@ -136,16 +136,26 @@ enum AttendForm { kNarrow, kWide, kWider };
 constexpr int kAttendNarrowCols = 16, kAttendWideCols = 64;
 constexpr int attend_cols(AttendForm f) { return f == kNarrow ? kAttendNarrowCols : f == kWide ? kAttendWideCols : 128; }
 // Workgroups of a CU that a form's registers allow, those that a launch's
-// tiles are spread over (one round of the card), and the partial slots that
-// takes: a unit is split into nc > 1 chunks only where its tiles exceed a
-// chunk's, so the split units' chunks are fewer than twice as many.
+// tiles are spread over, and the partial slots that takes: a unit is split
+// into nc > 1 chunks only where its tiles exceed a chunk's, so the split
+// units' chunks are fewer than twice as many. The tiles are spread over one
+// round of the card, and over three quarters of one in the narrow form with
+// two workgroups a CU: its units round up to whole chunks, which at a full
+// round leaves a few of them to a second (8 sequences of up to 30000: 63.5 us
+// over 512, 58.2 over 384, 61.3 over 320, 67.8 over 256; 16 of up to 8000:
+// 32.2, 29.0, 29.8, 32.0; 64 of up to 8191 and calls of many short ones: the
+// same within 3 % either way). The wide form loses by it (4 of 9 rows: 25.1
+// us over a full round, 26.8 over three quarters), the others do not change.
 constexpr int attend_per_cu(int dim, bool f32, AttendForm f) { return dim > 128 && (f32 || f == kNarrow) ? 1 : 2; }
-constexpr int attend_target(int dim, int dtype, AttendForm f) { return 256 * attend_per_cu(dim, dtype == 0, f); }
+constexpr int attend_target(int dim, int dtype, AttendForm f) {
+  const int per_cu = attend_per_cu(dim, dtype == 0, f);
+  return f == kNarrow && per_cu == 2 ? 384 : 256 * per_cu;
+}
 constexpr int attend_slots(int dim, int dtype, AttendForm f) { return 2 * attend_target(dim, dtype, f); }
 // Tiles that are worth a chunk of their own: four a wave of the narrow form,
 // where fewer cost more in start and join than they save; four of the wide
 // form, whose workgroups wait for memory; eight of the wider, which compute
-// (8 prompts of 512 rows: 52 us split at four and joined, 45 whole).
+// (8 prompts of 512 rows: 51.6 us split at four and joined, 49.1 whole).
 constexpr int attend_min_tiles(AttendForm f) { return f == kNarrow ? 16 : f == kWide ? 4 : 8; }
 hipError_t launch_attend(const AttendArgs &a, int dim, int dtype, AttendForm f, hipStream_t st);
 
