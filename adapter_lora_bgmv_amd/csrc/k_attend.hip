@@ -844,7 +844,7 @@ static void go(const AttendArgs &a, hipStream_t st) {
   const int s = a.kv.n < a.kv.n_seqs ? a.kv.n : a.kv.n_seqs;
   const long long blocks = s + ((long long)a.kv.n * a.G.d - s) / CB;  // sum of ceil(cols / CB) over s sequences at most
   // without splits there is a chunk a unit; a narrow launch of few units is
-  // faster with idle workgroups beside them (7.7 us for 8.2 with 512 beside 8)
+  // faster with idle workgroups beside them (7.7 us for 8.2 with 384 beside 8)
   hipLaunchKernelGGL((attend_kernel<D, NB, F32, WIDE>), dim3((unsigned)(((a.split || !WIDE ? a.per_head : 0) + blocks) * a.kv.H)), dim3(256), 0, st, a);
 }
 template <int D>
