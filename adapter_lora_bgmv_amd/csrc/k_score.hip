@@ -30,7 +30,7 @@
 //
 // HBM bounds large calls (4096 rows of 32000 bf16 logits: 58 us, 4.5 TB/s) and
 // the exponentials and compares follow closely, 14 vector instructions a
-// logit; latency bounds small ones (36 rows of 131071: 18 us).
+// logit; latency bounds small ones (36 rows of 131071: 17 us).
 #include <algorithm>
 
 #include "common.hpp"
@@ -406,12 +406,15 @@ __global__ __launch_bounds__(kScoreThreads) void score_kernel(ScoreArgs a) {
 
 // ---------------------------------------------------------------- launcher
 // Workgroups of a row, and the batches each takes: one where the rows alone
-// make about four workgroups a CU, otherwise as many as make that, down to a
-// batch each.
+// make two workgroups a CU, otherwise as many as make that, down to a batch
+// each.  Four a CU fit and do not pay, as each has a selection and a share of
+// the join: 64 rows of 128256 13.8 us for 16.2 with four, 700 of 32000 15.9
+// for 24.3, 1000 of 128256 52.7 for 60.2, 36 of 131071 17.4 for 18.1; the
+// other way round 200 of 128256 27.7 for 26.9 and 600 43.8 for 42.0.
 ScoreSplit score_split(int n, int n_vocab, int dtype) {
   const int ve = dtype == 0 ? 4 : 8, batch = kScoreThreads * kScoreBatch;
   const int all = (n_vocab + ve - 1 + batch - 1) / batch;  // a row may begin up to ve - 1 elements into its first vector
-  const int want = std::min(all, (1024 + n - 1) / n);
+  const int want = std::min(all, (512 + n - 1) / n);
   ScoreSplit r;
   r.batches = (all + want - 1) / want;
   r.chunks = (all + r.batches - 1) / r.batches;
