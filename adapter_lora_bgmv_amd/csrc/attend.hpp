@@ -126,19 +126,24 @@ __device__ __forceinline__ int unit_tiles(const AttendArgs &a, const SeqDev &s, 
 }
 
 // Item u of a head's list: units in order, each with its chunks.  Every wave
-// finds it by itself (lane l counts `per` sequences).  *slots: of a head's
-// split units together.
+// finds it by itself (lane l counts `per` sequences).  *all_slots: of a head's
+// split units together.  The launch and the workspace have room for the items
+// and slots of ranges that do not overlap.  A range begins where the one
+// before ends, so they do as soon as one falls: such a call has no work.
 template <int CB>
 __device__ __forceinline__ bool find_work(const AttendArgs &a, int u, int lane, Work *w, int *all_slots) {
   const int per = (a.kv.n_seqs + 63) >> 6, cap = kv_cap(a.kv);
   const int i0 = lane * per, i1 = min(i0 + per, a.kv.n_seqs);
   SeqDev first = {0, 0, 0, 0};  // the lane's only sequence where per is 1
-  if (i0 < i1) first = load_seq(a.kv, i0);
+  bool falls = false;
+  if (i0 < i1) first = load_seq(a.kv, i0, &falls);
   long long total = 0;
   for (int i = i0; i < i1; ++i) {
-    const SeqDev s = i == i0 ? first : load_seq(a.kv, i);
+    const SeqDev s = i == i0 ? first : load_seq(a.kv, i, &falls);
     total += (long long)seq_blocks<CB>(a, s) * unit_tiles<CB>(a, s, cap);
   }
+  *all_slots = 0;
+  if (__any(falls)) return false;
   // over the lanes in two parts of 24 and up to 32 bits
   total = min(total, 1ll << 50);
   const unsigned low = (unsigned)__builtin_amdgcn_readlane(wave_incl_scan((int)(total & 0xffffff)), 63);

@@ -28,11 +28,14 @@ struct SeqDev {
   int row0, rows, len, start;
 };
 
-__device__ __forceinline__ SeqDev load_seq(const KvDev &a, int i) {
+// *falls is set where the range ends before it begins.
+__device__ __forceinline__ SeqDev load_seq(const KvDev &a, int i, bool *falls = nullptr) {
   const int lo = a.indptr[i], hi = a.indptr[i + 1], len = a.kv_len[i];
   SeqDev s;
   s.row0 = min(max(lo, 0), a.n);
-  s.rows = max(min(max(hi, 0), a.n) - s.row0, 0);
+  const int rows = min(max(hi, 0), a.n) - s.row0;
+  if (falls) *falls |= rows < 0;
+  s.rows = max(rows, 0);
   s.len = max(len, 0);
   s.start = s.len - s.rows;
   return s;

@@ -1,0 +1,76 @@
+"""Edges of the verify-step operators' contracts: row ranges that decrease or
+leave the call, the ends of the size ranges, unusual numbers, other streams."""
+import numpy as np
+import pytest
+
+import verify_ref as R
+from adapter_lora_bgmv_amd import binding as B
+from test_gpu_verify import DT, Setup, dev, host
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    B.lora_init()
+
+
+# ---------------------------------------------------------------- row ranges
+RANGES = [
+    # row_indptr (repeated to the sequences), n
+    ("falls", lambda S: [0, 16] * (S // 2) + [0], 16),
+    ("falls once, long ones overlapping", lambda S: [0] * (S - 3) + [16, 0, 16, 0], 16),
+    ("leaves [0, n)", lambda S: [-7] + list(range(-3, S - 4)) + [2 ** 31 - 1], 20),
+    ("falls outside [0, n)", lambda S: [-3, -9] * (S // 2) + [2 ** 31 - 1], 16),
+]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("name,make,n", RANGES)
+def test_row_ranges_that_fall_or_leave_the_call(name, make, n, dtype):
+    """Sequences short and long, some of them split: whatever the ranges, nothing
+    outside the operands changes, and a workspace full of a larger call's leavings is
+    no way out of them.  Ranges that only leave [0, n) serve the rows inside it."""
+    S, H, G, D, P = 64, 2, 2, 64, 16
+    heads = H * G
+    s = Setup(400, [(1, 60)] * (S - 2) + [(1, 6000)] * 2, H, D, P)
+    code = DT[dtype][0]
+    tdt = getattr(torch, DT[dtype][1])
+    # the larger call that the workspace remembers
+    big = Setup(401, [(200, 5000), (190, 3000), (3, 8000)], H, D, P)
+    for max_rows in (1, 0):
+        seqs = B.KVSeqs(dev(s.seqs["table"]), dev(np.array(make(S), np.int32)), dev(s.seqs["kv_len"]), max_rows=max_rows)
+        need = B.lora_kv_attend_workspace_bytes(s.cache, seqs, code, heads, n)
+        ws = torch.zeros(max(need, B.lora_kv_attend_workspace_bytes(big.cache, big.dseqs, code, heads, big.n)), dtype=torch.uint8,
+                         device="cuda")
+        big.attend(dtype, heads, ws=ws)
+        row, pad = heads * D, 64
+        q = torch.randn(n, row, device="cuda").to(tdt)
+        box = torch.full((pad + n + pad, row), 33.0, dtype=tdt, device="cuda")
+        lbox = torch.full((pad + n + pad, heads), 33.0, device="cuda")
+        B.lora_kv_attend(s.cache, seqs, code, heads, q, row, 0.125, 0, n, box[pad:], row, lbox[pad:], ws, ws.numel())
+        torch.cuda.synchronize()
+        for t in (box, lbox):
+            assert bool((t[:pad] == 33).all()) and bool((t[pad + n:] == 33).all())
+        if name == "leaves [0, n)":  # a row a sequence
+            want, wl, mag, big_, toks = R.attend(s.host, {**s.seqs, "indptr": np.clip(make(S), 0, n)},
+                                                 host(q).reshape(n, heads, D), 0.125, 0)
+            bo, bl = R.attend_bounds(dtype, want, wl, mag, big_, toks, D)
+            assert (np.abs(host(box[pad:pad + n]).reshape(want.shape) - want) <= bo).all()
+            assert (np.abs(host(lbox[pad:pad + n]) - wl) <= bl).all()
+        # reads stay inside their rows, writes inside the pool
+        kbox, vbox = (torch.full((pad + n + pad, H * D), 33.0, dtype=tdt, device="cuda") for _ in range(2))
+        B.lora_kv_read(s.cache, seqs, code, kbox[pad:], H * D, vbox[pad:], H * D, n)
+        pool = torch.full((s.cache.k.numel() + 2 * 4096,), 99, dtype=torch.uint8, device="cuda")
+        shape = s.cache.k.shape
+        kp = pool[4096:-4096].view(shape)
+        other = B.KVCache(kp, kp.clone(), s.cache.k_scale.clone(), s.cache.v_scale.clone(), page_tokens=P, head_dim=D)
+        B.lora_kv_write(other, seqs, code, q, row, q[:, H * D:], row, n)
+        torch.cuda.synchronize()
+        for t in (kbox, vbox):
+            assert bool((t[:pad] == 33).all()) and bool((t[pad + n:] == 33).all())
+        assert bool((pool[:4096] == 99).all()) and bool((pool[-4096:] == 99).all())
+    s.check(dtype, heads)  # and the next call is served as ever
