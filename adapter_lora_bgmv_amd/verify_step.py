@@ -77,6 +77,8 @@ class VerifyStep:
                 B.lora_workspace_bytes(B.LORA_OP_APPLY, B.LORA_BF16, self.n, s.vocab, self.q_dim, 0),
                 B.lora_token_logprobs_workspace_bytes(B.LORA_BF16, s.vocab, self.n, s.top)]
         self.ws = [(zeros(max(b, 256), dtype=torch.uint8), b) for b in need]
+        if self.out.is_cuda:  # all of the above is there whatever stream the first step runs on
+            torch.cuda.current_stream().synchronize()
 
     def parts(self, x, stream=None):
         """The step's calls on hidden rows x, in order."""
@@ -96,12 +98,22 @@ class VerifyStep:
         }
 
     def run(self, x, lengths, ids, stream=None):
-        """Scores of the draft tokens `ids` [n]; `lengths` are the sequences' tokens, these drafts included."""
+        """Scores of the draft tokens `ids` [n]; `lengths` are the sequences' tokens, these drafts included.
+
+        The step's inputs are copied on the stream that its kernels run on (a
+        torch stream or a raw handle; None: the current one), so that they wait
+        for the step before.  x has to be ready on it, and the scores are.
+        """
         import torch
-        self.seqs.kv_len.copy_(torch.as_tensor(np.asarray(lengths, np.int32)))
-        self.ids.copy_(torch.as_tensor(np.asarray(ids, np.int32)))
-        for call in self.parts(x, stream).values():
-            call()
+        if stream is None:
+            stream = torch.cuda.current_stream()
+        elif not isinstance(stream, torch.cuda.Stream):
+            stream = torch.cuda.ExternalStream(stream) if stream else torch.cuda.default_stream()
+        with torch.cuda.stream(stream):
+            self.seqs.kv_len.copy_(torch.as_tensor(np.asarray(lengths, np.int32)))
+            self.ids.copy_(torch.as_tensor(np.asarray(ids, np.int32)))
+            for call in self.parts(x, stream).values():
+                call()
         return self.scores
 
 

@@ -74,3 +74,44 @@ def test_row_ranges_that_fall_or_leave_the_call(name, make, n, dtype):
             assert bool((t[:pad] == 33).all()) and bool((t[pad + n:] == 33).all())
         assert bool((pool[:4096] == 99).all()) and bool((pool[-4096:] == 99).all())
     s.check(dtype, heads)  # and the next call is served as ever
+
+
+# ---------------------------------------------------------------- streams
+def small_step(seed=5):
+    from adapter_lora_bgmv_amd import verify_step as V
+    z = V.Sizes(hidden=512, heads=8, kv_heads=2, head_dim=64, vocab=1000, page_tokens=16, slots=3, rank=16)
+    step = V.VerifyStep(z, n_seqs=3, draft=4, max_tokens=208, seed=seed)
+    g = torch.Generator(device="cuda").manual_seed(7)
+    for t in (step.cache.k, step.cache.v):
+        t.copy_(torch.randint(0, 126, t.shape, generator=g, device="cuda", dtype=torch.uint8))
+    step.cache.k_scale.fill_(120)
+    step.cache.v_scale.fill_(118)
+    torch.cuda.synchronize()
+    return step
+
+
+@pytest.mark.parametrize("raw", [False, True])  # a torch stream, a raw handle
+def test_verify_steps_on_a_side_stream(raw):
+    """Steps one after the other on another stream give what they give on the
+    current one, though the stream is kept busy while the next inputs come."""
+    rng = np.random.default_rng(8)
+    lens = [[50 + 4 * i, 7 + 4 * i, 150 + 4 * i] for i in range(6)]
+    ids = [rng.integers(0, 1000, 12) for _ in lens]
+    xs = [torch.from_numpy(rng.standard_normal((12, 512))).cuda().bfloat16() for _ in lens]
+    outs = []
+    for side in (False, True):
+        step, got = small_step(), []
+        stream = torch.cuda.Stream() if side else torch.cuda.current_stream()
+        busy = torch.zeros(1 << 26, device="cuda")
+        torch.cuda.synchronize()
+        for x, l, i in zip(xs, lens, ids):
+            with torch.cuda.stream(stream):
+                for _ in range(10):
+                    busy.add_(1.0)
+            step.run(x, l, i, (stream.cuda_stream if raw else stream) if side else None)
+            with torch.cuda.stream(stream):
+                got += [t.clone() for t in step.scores.values()] + [step.out.clone()]
+        torch.cuda.synchronize()
+        outs.append([host(t) for t in got] + [host(step.cache.k), host(step.cache.v)])
+    for a, b in zip(*outs):
+        assert np.array_equal(a, b)
