@@ -64,7 +64,7 @@ class lora_kv_seqs(C.Structure):
 
 
 _lib = None
-_lookup = []  # the calls that look up the current stream, once torch is there
+_lookup = None  # the calls that look up the current stream, once torch is there
 
 
 def lib() -> C.CDLL:
@@ -131,11 +131,13 @@ def _ptr(t) -> Optional[int]:
 
 
 def _stream(stream) -> Optional[int]:
+    global _lookup
     if stream is None:
-        if not _lookup:
+        found = _lookup
+        if found is None:  # threads that come here together set the same pair
             import torch
-            _lookup.extend((torch.cuda.current_device, torch._C._cuda_getCurrentRawStream))
-        device, raw = _lookup  # the current stream's handle without a Stream object: 0.3 us for 2.9
+            found = _lookup = (torch.cuda.current_device, torch._C._cuda_getCurrentRawStream)
+        device, raw = found  # the current stream's handle without a Stream object: 0.3 us for 2.9
         return raw(device())
     return getattr(stream, "cuda_stream", stream)
 
