@@ -339,13 +339,15 @@ __global__ __launch_bounds__(kScoreThreads) void score_kernel(ScoreArgs a) {
   __syncthreads();
   if (lds.arrived != (unsigned)a.chunks - 1) return;
 
-  // join, a chunk's numbers on each of the first threads (kScoreMaxChunks <= 256)
+  // join, a chunk's numbers on each of the first threads
+  static_assert(kScoreMaxChunks <= kScoreThreads, "a thread for every chunk");
   f32x4 r = {-INFINITY, 0.f, 0.f, 0.f};
   const __amdgpu_buffer_rsrc_t all = coherent_rsrc(base, (uint32_t)(rec * a.chunks));
   if (tid < a.chunks) r = ld16_coherent(all, (uint32_t)(tid * rec), 0);
   // pairs of keys: pair p of chunk c on thread c pairs + p, `rounds` of them
   const int pairs = (a.top + 1) / 2;
   constexpr int kRounds = kScoreMaxChunks * (kScoreMaxTop / 2) / kScoreThreads;
+  static_assert(kRounds * kScoreThreads == kScoreMaxChunks * (kScoreMaxTop / 2), "every pair has its place");
   u64 keys[2 * kRounds];
   uint32_t best = 0;
 #pragma unroll
@@ -414,7 +416,8 @@ __global__ __launch_bounds__(kScoreThreads) void score_kernel(ScoreArgs a) {
 ScoreSplit score_split(int n, int n_vocab, int dtype) {
   const int ve = dtype == 0 ? 4 : 8, batch = kScoreThreads * kScoreBatch;
   const int all = (n_vocab + ve - 1 + batch - 1) / batch;  // a row may begin up to ve - 1 elements into its first vector
-  const int want = std::min(all, (512 + n - 1) / n);
+  // a vocabulary of 2^20 whose rows may begin inside a vector has one batch more than the join takes chunks
+  const int want = std::min({all, (512 + n - 1) / n, kScoreMaxChunks});
   ScoreSplit r;
   r.batches = (all + want - 1) / want;
   r.chunks = (all + r.batches - 1) / r.batches;

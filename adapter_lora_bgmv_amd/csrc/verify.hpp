@@ -181,7 +181,7 @@ hipError_t launch_attend_join(const AttendJoin &a, int dim, int dtype, int forms
 // Scores of given tokens over rows of logits (k_score.hip).
 constexpr int kScoreThreads = 256;
 constexpr int kScoreMaxTop = 32;
-constexpr int kScoreMaxChunks = 128;  // of a row
+constexpr int kScoreMaxChunks = 128;  // of a row: score_split stays within it
 constexpr int kScoreBatch = 32;       // logits of a thread at a time
 struct ScoreArgs {
   const void *logits;  // [n][stride]

@@ -5,7 +5,7 @@ import pytest
 
 import verify_ref as R
 from adapter_lora_bgmv_amd import binding as B
-from test_gpu_verify import DT, Setup, dev, host
+from test_gpu_verify import DT, Setup, check_scores, dev, host
 
 torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
@@ -115,3 +115,18 @@ def test_verify_steps_on_a_side_stream(raw):
         outs.append([host(t) for t in got] + [host(step.cache.k), host(step.cache.v)])
     for a, b in zip(*outs):
         assert np.array_equal(a, b)
+
+
+# ---------------------------------------------------------------- scores
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("n,short,top", [(1, 0, 32), (2, 0, 32), (3, 1, 31), (2, 2, 32), (3, 6, 32), (2, 7, 30)])
+def test_scores_at_the_end_of_the_vocabulary_range(n, short, top, dtype):
+    """Rows of 2^20 logits or a few less that begin at every place of a 16-byte
+    vector, their largest logits at the very end."""
+    V = (1 << 20) - short
+    rng = np.random.default_rng(V + n)
+    x = rng.standard_normal((n, V))
+    x[:, V - 9:] = 8.0 + np.arange(9)
+    x[:, 3] = 7.0
+    for skew, extra in ((1, 1), (3, 2), (7, 3)):
+        check_scores(x, [V - 1] * n, top, dtype, skew, V + extra)
