@@ -130,3 +130,34 @@ def test_scores_at_the_end_of_the_vocabulary_range(n, short, top, dtype):
     x[:, 3] = 7.0
     for skew, extra in ((1, 1), (3, 2), (7, 3)):
         check_scores(x, [V - 1] * n, top, dtype, skew, V + extra)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("n,V,top", [(4, 40, 32), (4, 900, 32), (4, 70001, 32), (1100, 900, 5)])
+def test_alternatives_of_rows_with_nan_lie_in_the_vocabulary(n, V, top, dtype):
+    """NaN of either sign, in all of a row, most of it or half of it: NaN scores and different ids in range."""
+    rng = np.random.default_rng(V)
+    x = torch.from_numpy(rng.standard_normal((n, V)).astype(np.float32)).cuda()
+    share = torch.tensor([1.0, 0.97, 0.5, 1.0], device="cuda").repeat(n // 4)[:, None]
+    nan = torch.from_numpy(rng.random((n, V)).astype(np.float32)).cuda() < share
+    nan[:, 0] = True
+    bits, ty = (x.to(torch.bfloat16), torch.int16) if dtype == "bf16" else (x, torch.int32)
+    quiet = 0x7FC0 << (0 if dtype == "bf16" else 16)
+    sign = torch.from_numpy(rng.random((n, V))).cuda() < torch.tensor([1.0, 1.0, 0.5, 0.0], device="cuda").repeat(n // 4)[:, None]
+    lowest = -(1 << 15) if dtype == "bf16" else -(1 << 31)
+    filled = torch.where(sign, torch.tensor(quiet + lowest, dtype=ty, device="cuda"), torch.tensor(quiet, dtype=ty, device="cuda"))
+    logits = torch.where(nan, filled, bits.view(ty)).view(bits.dtype)
+    assert torch.isnan(logits[0]).all() and bool(torch.signbit(logits[0]).all())
+    code = DT[dtype][0]
+    need = B.lora_token_logprobs_workspace_bytes(code, V, n, top)
+    ws = torch.zeros(max(need, 16), dtype=torch.uint8, device="cuda")
+    lp, en, tl = torch.zeros(n, device="cuda"), torch.zeros(n, device="cuda"), torch.zeros(n, top, device="cuda")
+    ti = torch.full((n, top), -9, dtype=torch.int32, device="cuda")
+    for _ in range(2):
+        B.lora_token_logprobs(code, V, logits, V, torch.zeros(n, dtype=torch.int32, device="cuda"), n, top, lp, en, None, ti, tl,
+                              ws, need)
+    torch.cuda.synchronize()
+    for t in (lp, en, tl):
+        assert bool(torch.isnan(t).all())
+    assert bool(((ti >= 0) & (ti < V)).all())
+    assert bool((ti.sort(1).values.diff(dim=1) > 0).all())
