@@ -161,3 +161,16 @@ def test_alternatives_of_rows_with_nan_lie_in_the_vocabulary(n, V, top, dtype):
         assert bool(torch.isnan(t).all())
     assert bool(((ti >= 0) & (ti < V)).all())
     assert bool((ti.sort(1).values.diff(dim=1) > 0).all())
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("n,V,top", [(3, 40, 32), (3, 900, 20), (3, 70001, 32), (1100, 900, 5)])
+def test_zeros_of_either_sign_are_equal(n, V, top, dtype):
+    """Rows whose largest logits are 0 and -0, many of them or a few."""
+    rng = np.random.default_rng(V + 1)
+    for share in (1.0, 0.3, 6.0 / V):
+        x = -np.abs(rng.standard_normal((n, V))) - 1.0
+        zero = rng.random((n, V)) < share
+        x[zero] = 0.0
+        x[zero & (rng.random((n, V)) < 0.5)] = -0.0
+        check_scores(x, rng.integers(0, V, n), top, dtype)
