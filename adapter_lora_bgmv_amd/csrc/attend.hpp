@@ -92,10 +92,13 @@ __device__ __forceinline__ int lane_again() {
 // The lowest n of 16 bits, 0 <= n <= 16 once clamped.
 __device__ __forceinline__ uint32_t live_bits(int n) { return (1u << min(max(n, 0), 16)) - 1u; }
 
-// Of the 16 tokens from tok0, those that a column sees whose last token is hi - 1.
+// The first token that a column sees whose last token is hi - 1.  hi may be
+// negative and a window as large as an int: no difference is taken below 0.
+__device__ __forceinline__ int first_seen(int hi, int window) { return window && hi > window ? hi - window : 0; }
+
+// Of the 16 tokens from tok0, those that such a column sees.
 __device__ __forceinline__ uint32_t sees(int hi, int window, int tok0) {
-  const int first = window && hi > window ? hi - window : 0;
-  return live_bits(hi - tok0) & ~live_bits(first - tok0);
+  return live_bits(hi - tok0) & ~live_bits(first_seen(hi, window) - tok0);
 }
 
 // Bytes of four tokens from t0 that lie in [lo, hi).
@@ -118,7 +121,7 @@ __device__ __forceinline__ int seq_blocks(const AttendArgs &a, const SeqDev &s) 
 // Tiles that a unit of the sequence sees at most; 1 where it sees none (its rows are written as zeros).
 template <int CB>
 __device__ __forceinline__ int unit_tiles(const AttendArgs &a, const SeqDev &s, int cap) {
-  const int lo = a.window ? max(0, s.start + 1 - a.window) : 0, hi = min(s.len, cap);
+  const int lo = first_seen(s.start + 1, a.window), hi = min(s.len, cap);
   if (hi <= lo) return 1;
   const int all = (hi + kTile - 1) / kTile - lo / kTile;
   // tokens under a window: its own and one more for every further row of the unit

@@ -513,7 +513,7 @@ __global__ __launch_bounds__(256, attend_per_cu(D, F32, WIDE ? kWide : kNarrow))
   // the tokens that the unit's columns see, [lo_u, hi_u), and this chunk's tiles of them
   const int j_first = a.G.div(w.block * CB), j_last = a.G.div(w.block * CB + n_cols - 1);
   const int hi_u = max(min(w.s.start + j_last + 1, cap), 0);
-  const int lo_u = a.window ? max(w.s.start + j_first + 1 - a.window, 0) : 0;
+  const int lo_u = first_seen(w.s.start + j_first + 1, a.window);
   const int tile0 = lo_u / kTile, tiles = hi_u > lo_u ? (hi_u + kTile - 1) / kTile - tile0 : 0;
   int ta = tile0, tb = tile0 + tiles;
   if (w.nc > 1) {  // the first tiles % nc chunks take one more
@@ -526,7 +526,7 @@ __global__ __launch_bounds__(256, attend_per_cu(D, F32, WIDE ? kWide : kNarrow))
   const int c0 = w.block * CB + (WIDE ? wave * CW : 0);
   const int c1 = min(c0 + CW, w.s.rows * a.G.d);
   const int j0 = WIDE ? a.G.div(c0) : j_first, j1 = WIDE ? a.G.div(max(c1 - 1, 0)) : j_last;
-  const int hi_all = min(w.s.start + j0 + 1, cap), lo_all = a.window ? w.s.start + j1 + 1 - a.window : 0;
+  const int hi_all = min(w.s.start + j0 + 1, cap), lo_all = first_seen(w.s.start + j1 + 1, a.window);
   Columns<D, NB, F32> cols;
   PageInfo info;
 
@@ -598,7 +598,7 @@ __global__ __launch_bounds__(256, attend_per_cu(D, F32, WIDE ? kWide : kNarrow))
 #pragma unroll
     for (int k = 0; k < N - 1; ++k)
       if (ta + k < tb) bring(info.group, k, k);
-    const int wave_lo = a.window ? max(w.s.start + j0 + 1 - a.window, 0) : 0;
+    const int wave_lo = first_seen(w.s.start + j0 + 1, a.window);
     const int wave_hi = c0 < c1 ? min(w.s.start + j1 + 1, cap) : 0;
     PageInfo later = info;  // of the next 16 tiles
     int later_page = -1, i = 0, stage = 0;

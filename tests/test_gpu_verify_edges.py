@@ -76,6 +76,16 @@ def test_row_ranges_that_fall_or_leave_the_call(name, make, n, dtype):
     s.check(dtype, heads)  # and the next call is served as ever
 
 
+# ---------------------------------------------------------------- windows
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("D", [64, 256])
+@pytest.mark.parametrize("window", [2 ** 31 - 1, 2 ** 31 - 5, 2 ** 31 - 60, 5000])
+def test_windows_wider_than_the_sequences_hide_nothing(window, D, dtype):
+    """Up to the largest, also where a sequence has more rows than tokens, and
+    so rows at negative positions."""
+    s = Setup(410, [(6, 3), (40, 3), (70, 64), (3, 1), (5, 700)], 1, D, 16)
+    s.check(dtype, 4, window)
+
 # ---------------------------------------------------------------- streams
 def small_step(seed=5):
     from adapter_lora_bgmv_amd import verify_step as V
