@@ -201,10 +201,12 @@ __device__ __forceinline__ bool find_work(const AttendArgs &a, int u, int lane, 
 
 // ---------------------------------------------------------------- results
 // The exponents b of values that the matrix operand takes, as bytes, and
-// what it adds to them.
+// what it adds to them.  For f32 calls bf16's range would reach further than
+// the f32 sums': up to 2^60, 2^31 tokens of codes up to 2^9 under weights up
+// to 2^15 stay below 2^115.
 template <bool F32>
 struct ValueExp {
-  static constexpr int kLo = F32 ? 10 : 106, kHi = F32 ? 227 : 127, kAdd = F32 ? 0 : 6;
+  static constexpr int kLo = F32 ? 10 : 106, kHi = F32 ? 187 : 127, kAdd = F32 ? 0 : 6;
 };
 // What a column's sums are multiplied by at the end.  A row that saw nothing
 // has l = 0 and is zero; a NaN denominator stays one.

@@ -6,6 +6,7 @@ import pytest
 import verify_ref as R
 from adapter_lora_bgmv_amd import binding as B
 from test_gpu_verify import DT, Setup, check_scores, dev, host
+from test_gpu_verify_forms import set_codes
 
 torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
@@ -85,6 +86,21 @@ def test_windows_wider_than_the_sequences_hide_nothing(window, D, dtype):
     so rows at negative positions."""
     s = Setup(410, [(6, 3), (40, 3), (70, 64), (3, 1), (5, 700)], 1, D, 16)
     s.check(dtype, 4, window)
+
+# ---------------------------------------------------------------- values near the end of f32's range
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("lens", [[(1, 20000)], [(20, 20000), (3, 500)]])
+@pytest.mark.parametrize("power", [57, 70, 106, 116])
+def test_sums_over_many_large_values(power, lens, dtype):
+    """Values of 2^power in every page, then in every third of them: the output is
+    a mean of them and as finite as they are."""
+    s = Setup(420, lens, 1, 64, 128)
+    place = {int(p): i for i, p in enumerate(s.seqs["table"][0])}
+    set_codes(s, "v", lambda p, x: (2.0 + np.clip(x, -1.0, 2.0)) * 2.0 ** power)
+    s.check(dtype, 2, scale=2.0 ** -20)  # nearly equal weights
+    s.check(dtype, 2)
+    set_codes(s, "v", lambda p, x: x if place.get(p, 0) % 3 else x * 2.0 ** -power)
+    s.check(dtype, 2)
 
 # ---------------------------------------------------------------- streams
 def small_step(seed=5):
