@@ -293,7 +293,8 @@ __device__ __forceinline__ void store_row16(T *p, const uint32_t w[4], float sca
 // that the parts of a row are stored close together in time (4 x 4096 tokens,
 // 8 heads x 128: 25.1 -> 23.6 us, f32 47.8 -> 44.2); a call's rows are few
 // enough for pages to be a grid's second dimension.  Every product is exact:
-// e4m3 times a power of two in the range of the exponent bytes is a bf16 number.
+// e4m3 times a power of two in the range of the exponent bytes is a bf16
+// number, but for 256 2^120 and above, which become infinities.
 template <typename T, int D, int IT>
 __global__ __launch_bounds__(kKvThreads) void kv_read_kernel(KvDev a, T *krows, int k_stride, T *vrows, int v_stride) {
   const int tid = threadIdx.x, lane = tid & 63;

@@ -410,7 +410,9 @@ int lora_apply_stack(int32_t dtype, uint32_t n_out, uint32_t k_in, const void *W
  * The cache keeps keys and values in 8 bits.  It is cut into pages of
  * page_tokens tokens; a page's head holds page_tokens x head_dim e4m3 codes
  * of K, as many of V, and one scale byte for each.  A code c under scale
- * byte e stands for c * 2^(e - 127).  All arrays are [dev]:
+ * byte e stands for c * 2^(e - 127), for e from 10 to 247, the bytes that
+ * lora_kv_write leaves; under another byte it may stand for anything.  All
+ * arrays are [dev]:
  *   k, v              [n_pages][n_kv_heads][page_tokens * head_dim] bytes
  *   k_scale, v_scale  [n_pages][n_kv_heads] bytes
  * Within a page's head (token t, dim d) lies, in the order in which the
@@ -477,8 +479,10 @@ int lora_kv_write(const lora_kv_cache *cache, const lora_kv_seqs *seqs, int32_t 
 /*
  * Reads the tokens of the call's rows back, the inverse of lora_kv_write with
  * the same arguments (with row_indptr the running sum of kv_len: whole
- * sequences).  The values are exact in either dtype.  Rows whose position
- * names no page are not written.
+ * sequences).  The values are exact in either dtype, but for codes of 256 and
+ * more under scale byte 247, which stand for numbers beyond either's range
+ * (a written |x| of 248 * 2^120 = 3.297e38 or more is rounded to one) and are
+ * read as infinities.  Rows whose position names no page are not written.
  */
 int lora_kv_read(const lora_kv_cache *cache, const lora_kv_seqs *seqs, int32_t dtype, void *k,
                  uint32_t k_row_stride, void *v, uint32_t v_row_stride, uint32_t n, void *stream);

@@ -77,6 +77,30 @@ def test_row_ranges_that_fall_or_leave_the_call(name, make, n, dtype):
     s.check(dtype, heads)  # and the next call is served as ever
 
 
+# ---------------------------------------------------------------- cache
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_the_largest_numbers_read_back(dtype):
+    """Under the largest scale, 2^120, codes up to 240 are read exactly, and what
+    is rounded to 256 or more as infinity; a page's smaller values stay exact."""
+    H, D, P = 1, 64, 16
+    top = 2.0 ** 120
+    s = Setup(430, [(7, 7)], H, D, P)
+    x = np.zeros((7, 2 * D))
+    # 248 is the tie between 240 and 256; bf16 has the numbers used here
+    for t, v in enumerate([255.0, 248.0, 247.0, 240.0, 224.5, 2.0, 0.0]):
+        x[t] = v * top * np.where(np.arange(2 * D) % 3 == 1, -1.0, 1.0)
+    x[6, 9] = 2.0 ** 111
+    dx = dev(x, dtype)
+    B.lora_kv_write(s.cache, s.dseqs, DT[dtype][0], dx, 2 * D, dx[:, D:], 2 * D, s.n)
+    o = torch.zeros_like(dx)
+    B.lora_kv_read(s.cache, s.dseqs, DT[dtype][0], o, 2 * D, o[:, D:], 2 * D, s.n)
+    torch.cuda.synchronize()
+    assert host(s.cache.k_scale)[s.seqs["table"][0, 0], 0] == 247
+    want = np.sign(x) * np.array([np.inf, np.inf, 240 * top, 240 * top, 224 * top, 2 * top, 1.0])[:, None]
+    want[6] = 0.0
+    want[6, 9] = 2.0 ** 111
+    assert np.array_equal(host(o), want)
+
 # ---------------------------------------------------------------- windows
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("D", [64, 256])
