@@ -155,10 +155,18 @@ constexpr int attend_target(int dim, int dtype, AttendForm f) {
   return f == kNarrow && per_cu == 2 ? 384 : 256 * per_cu;
 }
 constexpr int attend_slots(int dim, int dtype, AttendForm f) { return 2 * attend_target(dim, dtype, f); }
-// Tiles that are worth a chunk of their own: four a wave of the narrow form,
-// where fewer cost more in start and join than they save; four of the wide
-// form, whose workgroups wait for memory; eight of the wider, which compute
-// (8 prompts of 512 rows: 51.6 us split at four and joined, 49.1 whole).
+// Tiles that are worth a chunk of their own: four a wave of the narrow form;
+// four of the wide form, whose workgroups wait for memory; eight of the wider,
+// whose units are many and write more than they read in the prompts that this
+// leaves whole.  Each helps some calls and costs others (us, 8 heads of 128
+// unless said, tables of 8192 tokens; at half as many tiles, at this, at twice):
+//   narrow  1 row over 701 tokens 10.6 / 9.9 / 9.9, over 4001 11.0 / 12.6 / 15.7;
+//           32 rows over 1001 19.5 / 17.5 / 17.5; 4 in f32 over 1501 14.4 / 15.9 / 19.0
+//   wide    4 x 9 rows over 709 12.9 / 15.5 / 18.0; 16 x 9 over 509 18.2 / 18.9 / 17.3;
+//           a prompt of 512 rows 256 wide 37.5 / 37.4 / 26.1
+//   wider   prompts of 512 rows: one 32.1 / 23.2 / 23.2, two 40.3 / 26.3 / 26.5; 512
+//           rows over 2512 49 / 48 / 55; 100 over 800 24.4 / 31.0 / 30.6; 40 over
+//           3040 26.1 / 29.2 / 43.2; 1024 rows 44.6 / 44.6 / 37.9
 constexpr int attend_min_tiles(AttendForm f) { return f == kNarrow ? 16 : f == kWide ? 4 : 8; }
 hipError_t launch_attend(const AttendArgs &a, int dim, int dtype, AttendForm f, hipStream_t st);
 
