@@ -42,17 +42,18 @@ constexpr int kScoreList = 1024;  // entries of the LDS list
 typedef unsigned long long u64;
 constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
 
-// Unsigned order of an f32's bits is its value's order: the zeros are equal
-// (-0 + 0 is 0), and NaN of either sign is above everything, so that the keys
-// of a row reach what its maximum reaches.
+// Unsigned order of an f32's bits is its value's order; the zeros are equal (-0 + 0 is 0).
 __device__ __forceinline__ uint32_t ordered(float x) {
   const uint32_t b = __float_as_uint(x + 0.f);
-  return x == x ? b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u) : ~0u;
+  return b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
 }
 __device__ __forceinline__ float from_ordered(uint32_t o) {
   return __uint_as_float(o & 0x80000000u ? o ^ 0x80000000u : ~o);
 }
-__device__ __forceinline__ u64 key_of(float x, uint32_t index) { return (u64)ordered(x) << 32 | (uint32_t)~index; }
+// NaN of either sign is above everything, so that the keys of a row reach what its maximum reaches.
+__device__ __forceinline__ u64 key_of(float x, uint32_t index) {
+  return (u64)(x == x ? ordered(x) : ~0u) << 32 | (uint32_t)~index;
+}
 
 template <typename T>
 struct Vec;
