@@ -224,3 +224,27 @@ def test_zeros_of_either_sign_are_equal(n, V, top, dtype):
         x[zero] = 0.0
         x[zero & (rng.random((n, V)) < 0.5)] = -0.0
         check_scores(x, rng.integers(0, V, n), top, dtype)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("n,V,top", [(513, 100001, 20), (512, 200000, 0), (130, 1 << 20, 7)])
+def test_scores_of_many_rows_over_a_large_vocabulary(n, V, top, dtype):
+    """A workgroup to a row, or a few: hundreds of terms to a thread's running sums."""
+    code, name = DT[dtype]
+    g = torch.Generator(device="cuda").manual_seed(V)
+    x = (torch.randn(n, V, generator=g, device="cuda") * 3.0).to(getattr(torch, name))
+    ids = torch.randint(0, V, (n,), generator=g, device="cuda", dtype=torch.int32)
+    lp, en, tl = torch.zeros(n, device="cuda"), torch.zeros(n, device="cuda"), torch.zeros(n, top, device="cuda")
+    rk, ti = torch.zeros(n, dtype=torch.int32, device="cuda"), torch.zeros(n, top, dtype=torch.int32, device="cuda")
+    need = B.lora_token_logprobs_workspace_bytes(code, V, n, top)
+    ws = torch.zeros(max(need, 16), dtype=torch.uint8, device="cuda")
+    B.lora_token_logprobs(code, V, x, V, ids, n, top, lp, en, rk, ti, tl, ws, need)
+    torch.cuda.synchronize()
+    some = list(range(0, n, max(n // 9, 1))) + [n - 1]
+    want = R.score(host(x[some]), host(ids[some]), top)
+    assert np.array_equal(host(rk[some]), want[2]) and np.array_equal(host(ti[some]), want[3])
+    # V / 256 terms a thread at most, then trees; exponents and exp2, log2 as for shorter rows
+    u = 2.0 ** -24
+    off = (V / 256 + 128) * u
+    for got, w, slack in ((lp, want[0], off), (tl, want[4], off), (en, want[1], off * (2 + np.log(V)))):
+        assert (np.abs(host(got[some]) - w) <= slack + 4 * u * np.abs(w)).all()
