@@ -111,6 +111,59 @@ def test_windows_wider_than_the_sequences_hide_nothing(window, D, dtype):
     s = Setup(410, [(6, 3), (40, 3), (70, 64), (3, 1), (5, 700)], 1, D, 16)
     s.check(dtype, 4, window)
 
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("window", [0, 50, 2 ** 31 - 1, 2 ** 31 - 30])
+def test_lengths_far_past_the_page_table(window, dtype):
+    """Up to the largest int: the rows stand past every page and see what the table
+    holds, or the part that a window of nearly that size leaves."""
+    s = Setup(411, [(5, 64), (40, 64), (1, 50), (2, 33)], 1, 64, 16)
+    s.seqs["kv_len"][:] = [2 ** 31 - 1, 2 ** 31 - 3, 2 ** 31 - 1, 33]
+    s.upload()
+    s.check(dtype, 4, window)
+    x = torch.randn(s.n, 128, device="cuda")
+    before = host(s.cache.k).copy()
+    s.seqs["kv_len"][3] = 0
+    s.upload()
+    B.lora_kv_write(s.cache, s.dseqs, B.LORA_F32, x, 128, x[:, 64:], 128, s.n)
+    o = torch.full_like(x, 5.0)
+    B.lora_kv_read(s.cache, s.dseqs, B.LORA_F32, o, 128, o[:, 64:], 128, s.n)
+    torch.cuda.synchronize()
+    assert np.array_equal(host(s.cache.k), before) and bool((o == 5).all())
+
+
+def test_a_cache_past_four_gibibytes():
+    """The last pages of a pool of 5 GiB a side give what the same pages give in a small one."""
+    H, D, P, heads = 8, 128, 128, 16
+    s = Setup(440, [(1, 900), (3, 300), (40, 500)], H, D, P)
+    few, many = s.host.ke.shape[0], 40960
+    shift = many - few
+    pools = [torch.empty(many, H, P * D, dtype=torch.uint8, device="cuda") for _ in range(2)]
+    exps = [torch.empty(many, H, dtype=torch.uint8, device="cuda") for _ in range(2)]
+    size = pools[0].numel()
+    assert size >= 5 << 30
+    for big, small in zip(pools + exps, (s.cache.k, s.cache.v, s.cache.k_scale, s.cache.v_scale)):
+        big[shift:] = small
+    large = B.KVCache(*pools, *exps, page_tokens=P, head_dim=D)
+    table = s.seqs["table"]
+    seqs = B.KVSeqs(dev(np.where(table >= 0, table + shift, table).astype(np.int32)), s.dseqs.row_indptr, s.dseqs.kv_len)
+    x = torch.randn(s.n, 2 * H * D, device="cuda").bfloat16()
+    q = torch.randn(s.n, heads * D, device="cuda").bfloat16()
+    got = []
+    for cache, sq in ((s.cache, s.dseqs), (large, seqs)):
+        B.lora_kv_write(cache, sq, B.LORA_BF16, x, 2 * H * D, x[:, H * D:], 2 * H * D, s.n)
+        o = torch.zeros_like(x)
+        B.lora_kv_read(cache, sq, B.LORA_BF16, o, 2 * H * D, o[:, H * D:], 2 * H * D, s.n)
+        need = B.lora_kv_attend_workspace_bytes(cache, sq, B.LORA_BF16, heads, s.n)
+        ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+        out = torch.zeros_like(q)
+        B.lora_kv_attend(cache, sq, B.LORA_BF16, heads, q, heads * D, D ** -0.5, 0, s.n, out, heads * D, None, ws, need)
+        torch.cuda.synchronize()
+        got.append([host(o), host(out)] + [host(t[-few:]) for t in (cache.k, cache.v, cache.k_scale, cache.v_scale)])
+    for a, b in zip(*got):
+        assert np.array_equal(a, b, equal_nan=a.dtype.kind == "f")
+    assert np.abs(got[0][1]).max() > 0.1
+
 # ---------------------------------------------------------------- values near the end of f32's range
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("lens", [[(1, 20000)], [(20, 20000), (3, 500)]])
