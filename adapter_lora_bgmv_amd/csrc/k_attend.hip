@@ -27,7 +27,7 @@
 // rescales the sums, which after a few tiles is rare.
 //
 // Rounding: bf16 calls take q as it is and round the weights, 2^8 at the
-// running maximum, to f16 (2^-12, an eighth of the output's own half step;
+// running maximum, to f16 (2^-11, an eighth of the output's own half step;
 // weights down to 2^-32 of the largest count); f32 calls split q and the
 // weights into three bf16 terms (24 bits) and take three products of each.
 // Scores, sums and outputs accumulate in f32.
@@ -36,10 +36,10 @@
 // each wave of a workgroup takes every fourth tile straight into registers,
 // and the four are joined through LDS; a decode batch is bound by HBM (64 rows
 // over 1 to 8192 tokens: 111 us, 4.8 TB/s), one row by latency (701 tokens:
-// 7.7 us).  Wide (more columns): the waves take 16 NB columns each and share
+// 7.8 us, 1.5 more where a wider page table adds the join).  Wide (more columns): the waves take 16 NB columns each and share
 // the tiles, which LDS-DMA brings in two or three ahead.  With two blocks a
 // wave it is bound by issue: 62 products and 313 other vector instructions a
-// tile (1024 rows over 16 000 tokens: 913 TFLOP/s, matrix unit busy 36 %).
+// tile (1024 rows over 16 000 tokens: 914 TFLOP/s, matrix unit busy 36 %).
 // Two blocks instead of one halve the conversions a product; three do not fit
 // the registers of two waves a SIMD.
 //

@@ -18,7 +18,7 @@
 //
 // Both kernels move bytes only, so HBM bounds large calls (4 x 4096 tokens of
 // 8 heads x 128 back to bf16 rows: 24 us, 4.3 TB/s, two thirds of it writes)
-// and latency small ones (64 rows joining their pages: 5.9 us, four dependent
+// and latency small ones (64 rows joining their pages: 5.7 us, four dependent
 // round trips).  A K item is one token's 16 dims: 32 bytes of bf16 row, 16 bytes of
 // code.  A V item is four tokens by four dims, transposed in registers by
 // byte permutes (the two layouts differ by exactly that transpose), the

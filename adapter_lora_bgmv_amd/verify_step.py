@@ -8,6 +8,8 @@
     attends over the cache (lora_kv_attend),
     projects to the vocabulary, base weights only (lora_apply), and
     scores the draft tokens (lora_token_logprobs).
+A model's position encoding, which the step leaves out, would turn queries and
+keys between the projection and the write.
 Everything stays on the device and on one stream; pages, lengths, adapters and
 token ids are device arrays whose contents change from step to step, so the
 calls can be captured into a graph once.  The command runs a step of the
