@@ -27,8 +27,9 @@
 // rescales the sums, which after a few tiles is rare.
 //
 // Rounding: bf16 calls take q as it is and round the weights, 2^8 at the
-// running maximum, to f16 (2^-11, an eighth of the output's own half step;
-// weights down to 2^-32 of the largest count); f32 calls split q and the
+// running maximum, to f16 (2^-11, an eighth of the output's own half step, for
+// weights down to 2^-22 of the largest; steps of 2^-32 of it below, which show
+// only where every larger weight meets a zero); f32 calls split q and the
 // weights into three bf16 terms (24 bits) and take three products of each.
 // Scores, sums and outputs accumulate in f32.
 //

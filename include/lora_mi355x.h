@@ -498,8 +498,11 @@ int lora_kv_read(const lora_kv_cache *cache, const lora_kv_seqs *seqs, int32_t d
  * are [dev] [n][row stride], head h at h * head_dim, strides and pointers as
  * in lora_kv_write; scale is finite and above 0.  What a token that a row
  * does not see holds, NaN included, does not reach that row.  Scores, sums
- * and outputs run in f32 (bf16 calls round the weights to 11 bits before the
- * product with v); out is rounded once.  The order of every sum follows from
+ * and outputs run in f32; out is rounded once.  bf16 calls round the weights
+ * to f16 before the product with v, the row's largest being 2^8 or more: 11
+ * bits, fewer below 2^-22 of the largest, where the step is 2^-32 of it (a
+ * page's scale counts into its tokens' weights as far as it lies outside
+ * 2^-21 .. 1).  The order of every sum follows from
  * the call's lengths alone.  workspace [dev] of at least
  * lora_kv_attend_workspace_bytes(...) bytes (a function of the head counts
  * and sizes, dtype, n, n_seqs, the page table's width and max_rows), of any

@@ -179,6 +179,44 @@ def test_sums_over_many_large_values(power, lens, dtype):
     set_codes(s, "v", lambda p, x: x if place.get(p, 0) % 3 else x * 2.0 ** -power)
     s.check(dtype, 2)
 
+# ---------------------------------------------------------------- weights far below the largest
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("lens", [[(1, 300)], [(9, 300)], [(40, 300)]])
+@pytest.mark.parametrize("gap", [10, 20, 26, 31, 36, 60])
+def test_small_weights_where_the_largest_meet_zeros(gap, lens, dtype):
+    """One token outweighs all others by 2^gap and is zero in half of the dims,
+    where the outputs are the others': as exact as any down to 2^-22, from
+    there on within half a step, 2^-33 of the largest weight, a token."""
+    D, pos = 64, 5
+    s = Setup(450, lens, 1, D, 16, spread=0.0)
+    page = int(s.seqs["table"][0, pos // 16])
+
+    def keys(p, x):
+        y = np.zeros_like(x)
+        y[:, 0] = x[:, 0] * 0.01
+        if p == page:
+            y[pos, 0] = gap * np.log(2.0)
+        return y
+
+    def values(p, x):
+        if p == page:
+            x[pos, ::2] = 0.0
+        return x
+
+    set_codes(s, "k", keys)
+    set_codes(s, "v", values)
+    q = np.zeros((s.n, 2, D))
+    q[:, :, 0] = 1.0
+    q, out, lse = s.attend(dtype, 2, scale=1.0, q=q)
+    want, wl, mag, big, toks = R.attend(s.host, s.seqs, q, 1.0, 0)
+    bo, bl = R.attend_bounds(dtype, want, wl, mag, big, toks, D)
+    if dtype == "bf16" and gap > 21:  # keys' rounding moves the gap by a part in 16
+        pages = s.seqs["table"][0, :-(-lens[0][1] // 16)]
+        v = R.TABLE[s.host.v[pages, 0]] * np.exp2(s.host.ve[pages, 0].astype(float) - 127)[:, None, None]
+        bo = bo + 2.0 ** -33 * np.abs(v.reshape(-1, D)[:lens[0][1]]).sum(0)
+    assert (np.abs(out - want) <= bo).all() and (np.abs(lse - wl) <= bl).all()
+    assert np.abs(out[..., ::2]).max() < 300 * 2.0 ** -(gap * 15 / 16) * 300
+
 # ---------------------------------------------------------------- streams
 def small_step(seed=5):
     from adapter_lora_bgmv_amd import verify_step as V
