@@ -30,7 +30,9 @@ EXPORTS = ("lora_last_error", "lora_version", "lora_init", "lora_scale", "lora_s
            "lora_set_profile_events", "lora_moe_grouped_shrink", "lora_moe_grouped_expand_fold",
            "lora_apply_moe_grouped", "lora_apply_stack", "lora_embedding_pair",
            "lora_embed_rows", "lora_kv_write", "lora_kv_read", "lora_kv_attend_workspace_bytes",
-           "lora_kv_attend", "lora_token_logprobs_workspace_bytes", "lora_token_logprobs")
+           "lora_kv_attend", "lora_token_logprobs_workspace_bytes", "lora_token_logprobs",
+           "lora_kv_write_rotary", "lora_token_sample_workspace_bytes", "lora_token_sample", "lora_quantize_fp8",
+           "lora_matmul_fp8_workspace_bytes", "lora_matmul_fp8")
 
 
 class LoraError(RuntimeError):
@@ -61,6 +63,10 @@ class lora_kv_seqs(C.Structure):
     _fields_ = [("page_table", C.c_void_p), ("row_indptr", C.c_void_p), ("kv_len", C.c_void_p),
                 ("n_seqs", C.c_uint32), ("max_pages", C.c_uint32), ("table_stride", C.c_uint32),
                 ("max_rows", C.c_uint32)]
+
+
+class lora_rotary(C.Structure):
+    _fields_ = [("inv_freq", C.c_void_p), ("rot_dim", C.c_uint32), ("interleaved", C.c_int32)]
 
 
 _lib = None
@@ -117,6 +123,14 @@ def lib() -> C.CDLL:
     L.lora_token_logprobs_workspace_bytes.restype = sz
     L.lora_token_logprobs_workspace_bytes.argtypes = [i32, u32, u32, u32]
     L.lora_token_logprobs.argtypes = [i32, u32, vp, u32, vp, u32, u32, vp, vp, vp, vp, vp, vp, sz, vp]
+    L.lora_kv_write_rotary.argtypes = [KP, SP, C.POINTER(lora_rotary), i32, u32, vp, u32, vp, u32, vp, u32, vp, u32, u32, vp]
+    L.lora_token_sample_workspace_bytes.restype = sz
+    L.lora_token_sample_workspace_bytes.argtypes = [i32, u32, u32]
+    L.lora_token_sample.argtypes = [i32, u32, vp, u32, vp, vp, vp, vp, vp, u32, vp, vp, vp, sz, vp]
+    L.lora_quantize_fp8.argtypes = [i32, u32, u32, vp, u32, u32, vp, u32, vp, u32, vp]
+    L.lora_matmul_fp8_workspace_bytes.restype = sz
+    L.lora_matmul_fp8_workspace_bytes.argtypes = [i32, u32, u32, u32]
+    L.lora_matmul_fp8.argtypes = [i32, u32, u32, vp, u32, vp, u32, vp, u32, vp, u32, u32, vp, u32, vp, sz, vp]
     _lib = L
     return L
 
@@ -434,3 +448,53 @@ def lora_token_logprobs(dtype: int, n_vocab: int, logits, row_stride: int, token
     _check(lib().lora_token_logprobs(dtype, n_vocab, _ptr(logits), row_stride, _ptr(token_ids), n, top,
                                      _ptr(logp), _ptr(entropy), _ptr(rank), _ptr(top_ids), _ptr(top_logp),
                                      _ptr(workspace), workspace_bytes, _stream(stream)))
+
+
+# ---------------------------------------------------------------- rotation, sampling
+class Rotary:
+    """The position rotation of a model's heads (lora_rotary): device f32
+    ``inv_freq [rot_dim / 2]``, contiguous; ``interleaved`` pairs are (2i, 2i + 1),
+    otherwise (i, i + rot_dim / 2)."""
+
+    def __init__(self, inv_freq, *, interleaved: bool = False):
+        import torch
+        if inv_freq.dtype != torch.float32 or inv_freq.dim() != 1 or not inv_freq.is_contiguous():
+            raise ValueError(f"inv_freq must be contiguous float32 of one dimension: got {inv_freq.dtype} {tuple(inv_freq.shape)}")
+        self.inv_freq, self.rot_dim, self.interleaved = inv_freq, 2 * inv_freq.numel(), bool(interleaved)
+        self.c = lora_rotary(inv_freq.data_ptr(), self.rot_dim, int(self.interleaved))
+        self.ref = C.byref(self.c)
+
+
+def lora_kv_write_rotary(cache: KVCache, seqs: KVSeqs, rotary: Rotary, dtype: int, n_heads: int, q, q_row_stride: int, q_out,
+                         q_out_row_stride: int, k, k_row_stride: int, v, v_row_stride: int, n: int, stream=None):
+    _check(lib().lora_kv_write_rotary(cache.ref, seqs.ref, rotary.ref, dtype, n_heads, _ptr(q), q_row_stride, _ptr(q_out),
+                                      q_out_row_stride, _ptr(k), k_row_stride, _ptr(v), v_row_stride, n, _stream(stream)))
+
+
+def lora_token_sample_workspace_bytes(dtype: int, n_vocab: int, n: int) -> int:
+    return int(lib().lora_token_sample_workspace_bytes(dtype, n_vocab, n))
+
+
+def lora_token_sample(dtype: int, n_vocab: int, logits, row_stride: int, temperature, top_k, top_p, min_p, uniform, n: int, ids,
+                      logp, workspace, workspace_bytes: int, stream=None):
+    _check(lib().lora_token_sample(dtype, n_vocab, _ptr(logits), row_stride, _ptr(temperature), _ptr(top_k), _ptr(top_p),
+                                   _ptr(min_p), _ptr(uniform), n, _ptr(ids), _ptr(logp), _ptr(workspace), workspace_bytes,
+                                   _stream(stream)))
+
+
+# ---------------------------------------------------------------- the base projection in 8 bits
+def lora_quantize_fp8(dtype: int, n_rows: int, k: int, x, x_row_stride: int, block_rows: int, codes, codes_row_stride: int, scale,
+                      scale_row_stride: int, stream=None):
+    _check(lib().lora_quantize_fp8(dtype, n_rows, k, _ptr(x), x_row_stride, block_rows, _ptr(codes), codes_row_stride, _ptr(scale),
+                                   scale_row_stride, _stream(stream)))
+
+
+def lora_matmul_fp8_workspace_bytes(dtype: int, n_out: int, k_in: int, n: int) -> int:
+    return int(lib().lora_matmul_fp8_workspace_bytes(dtype, n_out, k_in, n))
+
+
+def lora_matmul_fp8(dtype: int, n_out: int, k_in: int, W, w_row_stride: int, w_scale, w_scale_stride: int, x, x_row_stride: int,
+                    x_scale, x_scale_stride: int, n: int, y, y_row_stride: int, workspace, workspace_bytes: int, stream=None):
+    _check(lib().lora_matmul_fp8(dtype, n_out, k_in, _ptr(W), w_row_stride, _ptr(w_scale), w_scale_stride, _ptr(x), x_row_stride,
+                                 _ptr(x_scale), x_scale_stride, n, _ptr(y), y_row_stride, _ptr(workspace), workspace_bytes,
+                                 _stream(stream)))

@@ -15,6 +15,20 @@ int launch_status(hipError_t e, const char *what);
 int check_device(const char *what);
 // Records the caller's profile event i, if set (lora_set_profile_events).
 void prof_record(int i, hipStream_t st);
+// LORA_OK for a known dtype.
+int check_type(const char *what, int32_t dtype);
+// Rows of `width` elements: 16-byte accesses at every multiple of 16 bytes.
+int check_rows(const char *what, int32_t dtype, const char *name, const void *p, uint32_t stride, uint64_t width, uint32_t n);
+// A call of one main kernel, between the caller's profile events.
+template <typename F>
+int timed(const char *what, hipStream_t st, F launch) {
+  prof_record(0, st);
+  prof_record(1, st);
+  const int e = launch_status(launch(), what);
+  prof_record(2, st);
+  prof_record(3, st);
+  return e;
+}
 inline bool aligned16(const void *p) { return ((uintptr_t)p & 15u) == 0; }
 constexpr uint32_t kMaxRows = 16384;  // of any call's batch
 

@@ -24,13 +24,16 @@
 // byte permutes (the two layouts differ by exactly that transpose), the
 // quad's index fastest over the lanes so that four lanes store 16 bytes side
 // by side.
+#include <algorithm>
+#include <climits>
+
 #include "common.hpp"
+#include "e4m3.hpp"
 #include "verify.hpp"
 
 namespace lora {
 
 constexpr int kKvThreads = 256;
-constexpr int kExpMin = 10, kExpMax = 247;  // 2^-117 .. 2^120
 
 // The pages that a sequence's rows touch: logical pages [p0, p0 + count).
 __device__ __forceinline__ int touched(const KvDev &a, const SeqDev &s, int *p0) {
@@ -85,57 +88,6 @@ __device__ __forceinline__ void transpose4(uint32_t w[4]) {
   w[3] = __builtin_amdgcn_perm(d, b, 0x07060302);
 }
 
-// Four values of a row as f32, from registers.
-template <typename T>
-struct Raw4;
-template <>
-struct Raw4<float> {
-  uint4 r;
-  __device__ void load(const float *p) { r = ldg16(p); }
-  __device__ void zero() { r = z4(); }
-  __device__ float at(int i) const { return __uint_as_float(i == 0 ? r.x : i == 1 ? r.y : i == 2 ? r.z : r.w); }
-};
-template <>
-struct Raw4<u16> {
-  uint2 r;
-  __device__ void load(const u16 *p) {
-    typedef unsigned u32x2n __attribute__((ext_vector_type(2)));
-    const u32x2n v = *(const __attribute__((address_space(1))) u32x2n *)(uintptr_t)p;
-    r = make_uint2(v.x, v.y);
-  }
-  __device__ void zero() { r = make_uint2(0u, 0u); }
-  __device__ float at(int i) const {
-    const uint32_t w = i < 2 ? r.x : r.y;
-    return __uint_as_float(i & 1 ? w & 0xffff0000u : w << 16);
-  }
-};
-
-// |x|'s bits where x is finite, 0 elsewhere: unsigned order is magnitude order.
-__device__ __forceinline__ uint32_t finite_bits(float x) {
-  const uint32_t b = __float_as_uint(x) & 0x7fffffffu;
-  return b < 0x7f800000u ? b : 0u;
-}
-
-// The exponent byte for a largest magnitude m 2^(E - 127), 1 <= m < 2: 448 is
-// 1.75 2^8, so 2^(E - 135) does where m <= 1.75 and twice that elsewhere.
-__device__ __forceinline__ int exp_for(uint32_t amax_bits) {
-  const int e = (int)(amax_bits >> 23) - 8 + ((amax_bits & 0x7fffffu) > 0x600000u);
-  return min(max(e, kExpMin), kExpMax);
-}
-
-// Four scaled values as codes; infinities and NaN become NaN, so that they
-// show in what reads them.  The conversion rounds to nearest, ties to even,
-// and nothing exceeds 448.
-__device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d, float inv) {
-  const float qnan = __uint_as_float(0x7fc00000u);
-  a = finite_bits(a) || a == 0.f ? a * inv : qnan;
-  b = finite_bits(b) || b == 0.f ? b * inv : qnan;
-  c = finite_bits(c) || c == 0.f ? c * inv : qnan;
-  d = finite_bits(d) || d == 0.f ? d * inv : qnan;
-  int w = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
-  return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(c, d, w, true);
-}
-
 // Four codes moved by a power of two: exact while normal, rounded to nearest even below.
 __device__ __forceinline__ uint32_t moved4(uint32_t w, int by) {
   const f32x2 a = __builtin_amdgcn_cvt_pk_f32_fp8((int)w, false), b = __builtin_amdgcn_cvt_pk_f32_fp8((int)w, true);
@@ -152,20 +104,18 @@ __device__ __forceinline__ uint32_t byte_mask(int t0, int lo, int hi) {
 __device__ __forceinline__ void st4(uint32_t *p, uint32_t v) { *p = v; }
 
 // ---------------------------------------------------------------- write
-// Grid: touched pages x heads x {K, V}.  IT items of 16 values per thread
-// cover the page (P D = 16 IT 256 at most).
+// One (page, head) of K or of V.  IT items of 16 values per thread cover the
+// page (P D = 16 IT 256 at most).
 template <typename T, int D, int IT>
-__global__ __launch_bounds__(kKvThreads) void kv_write_kernel(KvDev a, const T *krows, int k_stride, const T *vrows,
-                                                              int v_stride) {
-  __shared__ uint32_t wave_max[kKvThreads / 64];
+__device__ __forceinline__ void write_page(const KvDev &a, int u, int h, bool is_v, const T *krows, int k_stride, const T *vrows,
+                                           int v_stride, uint32_t *wave_max) {
   const int tid = threadIdx.x, lane = tid & 63;
   SeqDev s;
   int seq, lp;
-  if (!find_page(a, blockIdx.x, lane, &s, &seq, &lp)) return;
+  if (!find_page(a, u, lane, &s, &seq, &lp)) return;
   const int page = page_of(a, seq, lp);
   if (page < 0) return;
-  const int h = blockIdx.y, P = 1 << a.page_shift, t_page = lp << a.page_shift;
-  const bool is_v = blockIdx.z != 0;
+  const int P = 1 << a.page_shift, t_page = lp << a.page_shift;
   // new tokens of the page [t0, t1), and the first's row
   const int t0 = max(s.start - t_page, 0), t1 = min(s.len - t_page, P);
   const long long row0 = (long long)s.row0 + (t_page - s.start);  // row of the page's token 0, were it new
@@ -254,6 +204,263 @@ __global__ __launch_bounds__(kKvThreads) void kv_write_kernel(KvDev a, const T *
       }
     }
   }
+}
+
+// Grid: touched pages x heads x {K, V}.
+template <typename T, int D, int IT>
+__global__ __launch_bounds__(kKvThreads) void kv_write_kernel(KvDev a, const T *krows, int k_stride, const T *vrows,
+                                                              int v_stride) {
+  __shared__ uint32_t wave_max[kKvThreads / 64];
+  write_page<T, D, IT>(a, blockIdx.x, blockIdx.y, blockIdx.z != 0, krows, k_stride, vrows, v_stride, wave_max);
+}
+
+// ---------------------------------------------------------------- write with rotation
+// Pair i of a head's first `rot` dims turns by the angle p inv_freq[i] of its
+// token's position p:
+//     (x, y) -> (x cos - y sin, y cos + x sin).
+// An item is eight pairs of one token, 16 dims: pairs (i, i + rot/2) take
+// eight dims of either half, interleaved ones (2i, 2i + 1) and dims past
+// `rot` sixteen side by side.
+//
+// The angle of a far position loses digits in 32 bits (p = 131071 at frequency
+// 1: 0.008 of a turn's 2 pi in steps), so it is formed and reduced in 64.
+// Keys are turned in 64 bits as well and rounded once to f32, so that the
+// scale of a page and the codes next to a rounding border follow from the
+// numbers and not from the order of operations; that costs nothing, 64-bit
+// arithmetic running at the f32 rate here and memory bounding the call.
+// Queries are turned in 32 bits from the same cosines.
+template <typename T>
+struct Raw8 {
+  static constexpr int NV = sizeof(T) / 2;
+  uint4 r[NV];
+  __device__ void load(const T *p) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) r[i] = ldg16((const char *)p + 16 * i);
+  }
+  __device__ float at(int i) const {
+    if constexpr (sizeof(T) == 4) {
+      const uint4 v = r[i / 4];
+      return __uint_as_float(i % 4 == 0 ? v.x : i % 4 == 1 ? v.y : i % 4 == 2 ? v.z : v.w);
+    } else {
+      const uint4 v = r[0];
+      const uint32_t w = i < 2 ? v.x : i < 4 ? v.y : i < 6 ? v.z : v.w;
+      return __uint_as_float(i & 1 ? w & 0xffff0000u : w << 16);
+    }
+  }
+};
+
+// cos and sin by Taylor's series on [-pi/4, pi/4], to 1e-16: quarter turns are
+// taken off first, pi/2 in two parts so that up to 2^30 of them lose nothing.
+__device__ __forceinline__ void cos_sin(double a, double *c, double *s) {
+  if (!(fabs(a) < 1073741824.0)) {
+    sincos(a, s, c);
+    return;
+  }
+  const double n = rint(a * 0.63661977236758134308);
+  double r = fma(-n, 1.57079632679489655800, a);
+  r = fma(-n, 6.12323399573676603587e-17, r);
+  const double q = r * r;
+  double sp = -1.0 / 1307674368000.0, cp = 1.0 / 20922789888000.0;
+  sp = fma(sp, q, 1.0 / 6227020800.0);
+  cp = fma(cp, q, -1.0 / 87178291200.0);
+  sp = fma(sp, q, -1.0 / 39916800.0);
+  cp = fma(cp, q, 1.0 / 479001600.0);
+  sp = fma(sp, q, 1.0 / 362880.0);
+  cp = fma(cp, q, -1.0 / 3628800.0);
+  sp = fma(sp, q, -1.0 / 5040.0);
+  cp = fma(cp, q, 1.0 / 40320.0);
+  sp = fma(sp, q, 1.0 / 120.0);
+  cp = fma(cp, q, -1.0 / 720.0);
+  sp = fma(sp, q, -1.0 / 6.0);
+  cp = fma(cp, q, 1.0 / 24.0);
+  cp = fma(cp, q, -0.5);
+  sp = fma(sp * q, r, r);
+  cp = fma(cp, q, 1.0);
+  const int k = (int)n;
+  const double x = k & 1 ? sp : cp, y = k & 1 ? cp : sp;
+  *c = (k + 1) & 2 ? -x : x;
+  *s = k & 2 ? -y : y;
+}
+
+// The dims of item c of a head: eight at d0, eight at d1; whether they turn.
+__device__ __forceinline__ bool item_dims(const RotaryDev &rot, int c, int *d0, int *d1) {
+  const bool turns = c < rot.rot / 16;
+  const bool split = turns && !rot.interleaved;
+  *d0 = split ? 8 * c : 16 * c;
+  *d1 = split ? rot.rot / 2 + 8 * c : 16 * c + 8;
+  return turns;
+}
+
+template <typename T, int D, int IT>
+__device__ __forceinline__ void write_turned_page(const KvDev &a, const RotaryDev &rot, int u, int h, const T *krows, int k_stride,
+                                                  uint32_t *wave_max) {
+  const int tid = threadIdx.x, lane = tid & 63;
+  SeqDev s;
+  int seq, lp;
+  if (!find_page(a, u, lane, &s, &seq, &lp)) return;
+  const int page = page_of(a, seq, lp);
+  if (page < 0) return;
+  const int P = 1 << a.page_shift, t_page = lp << a.page_shift;
+  const int t0 = max(s.start - t_page, 0), t1 = min(s.len - t_page, P);
+  const long long row0 = (long long)s.row0 + (t_page - s.start);  // row of the page's token 0, were it new
+  uint8_t *codes = a.k + ((size_t)page * a.H + h) * ((size_t)P * D);
+  uint8_t *ep = a.ke + (size_t)page * a.H + h;
+  const int before = t0 > 0 ? *ep : 0;
+  const T *src = krows + (size_t)h * D;
+  const int items = P * D / 16;
+  // 256 is a multiple of a token's D / 16 items: a thread has the same dims of every token
+  static_assert(kKvThreads % (D / 16) == 0, "a thread's items share their dims");
+  const int c = tid % (D / 16);
+  int d0, d1;
+  const bool turns = item_dims(rot, c, &d0, &d1);
+
+  Raw8<T> raw[IT][2];
+#pragma unroll
+  for (int j = 0; j < IT; ++j) {
+    const int it = tid + j * kKvThreads, t = it / (D / 16);
+    if (it < items && t >= t0 && t < t1) {
+      const T *p = src + (size_t)(row0 + t) * k_stride;
+      raw[j][0].load(p + d0);
+      raw[j][1].load(p + d1);
+    }
+  }
+  double f[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) f[i] = turns ? (double)rot.inv_freq[8 * c + i] : 0.0;
+  float x[IT][16];
+  uint32_t big = 0;
+#pragma unroll
+  for (int j = 0; j < IT; ++j) {
+    const int it = tid + j * kKvThreads, t = it / (D / 16);
+    const bool live = it < items && t >= t0 && t < t1;
+#pragma unroll
+    for (int e = 0; e < 16; ++e) x[j][e] = live ? raw[j][e / 8].at(e % 8) : 0.f;
+    if (live && turns) {
+      const double p = (double)(t_page + t);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        double cs, sn;
+        cos_sin(p * f[i], &cs, &sn);
+        if (rot.interleaved) {
+          const double v = x[j][2 * i], w = x[j][2 * i + 1];
+          x[j][2 * i] = (float)(v * cs - w * sn);
+          x[j][2 * i + 1] = (float)(w * cs + v * sn);
+        } else {
+          const double v = x[j][i], w = x[j][i + 8];
+          x[j][i] = (float)(v * cs - w * sn);
+          x[j][i + 8] = (float)(w * cs + v * sn);
+        }
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < 16; ++e) big = max(big, finite_bits(x[j][e]));
+  }
+  big = (uint32_t)wave_reduce((int)big, 0, [](int a, int b) { return max(a, b); });  // bits of finite numbers: no sign
+  if (lane == 0) wave_max[tid >> 6] = big;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kKvThreads / 64; ++w) big = max(big, wave_max[w]);
+  const int e = min(max(before, exp_for(big)), kExpMax);
+  const int by = before - e;  // old tokens move by 2^by
+  const bool move = t0 > 0 && by != 0;
+  const float inv = __uint_as_float((uint32_t)(254 - e) << 23);
+  if (tid == 0) *ep = (uint8_t)e;
+#pragma unroll
+  for (int j = 0; j < IT; ++j) {
+    const int it = tid + j * kKvThreads, t = it / (D / 16);
+    if (it >= items) continue;
+    uint8_t *row = codes + (t >> 4) * (16 * D) + ((t >> 2) & 3) * (4 * D) + (t & 3) * 16;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int d = i ? d1 : d0;
+      uint2 *p = (uint2 *)(row + d / 16 * 64 + d % 16);
+      const float *y = x[j] + 8 * i;
+      if (t >= t0 && t < t1) *p = make_uint2(codes4(y[0], y[1], y[2], y[3], inv), codes4(y[4], y[5], y[6], y[7], inv));
+      else if (move && t < t0) *p = make_uint2(moved4(p->x, by), moved4(p->y, by));
+    }
+  }
+}
+
+// Queries: a workgroup takes 256 / (D/16) rows and `per` heads of them; a
+// thread has one row's item, its cosines in registers, and walks the heads.
+template <typename T, int D>
+__device__ __forceinline__ void turn_queries(const KvDev &a, const RotaryDev &rot, const TurnArgs &q, int block, int *pos) {
+  constexpr int kRows = kKvThreads / (D / 16);
+  const int tid = threadIdx.x;
+  const int rb = block / q.groups, r0 = rb * kRows, h0 = (block - rb * q.groups) * q.per;
+  if (tid < kRows) pos[tid] = INT_MIN;
+  __syncthreads();
+  // every sequence with rows among the workgroup's leaves their positions; a row of none has none
+  for (int i = tid; i < a.n_seqs; i += kKvThreads) {
+    if (a.indptr[i + 1] <= r0 || a.indptr[i] >= r0 + kRows) continue;
+    const SeqDev s = load_seq(a, i);
+    for (int r = max(s.row0, r0); r < min(s.row0 + s.rows, r0 + kRows); ++r) pos[r - r0] = s.start + (r - s.row0);
+  }
+  __syncthreads();
+  const int c = tid % (D / 16), r = r0 + tid / (D / 16), p = pos[tid / (D / 16)];
+  if (p == INT_MIN) return;
+  int d0, d1;
+  const bool turns = item_dims(rot, c, &d0, &d1);
+  float cs[8], sn[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    double x = 1.0, y = 0.0;
+    if (turns) cos_sin((double)p * (double)rot.inv_freq[8 * c + i], &x, &y);
+    cs[i] = (float)x;
+    sn[i] = (float)y;
+  }
+  const T *src = (const T *)q.q + (size_t)r * q.q_stride;
+  T *dst = (T *)q.out + (size_t)r * q.out_stride;
+#pragma unroll 4
+  for (int h = h0; h < min(h0 + q.per, q.heads); ++h) {
+    Raw8<T> in[2];
+    in[0].load(src + (size_t)h * D + d0);
+    in[1].load(src + (size_t)h * D + d1);
+    float x[16];
+#pragma unroll
+    for (int e = 0; e < 16; ++e) x[e] = in[e / 8].at(e % 8);
+    if (turns) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        if (rot.interleaved) {
+          const float v = x[2 * i], w = x[2 * i + 1];
+          x[2 * i] = fmaf(v, cs[i], -w * sn[i]);
+          x[2 * i + 1] = fmaf(w, cs[i], v * sn[i]);
+        } else {
+          const float v = x[i], w = x[i + 8];
+          x[i] = fmaf(v, cs[i], -w * sn[i]);
+          x[i + 8] = fmaf(w, cs[i], v * sn[i]);
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      T *to = dst + (size_t)h * D + (i ? d1 : d0);
+      const float *y = x + 8 * i;
+      if constexpr (sizeof(T) == 4) {
+        ((float4 *)to)[0] = make_float4(y[0], y[1], y[2], y[3]);
+        ((float4 *)to)[1] = make_float4(y[4], y[5], y[6], y[7]);
+      } else {
+        *(uint4 *)to = make_uint4(pack2(f2bf(y[0]), f2bf(y[1])), pack2(f2bf(y[2]), f2bf(y[3])), pack2(f2bf(y[4]), f2bf(y[5])),
+                                  pack2(f2bf(y[6]), f2bf(y[7])));
+      }
+    }
+  }
+}
+
+// Grid: touched pages x {K, V} x heads, heads fastest, then the queries' workgroups.
+template <typename T, int D, int IT>
+__global__ __launch_bounds__(kKvThreads) void kv_write_rotary_kernel(KvDev a, RotaryDev rot, TurnArgs q, const T *krows,
+                                                                     int k_stride, const T *vrows, int v_stride) {
+  __shared__ uint32_t wave_max[kKvThreads / 64];
+  __shared__ int pos[64];
+  if ((int)blockIdx.x >= q.first) {
+    turn_queries<T, D>(a, rot, q, blockIdx.x - q.first, pos);
+    return;
+  }
+  const int both = blockIdx.x / a.H, h = blockIdx.x - both * a.H;
+  if (both & 1) write_page<T, D, IT>(a, both >> 1, h, true, krows, k_stride, vrows, v_stride, wave_max);
+  else write_turned_page<T, D, IT>(a, rot, both >> 1, h, krows, k_stride, wave_max);
 }
 
 // ---------------------------------------------------------------- read
@@ -372,6 +579,20 @@ struct ReadK {
       hipLaunchKernelGGL((kv_read_kernel<T, D, IT>), dim3(grid.y, grid.x, 2), dim3(kKvThreads), 0, st, kv, (T *)k, ks, (T *)v, vs);
   }
 };
+// Heads of a queries' workgroup: as many as leave the card enough of them.
+template <typename T, int D, int IT>
+struct RotaryK {
+  static void go(dim3 grid, hipStream_t st, const KvDev &kv, RotaryDev rot, TurnArgs q, const void *k, int ks, const void *v, int vs) {
+    if constexpr (IT * kKvThreads * 16 <= D * 128) {
+      const int rows = kKvThreads / (D / 16), row_blocks = (kv.n + rows - 1) / rows;
+      q.per = std::max(1, std::min(q.heads, q.heads * row_blocks / 1024));
+      q.groups = (q.heads + q.per - 1) / q.per;
+      q.first = (int)(grid.x * grid.y * 2);
+      hipLaunchKernelGGL((kv_write_rotary_kernel<T, D, IT>), dim3(q.first + row_blocks * q.groups), dim3(kKvThreads), 0, st, kv, rot,
+                         q, (const T *)k, ks, (const T *)v, vs);
+    }
+  }
+};
 template <template <typename, int, int> class K, typename... A>
 static hipError_t launch_by_type(const KvDev &kv, int dim, int dtype, hipStream_t st, A... args) {
   if (dtype == 0) {
@@ -389,6 +610,10 @@ static hipError_t launch_by_type(const KvDev &kv, int dim, int dtype, hipStream_
 hipError_t launch_kv_write(const KvDev &kv, int dim, int dtype, const void *k, int k_stride, const void *v, int v_stride,
                            hipStream_t st) {
   return launch_by_type<WriteK>(kv, dim, dtype, st, k, k_stride, v, v_stride);
+}
+hipError_t launch_kv_write_rotary(const KvDev &kv, const RotaryDev &rot, const TurnArgs &q, int dim, int dtype, const void *k,
+                                  int k_stride, const void *v, int v_stride, hipStream_t st) {
+  return launch_by_type<RotaryK>(kv, dim, dtype, st, rot, q, k, k_stride, v, v_stride);
 }
 hipError_t launch_kv_read(const KvDev &kv, int dim, int dtype, void *k, int k_stride, void *v, int v_stride,
                           hipStream_t st) {

@@ -5,6 +5,7 @@
 #include <stdint.h>
 
 #include "common.hpp"
+#include "e4m3.hpp"
 
 namespace lora {
 
@@ -80,10 +81,8 @@ __device__ __forceinline__ SeqDev seq_of_lane(const SeqDev &s, int lane) {
 }
 
 // The e4m3 byte pair conversions (gfx950).
-typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
-typedef float f32x2 __attribute__((ext_vector_type(2)));
 
 hipError_t launch_kv_write(const KvDev &kv, int dim, int dtype, const void *k, int k_stride, const void *v, int v_stride,
                            hipStream_t st);
@@ -105,6 +104,21 @@ inline FastDiv fast_div(int d) {
   f.m = (uint32_t)((1ull << (31 + f.s)) / (uint64_t)d + 1);
   return f;
 }
+
+// The rotation on the way into the cache (lora_rotary), and the queries that turn beside the keys.
+struct RotaryDev {
+  const float *inv_freq;  // [rot / 2]
+  int rot;                // dims of a head that turn, a multiple of 16
+  bool interleaved;       // pairs (2i, 2i + 1); otherwise (i, i + rot / 2)
+};
+struct TurnArgs {
+  const void *q;
+  void *out;
+  int q_stride, out_stride, heads;
+  int per, groups, first;  // heads of a workgroup, workgroups of a row, the grid's first: set by the launcher
+};
+hipError_t launch_kv_write_rotary(const KvDev &kv, const RotaryDev &rot, const TurnArgs &q, int dim, int dtype, const void *k,
+                                  int k_stride, const void *v, int v_stride, hipStream_t st);
 
 // The attention over the cache (k_attend.hip).
 // A chunk of a split unit leaves [CB][D] sums, then M, Ml and l per column,
@@ -212,6 +226,20 @@ ScoreSplit score_split(int n, int n_vocab, int dtype);
 // Bytes of one chunk's record: maximum, sum, weighted sum, count, then the top keys.
 __host__ __device__ inline size_t score_record_bytes(int top) { return 16 + 8 * (size_t)((top + 1) / 2 * 2); }
 hipError_t launch_score(const ScoreArgs &a, int dtype, hipStream_t st);
+
+// Tokens drawn from rows of logits (k_sample.hip).
+constexpr int kSampleThreads = 256;
+struct SampleArgs {
+  const void *logits;  // [n][stride]
+  long long stride;
+  int n, n_vocab;
+  const float *temperature, *top_p, *min_p;  // [n], or null
+  const int32_t *top_k;                      // [n] or null
+  const float *uniform;                      // [n]
+  int32_t *ids;                              // [n]
+  float *logp;                               // [n] or null
+};
+hipError_t launch_sample(const SampleArgs &a, int dtype, hipStream_t st);
 
 // Upper bound of the pages that n rows of n_seqs sequences touch: a sequence
 // of m rows touches at most m pages and at most (m + P - 2) / P + 1.

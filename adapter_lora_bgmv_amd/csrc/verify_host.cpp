@@ -15,15 +15,32 @@
 
 using namespace lora;
 
-namespace {
-
-size_t up256(size_t v) { return (v + 255) & ~(size_t)255; }
+namespace lora {
 
 int check_type(const char *what, int32_t dtype) {
   if (dtype != LORA_F32 && dtype != LORA_BF16)
     return fail(LORA_ERR_DTYPE, "%s: dtype %d is neither LORA_F32 (0) nor LORA_BF16 (1)", what, dtype);
   return LORA_OK;
 }
+
+int check_rows(const char *what, int32_t dtype, const char *name, const void *p, uint32_t stride, uint64_t width, uint32_t n) {
+  const uint32_t unit = dtype == LORA_BF16 ? 8 : 4;
+  if (stride < width)
+    return fail(LORA_ERR_STRIDE, "%s: %s row stride %u < its row of %llu elements", what, name, stride, (unsigned long long)width);
+  if (stride > (uint32_t)INT_MAX)
+    return fail(LORA_ERR_STRIDE, "%s: %s row stride %u exceeds %d", what, name, stride, INT_MAX);
+  if (stride % unit)
+    return fail(LORA_ERR_UNSUPPORTED, "%s: %s row stride %u must be a multiple of %u", what, name, stride, unit);
+  if (n && !p) return fail(LORA_ERR_NULL_PTR, "%s: %s must be non-NULL", what, name);
+  if (n && !aligned16(p)) return fail(LORA_ERR_UNSUPPORTED, "%s: %s %p must be 16-byte aligned", what, name, p);
+  return LORA_OK;
+}
+
+}  // namespace lora
+
+namespace {
+
+size_t up256(size_t v) { return (v + 255) & ~(size_t)255; }
 
 // The cache and the sequences of a call of n rows; fills *d.
 int check_kv(const char *what, const lora_kv_cache *c, const lora_kv_seqs *s, uint32_t n, KvDev *d) {
@@ -72,30 +89,6 @@ int check_kv(const char *what, const lora_kv_cache *c, const lora_kv_seqs *s, ui
   d->n_seqs = (int)s->n_seqs;
   d->n = (int)n;
   return LORA_OK;
-}
-
-// Rows of `width` elements: 16-byte accesses at every head.
-int check_rows(const char *what, int32_t dtype, const char *name, const void *p, uint32_t stride, uint64_t width, uint32_t n) {
-  const uint32_t unit = dtype == LORA_BF16 ? 8 : 4;
-  if (stride < width)
-    return fail(LORA_ERR_STRIDE, "%s: %s row stride %u < its row of %llu elements", what, name, stride, (unsigned long long)width);
-  if (stride > (uint32_t)INT_MAX)
-    return fail(LORA_ERR_STRIDE, "%s: %s row stride %u exceeds %d", what, name, stride, INT_MAX);
-  if (stride % unit)
-    return fail(LORA_ERR_UNSUPPORTED, "%s: %s row stride %u must be a multiple of %u", what, name, stride, unit);
-  if (n && !p) return fail(LORA_ERR_NULL_PTR, "%s: %s must be non-NULL", what, name);
-  if (n && !aligned16(p)) return fail(LORA_ERR_UNSUPPORTED, "%s: %s %p must be 16-byte aligned", what, name, p);
-  return LORA_OK;
-}
-
-template <typename F>
-int timed(const char *what, hipStream_t st, F launch) {
-  prof_record(0, st);
-  prof_record(1, st);
-  const int e = launch_status(launch(), what);
-  prof_record(2, st);
-  prof_record(3, st);
-  return e;
 }
 
 // Which forms an attention call launches.  Sequences of up to
@@ -159,6 +152,49 @@ int lora_kv_write(const lora_kv_cache *cache, const lora_kv_seqs *seqs, int32_t 
   hipStream_t st = (hipStream_t)stream;
   return timed(what, st, [&] {
     return launch_kv_write(d, (int)cache->head_dim, dtype, k, (int)k_row_stride, v, (int)v_row_stride, st);
+  });
+}
+
+int lora_kv_write_rotary(const lora_kv_cache *cache, const lora_kv_seqs *seqs, const lora_rotary *rotary, int32_t dtype,
+                         uint32_t n_heads, const void *q, uint32_t q_row_stride, void *q_out, uint32_t q_out_row_stride,
+                         const void *k, uint32_t k_row_stride, const void *v, uint32_t v_row_stride, uint32_t n, void *stream) {
+  clear_err();
+  const char *what = "lora_kv_write_rotary";
+  KvDev d{};
+  if (int e = check_type(what, dtype)) return e;
+  if (int e = check_kv(what, cache, seqs, n, &d)) return e;
+  if (!rotary || !rotary->inv_freq)
+    return fail(LORA_ERR_NULL_PTR, "%s: rotary %p and its inv_freq must be non-NULL", what, (const void *)rotary);
+  if ((uintptr_t)rotary->inv_freq % 4)
+    return fail(LORA_ERR_UNSUPPORTED, "%s: inv_freq %p must be aligned to its 4 bytes", what, (const void *)rotary->inv_freq);
+  if (rotary->rot_dim == 0 || rotary->rot_dim > cache->head_dim || rotary->rot_dim % 16)
+    return fail(LORA_ERR_UNSUPPORTED, "%s: rot_dim %u must be a multiple of 16, at most head_dim %u", what, rotary->rot_dim,
+                cache->head_dim);
+  if (rotary->interleaved != 0 && rotary->interleaved != 1)
+    return fail(LORA_ERR_UNSUPPORTED, "%s: interleaved %d must be 0 or 1", what, rotary->interleaved);
+  if (n_heads > 65535) return fail(LORA_ERR_SHAPE, "%s: n_heads %u exceeds 65535", what, n_heads);
+  const uint64_t row = (uint64_t)cache->n_kv_heads * cache->head_dim, q_row = (uint64_t)n_heads * cache->head_dim;
+  if (n_heads) {
+    if (int e = check_rows(what, dtype, "q", q, q_row_stride, q_row, n)) return e;
+    if (int e = check_rows(what, dtype, "q_out", q_out, q_out_row_stride, q_row, n)) return e;
+    if (n && q == q_out && q_row_stride != q_out_row_stride)
+      return fail(LORA_ERR_STRIDE, "%s: in place, q row stride %u and q_out row stride %u must be equal", what, q_row_stride,
+                  q_out_row_stride);
+  }
+  if (int e = check_rows(what, dtype, "k", k, k_row_stride, row, n)) return e;
+  if (int e = check_rows(what, dtype, "v", v, v_row_stride, row, n)) return e;
+  if (n == 0) return LORA_OK;
+  const uint64_t grid = 2ull * kv_max_touched((int)n, (int)seqs->n_seqs, (int)cache->page_tokens) * cache->n_kv_heads +
+                        (uint64_t)n_heads * n;
+  if (grid > (uint64_t)INT_MAX)
+    return fail(LORA_ERR_SHAPE, "%s: n %u rows of n_kv_heads %u and n_heads %u need more than 2^31 - 1 workgroups", what, n,
+                cache->n_kv_heads, n_heads);
+  if (int e = check_device(what)) return e;
+  const RotaryDev rot{rotary->inv_freq, (int)rotary->rot_dim, rotary->interleaved != 0};
+  const TurnArgs turn{q, q_out, (int)q_row_stride, (int)q_out_row_stride, (int)n_heads, 0, 0, 0};
+  hipStream_t st = (hipStream_t)stream;
+  return timed(what, st, [&] {
+    return launch_kv_write_rotary(d, rot, turn, (int)cache->head_dim, dtype, k, (int)k_row_stride, v, (int)v_row_stride, st);
   });
 }
 
@@ -305,6 +341,39 @@ int lora_token_logprobs(int32_t dtype, uint32_t n_vocab, const void *logits, uin
   a.part = (float *)((char *)workspace + up256((size_t)n * 4));
   hipStream_t st = (hipStream_t)stream;
   return timed(what, st, [&] { return launch_score(a, dtype, st); });
+}
+
+size_t lora_token_sample_workspace_bytes(int32_t, uint32_t, uint32_t) { return 0; }
+
+int lora_token_sample(int32_t dtype, uint32_t n_vocab, const void *logits, uint32_t row_stride, const float *temperature,
+                      const int32_t *top_k, const float *top_p, const float *min_p, const float *uniform, uint32_t n, int32_t *ids,
+                      float *logp, void *workspace, size_t workspace_bytes, void *stream) {
+  clear_err();
+  const char *what = "lora_token_sample";
+  if (int e = check_type(what, dtype)) return e;
+  if (n_vocab == 0 || n_vocab > LORA_MAX_VOCAB)
+    return fail(LORA_ERR_SHAPE, "%s: n_vocab %u must be in 1..%u", what, n_vocab, LORA_MAX_VOCAB);
+  if (n > kMaxRows)
+    return fail(LORA_ERR_SHAPE, "%s: [n %u x n_vocab %u]: n exceeds the limit %u", what, n, n_vocab, kMaxRows);
+  if (row_stride < n_vocab)
+    return fail(LORA_ERR_STRIDE, "%s: row_stride %u < n_vocab %u", what, row_stride, n_vocab);
+  if (n == 0) return LORA_OK;
+  if (!logits || !uniform || !ids)
+    return fail(LORA_ERR_NULL_PTR, "%s: [n %u x n_vocab %u]: logits %p, uniform %p, ids %p must be non-NULL", what, n, n_vocab,
+                logits, (const void *)uniform, (const void *)ids);
+  const size_t size = dtype == LORA_F32 ? 4 : 2;
+  if ((uintptr_t)logits % size)
+    return fail(LORA_ERR_UNSUPPORTED, "%s: logits %p must be aligned to their %zu bytes", what, logits, size);
+  const size_t need = lora_token_sample_workspace_bytes(dtype, n_vocab, n);
+  if (need && (!workspace || workspace_bytes < need))
+    return fail(LORA_ERR_WORKSPACE, "%s: [n %u x n_vocab %u]: workspace %p of %zu bytes, %zu needed", what, n, n_vocab, workspace,
+                workspace_bytes, need);
+  if (need && !aligned16(workspace))
+    return fail(LORA_ERR_UNSUPPORTED, "%s: workspace %p is not 16-byte aligned", what, workspace);
+  if (int e = check_device(what)) return e;
+  const SampleArgs a{logits, row_stride, (int)n, (int)n_vocab, temperature, top_p, min_p, top_k, uniform, ids, logp};
+  hipStream_t st = (hipStream_t)stream;
+  return timed(what, st, [&] { return launch_sample(a, dtype, st); });
 }
 
 }  // extern "C"

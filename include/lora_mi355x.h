@@ -187,7 +187,7 @@ size_t lora_workspace_bytes(int32_t op, int32_t dtype, uint32_t n_rows, uint32_t
  * later fused call on the calling thread (lora_apply, lora_apply_segmented,
  * lora_apply_moe_gather, lora_apply_moe_grouped, lora_apply_stack,
  * lora_embed_rows, lora_kv_write, lora_kv_read, lora_kv_attend,
- * lora_token_logprobs) records on its stream events[0] before its first kernel, events[1] right before
+ * lora_token_logprobs, lora_kv_write_rotary, lora_token_sample, lora_quantize_fp8, lora_matmul_fp8) records on its stream events[0] before its first kernel, events[1] right before
  * its main kernel (after the route plan and shrink kernel where there is
  * one), events[2] right after the main kernel, and events[3] after its last
  * kernel (the decode epilogue, or a stack's further levels, where there are
@@ -477,6 +477,37 @@ int lora_kv_write(const lora_kv_cache *cache, const lora_kv_seqs *seqs, int32_t 
                   uint32_t k_row_stride, const void *v, uint32_t v_row_stride, uint32_t n, void *stream);
 
 /*
+ * The position rotation (rotary embedding) on the way into the cache: pair i
+ * of a head's first rot_dim dims turns by the angle p * inv_freq[i] of its
+ * row's position p,  (a, b) -> (a cos - b sin, b cos + a sin).  Pairs are (i,
+ * i + rot_dim/2) or, interleaved, (2i, 2i + 1); dims from rot_dim on stay.
+ * inv_freq is [dev] f32 [rot_dim/2], any numbers: a caller scales positions
+ * through them.  The struct itself is [host].
+ */
+typedef struct lora_rotary {
+  const float *inv_freq; /* [dev] [rot_dim / 2] */
+  uint32_t rot_dim;      /* a multiple of 16, at most head_dim */
+  int32_t interleaved;   /* 0 or 1 */
+} lora_rotary;
+
+/*
+ * lora_kv_write with the rotation: keys are turned and quantised into the
+ * cache, values quantised as they are, and the call's queries, q [dev]
+ * [n][q_row_stride] of n_heads heads, turned into q_out [dev]
+ * [n][q_out_row_stride], which may be q itself with the same stride but
+ * overlaps it in no other way.  n_heads 0 turns no queries (q and q_out are
+ * not read).  Positions are those of lora_kv_seqs; a query's row needs no
+ * page, its position may be past the table or below 0, and a row outside
+ * every sequence is not written.  Angles are formed and reduced in 64 bits;
+ * keys are turned in 64 bits and rounded once to f32, from which scale and
+ * codes follow as in lora_kv_write; queries are turned in f32 and rounded
+ * once.  A pair that holds an infinity or NaN is stored as NaN.  No workspace.
+ */
+int lora_kv_write_rotary(const lora_kv_cache *cache, const lora_kv_seqs *seqs, const lora_rotary *rotary, int32_t dtype,
+                         uint32_t n_heads, const void *q, uint32_t q_row_stride, void *q_out, uint32_t q_out_row_stride,
+                         const void *k, uint32_t k_row_stride, const void *v, uint32_t v_row_stride, uint32_t n, void *stream);
+
+/*
  * Reads the tokens of the call's rows back, the inverse of lora_kv_write with
  * the same arguments (with row_indptr the running sum of kv_len: whole
  * sequences).  The values are exact in either dtype, but for codes of 256 and
@@ -538,6 +569,78 @@ int lora_token_logprobs(int32_t dtype, uint32_t n_vocab, const void *logits, uin
                         const int32_t *token_ids, uint32_t n, uint32_t top, float *logp, float *entropy,
                         int32_t *rank, int32_t *top_ids, float *top_logp, void *workspace,
                         size_t workspace_bytes, void *stream);
+
+/*
+ * Draws one token of every row of logits x [dev] [n][row_stride >= n_vocab]
+ * (any alignment of whole elements; dtype is the logits').  With m the row's
+ * maximum and T its temperature, token t has the weight
+ *   W_t = rint(2^43 exp((x_t - m) / T)),
+ * a whole number, so that sums and with them the token depend on the row
+ * alone, not on the batch.  In the order by value, equal values by the lower
+ * index first, these stay:
+ *   the first top_k[i] tokens (all, where it is 0, negative or >= n_vocab);
+ *   of those the fewest first ones whose weights reach top_p[i] of theirs
+ *   (all, where it is 1 or more);
+ *   of those the ones of at least min_p[i] 2^43 (all, where it is 0 or less);
+ *   the first token always.
+ * ids[i] is the first token, by index, at which the running sum of the
+ * weights that stayed exceeds floor(uniform[i] * their sum), both products
+ * in 64-bit floating point; uniform below 0 counts as 0, and from 1 on takes
+ * the last token of a weight.  T = 0 takes the row's largest logit, the lowest
+ * index among equals.  logp[i] is the natural logarithm of the token's share
+ * of what stayed (0 for T = 0); logp may be NULL.  temperature, top_k, top_p
+ * and min_p are [dev] [n], each may be NULL: 1, 0, 1 and 0 for every row.
+ * Logits of -infinity are never drawn.  A row that holds NaN or +infinity or
+ * nothing but -infinity, whose temperature is negative, infinite or NaN, or
+ * whose top_p, min_p or uniform is NaN, has id -1 and logp NaN.  workspace
+ * [dev] of at least lora_token_sample_workspace_bytes(...) bytes, which may
+ * be 0, zero-filled before its first use with a shape; calls that may run at
+ * the same time need one each.
+ */
+size_t lora_token_sample_workspace_bytes(int32_t dtype, uint32_t n_vocab, uint32_t n);
+int lora_token_sample(int32_t dtype, uint32_t n_vocab, const void *logits, uint32_t row_stride, const float *temperature,
+                      const int32_t *top_k, const float *top_p, const float *min_p, const float *uniform, uint32_t n, int32_t *ids,
+                      float *logp, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * The base projection in 8 bits.  Activations and weights are e4m3 codes with
+ * an f32 scale for each block of 128 columns: of one row for activations, of
+ * 128 rows for weights.  The last blocks may be cut.
+ *
+ * lora_quantize_fp8 brings rows x [dev] [n_rows][x_row_stride] to codes [dev]
+ * [n_rows][codes_row_stride] bytes and scale [dev] f32 [ceil(n_rows /
+ * block_rows)][scale_row_stride >= ceil(k / 128)], block_rows 1 or 128.  A
+ * block's scale is the smallest power of two s with |x| <= 448 s for its
+ * finite values, within 2^-117 .. 2^120; codes are x / s, rounded once to
+ * nearest even, infinities and NaN as NaN.  k is a multiple of 16,
+ * codes_row_stride too, x_row_stride of 8 (bf16) or 4 (f32), x and codes
+ * 16-byte aligned.  No workspace.
+ */
+int lora_quantize_fp8(int32_t dtype, uint32_t n_rows, uint32_t k, const void *x, uint32_t x_row_stride, uint32_t block_rows,
+                      void *codes, uint32_t codes_row_stride, float *scale, uint32_t scale_row_stride, void *stream);
+
+/*
+ *   y[i][o] = sum over blocks b of x_scale[i][b] w_scale[o / 128][b] *
+ *             sum over k in b of x[i][k] W[o][k]
+ * with codes W [dev] [n_out][w_row_stride], x [dev] [n][x_row_stride] and
+ * their scales [dev], any f32 numbers, [ceil(n_out / 128)][w_scale_stride] and
+ * [n][x_scale_stride].  dtype is that of y [dev] [n][y_row_stride]; a LoRA
+ * term joins through lora_shrink and lora_expand_fold.  k_in is a multiple of
+ * 16, at most 65536, n_out of 8, strides of codes of 16, y_row_stride of 8
+ * (bf16) or 4 (f32), and codes and y are 16-byte aligned; n is limited to
+ * 16384.  The scaled sums of the blocks add up in f32 and y is rounded once.
+ * Within a block f32 calls keep f32 sums of the exact products, bf16 calls
+ * sums that are off by up to 2^-10 of the sum of the products' magnitudes,
+ * 2^-16 typically (what the 8-bit matrix instruction keeps).  The order of every sum follows
+ * from the sizes alone.  workspace [dev] of at least
+ * lora_matmul_fp8_workspace_bytes(...) bytes, which may be 0, zero-filled
+ * before its first use with a shape; calls that may run at the same time need
+ * one each.
+ */
+size_t lora_matmul_fp8_workspace_bytes(int32_t dtype, uint32_t n_out, uint32_t k_in, uint32_t n);
+int lora_matmul_fp8(int32_t dtype, uint32_t n_out, uint32_t k_in, const void *W, uint32_t w_row_stride, const float *w_scale,
+                    uint32_t w_scale_stride, const void *x, uint32_t x_row_stride, const float *x_scale, uint32_t x_scale_stride,
+                    uint32_t n, void *y, uint32_t y_row_stride, void *workspace, size_t workspace_bytes, void *stream);
 
 #ifdef __cplusplus
 }
