@@ -11,13 +11,29 @@
 // All filters keep a prefix of one order, by value, equal values by the lower
 // index first: top-k the first k, top-p the fewest whose weights reach p of
 // what top-k kept, min-p those of at least that part of the largest weight.
-// So a row needs one cut in that order: a value's key and the last index that
+// So a row needs one cut in that order, a value's key with the last index that
 // is kept among its equals.  Tokens are then run through by index, and the
 // first at which the running sum exceeds floor(u sum) is the row's.
 //
-// A cut is found by three histograms over the key's bits (11, 11 and 10), each
-// over the tokens of the bin that the one before found, counts for top-k and
-// weights for top-p, and the cut among equals by a count in order of index.
+// The exponent's whole steps, n = rint(256 log2(e) (x - m) / T), serve twice:
+// they pick 2^(n/256) from a table, and 16 of them are a bin.  Rows go by what
+// they ask for:
+//   top-k up to 512: the row's maximum comes with those of its parts, 32
+//     logits each.  The bin that k of these maxima reach bounds the k-th
+//     largest logit from below, so the few logits from there up are listed
+//     and everything else happens among them.
+//   top-p: the weights of every bin are summed, the bin in which the cut lies
+//     follows, its logits are listed, and the cut among them by their
+//     finer bins and then one by one.
+//   neither: the weights are summed.
+// Sums are kept for each segment of 2048 logits, a wave's 32 a lane.  The
+// segment that holds the number drawn is read again by the whole workgroup.
+// Where a list overflows (many equal logits), the cut is found by histograms
+// over the key's bits, 11, 11 and 10 of them, and a count in order of index.
+//
+// Few rows are spread over workgroups by kernels that each end where all of a
+// row is needed: maxima, sums and lists, lists of top-p's bin, the drawing.
+#include <algorithm>
 #include <climits>
 
 #include "common.hpp"
@@ -26,12 +42,22 @@
 namespace lora {
 
 typedef unsigned long long u64;
-constexpr int kSampleBins = 2048;
+constexpr int kRadixBins = 2048;
+constexpr int kBins = 768;           // of 16 steps, 1/16 of a power of two: 48 powers, beyond which weights are 0
+constexpr int kLowest = kBins - 1;   // holds weights of 0 only
+constexpr int kMostListedK = 512;    // top-k that goes by the parts' maxima
+constexpr int kParts = 4096;         // maxima that a row keeps at most
+constexpr int kWaves = kSampleThreads / 64;
+constexpr double kUnit = 8796093022208.0;  // 2^43
 
 __device__ __forceinline__ uint32_t sample_key(float x) {  // unsigned order is the value's; the zeros are equal
   const uint32_t b = __float_as_uint(x + 0.f);
   return b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
 }
+__device__ __forceinline__ float value_of(uint32_t key) { return __uint_as_float(key & 0x80000000u ? key ^ 0x80000000u : ~key); }
+// Larger values first, equal ones by the lower index.
+__device__ __forceinline__ u64 place_of(float x, int index) { return (u64)sample_key(x) << 32 | (uint32_t)~index; }
+__device__ __forceinline__ int index_of(u64 place) { return (int)~(uint32_t)place; }
 
 template <typename T>
 struct Logits;
@@ -41,7 +67,6 @@ struct Logits<float> {
   static __device__ float at(const uint4 &v, int e) {
     return __uint_as_float(e == 0 ? v.x : e == 1 ? v.y : e == 2 ? v.z : v.w);
   }
-  static __device__ float one(const float *p) { return *p; }
 };
 template <>
 struct Logits<u16> {
@@ -50,7 +75,6 @@ struct Logits<u16> {
     const uint32_t w = e < 2 ? v.x : e < 4 ? v.y : e < 6 ? v.z : v.w;
     return __uint_as_float(e & 1 ? w & 0xffff0000u : w << 16);
   }
-  static __device__ float one(const u16 *p) { return bf2f(*p); }
 };
 
 // Sum over the lanes up to and including this one, in registers (as wave_incl_scan, 64 bits).
@@ -72,48 +96,62 @@ __device__ __forceinline__ u64 lane_of64(u64 v, int lane) {
   return (u64)(uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(v >> 32), lane) << 32 |
          (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)v, lane);
 }
-
-// 2^43 2^t rounded to a whole number, for t <= 0.  Taylor's series of 2^f on
-// [-1/2, 1/2], to 1e-14; adding 2^52 rounds to nearest even and leaves the
-// number in the low bits.
-__device__ __forceinline__ u64 weight_of(double t) {
-  t = fmax(t, -64.0);  // rounds to 0 from -44 on; NaN is kept out by the callers
-  const double n = rint(t), f = (t - n) * 0.69314718055994530942;
-  double p = 1.0 / 479001600.0;
-  p = fma(p, f, 1.0 / 39916800.0);
-  p = fma(p, f, 1.0 / 3628800.0);
-  p = fma(p, f, 1.0 / 362880.0);
-  p = fma(p, f, 1.0 / 40320.0);
-  p = fma(p, f, 1.0 / 5040.0);
-  p = fma(p, f, 1.0 / 720.0);
-  p = fma(p, f, 1.0 / 120.0);
-  p = fma(p, f, 1.0 / 24.0);
-  p = fma(p, f, 1.0 / 6.0);
-  p = fma(p, f, 0.5);
-  p = fma(p, f, 1.0);
-  p = fma(p, f, 1.0);
-  const double w = ldexp(p, (int)n + 43) + 4503599627370496.0;
-  return (u64)__double_as_longlong(w) & 0xfffffffffffffull;
-}
+__device__ __forceinline__ u64 wave_sum64(u64 v) { return lane_of64(wave_scan64(v), 63); }
 
 struct SampleLds {
-  u64 bins[kSampleBins];
-
-  u64 scan[4];
+  double table[256];  // 2^43 2^(j/256)
+  u64 bins[kBins];
+  u64 seg[kSampleMaxSegs];
+  union {
+    struct {
+      u64 list[kSampleList], w[kSampleList];
+    };
+    float parts[kParts];
+    u64 radix[kRadixBins];
+  };
+  u64 scan[kWaves];
   u64 found_above;
-  int found, index;
-  float m[4];
-  int bad;
+  float m[kWaves];
+  int found, index, count, picked, bad;
 };
 
-// The row, as the kernel's phases see it.
+// A row and its settings.  cut: what is kept so far, places from `cut` up.
 template <typename T>
 struct Row {
-  static constexpr int VE = Logits<T>::N;
+  static constexpr int VE = Logits<T>::N, NV = kSampleSeg / 64 / VE;
   const T *x;
-  int V, skew, tiles;  // a tile: VE logits of every thread
+  int V, skew, segs;
   float m;
-  double per;  // log2(e) / T
+  double steps;  // 256 log2(e) / T
+  u64 cut, least;
+  int top_k;
+  float temp, top_p, min_p, u;
+  bool greedy;
+
+  __device__ void begin(const SampleArgs &a, int r) {
+    x = (const T *)a.logits + (long long)r * a.stride;
+    V = a.n_vocab;
+    skew = (int)(((uintptr_t)x & 15) / sizeof(T));
+    segs = (V + skew + kSampleSeg - 1) / kSampleSeg;
+    temp = a.temperature ? a.temperature[r] : 1.f;
+    top_p = a.top_p ? a.top_p[r] : 1.f;
+    min_p = a.min_p ? a.min_p[r] : 0.f;
+    top_k = a.top_k ? a.top_k[r] : 0;
+    u = a.uniform[r];
+    greedy = temp == 0.f;
+    if (greedy || min_p > 1.f) top_k = 1;
+    if (top_k >= V || top_k < 0) top_k = 0;
+    if (top_k == 1) top_p = 1.f;
+    cut = 0;
+    least = min_p > 0.f && min_p <= 1.f ? (u64)ceil((double)min_p * kUnit) : 0;
+  }
+  // False for a row without a distribution; max is NaN where the row holds one.
+  __device__ bool set_max(float max) {
+    m = max;
+    steps = 369.32993046757463228 / (greedy ? 1.0 : (double)temp);
+    return fabsf(max) < INFINITY && temp >= 0.f && temp < INFINITY && top_p == top_p && min_p == min_p && u == u;
+  }
+  __device__ bool by_list() const { return top_k > 0 && top_k <= kMostListedK; }
 
   __device__ uint4 load(int at) const {  // elements outside the row: -inf
     constexpr uint32_t kNegInf = sizeof(T) == 4 ? 0xff800000u : 0xff80ff80u;
@@ -129,224 +167,805 @@ struct Row {
     }
     return make_uint4(w[0], w[1], w[2], w[3]);
   }
-  __device__ int first(int tile) const { return (tile * kSampleThreads + (int)threadIdx.x) * VE - skew; }
-  __device__ u64 weight(float v) const { return weight_of(((double)v - (double)m) * per); }
-  // f(value, index) for every logit of the thread's
+  // f(segment, first index of vector i's elements, the vectors) for the wave's segments of [s0, s1), the next one's loads in flight.
   template <typename F>
-  __device__ void each(F f) const {
-    for (int i = 0; i < tiles; ++i) {
-      const int at = first(i);
-      const uint4 w = load(at);
+  __device__ void segments(int s0, int s1, F f) const {
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    int s = s0 + wave;
+    if (s >= s1) return;
+    auto first = [&](int seg, int i) { return seg * kSampleSeg - skew + (i * 64 + lane) * VE; };
+    uint4 next[NV];
 #pragma unroll
-      for (int e = 0; e < VE; ++e)
-        if (at + e >= 0 && at + e < V) f(Logits<T>::at(w, e), at + e);
+    for (int i = 0; i < NV; ++i) next[i] = load(first(s, i));
+    for (; s < s1; s += kWaves) {
+      uint4 v[NV];
+#pragma unroll
+      for (int i = 0; i < NV; ++i) v[i] = next[i];
+      if (s + kWaves < s1) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) next[i] = load(first(s + kWaves, i));
+      }
+      f(s, first(s, 0), v);
     }
   }
+  static __device__ int index(int first, int i, int e) { return first + i * 64 * VE + e; }
+
+  // 256 log2 of the weight's share, at least -16 kBins + 1: from there on weights are 0.
+  __device__ double exponent(float v) const { return fmax(((double)v - (double)m) * steps, (double)(1 - 16 * kBins)); }
+  static __device__ int whole(double t) { return (int)(uint32_t)__double_as_longlong(t + 6755399441055744.0); }  // + 1.5 2^52
+  static __device__ int bin_of(int n) { return -n >> 4; }
+  __device__ int bin(float v) const { return bin_of(whole(exponent(v))); }
+  // The place within its bin, in 256 parts: larger weights first.
+  __device__ int fine_bin(float v, int b) const {
+    return min(max((int)((-exponent(v) - 16.0 * b + 0.5) * 16.0), 0), 255);
+  }
+  // 2^n/256 from the table, times e^g for what is left, |g| <= ln(2)/512 = a:
+  // a^2 g^2 / 24 stands for the series' fourth term, which leaves 3.5e-14 at
+  // most; adding 2^52 rounds to nearest even and leaves the number
+  // in the low bits, above which the sum of 2^52's own bits is taken off.
+  static constexpr u64 kMagicBits = 0x4330000000000000ull;
+  __device__ u64 magic_weight(double t, const double *table) const {
+    const double z = t + 6755399441055744.0;
+    const int n = (int)(uint32_t)__double_as_longlong(z);
+    const double g = (t - (z - 6755399441055744.0)) * 0.0027076061740622862;
+    constexpr double a2 = 1.8327827e-6;
+    double p = fma(g, 1.0 / 6.0, 0.5 + a2 / 24.0);
+    p = fma(p, g, 1.0);
+    const double w = table[n & 255];
+    const double r = fma(w, p * g, w);
+    const u64 bits = (u64)__double_as_longlong(r) + ((u64)((uint32_t)(n >> 8) << 20) << 32);
+    return (u64)__double_as_longlong(__longlong_as_double((long long)bits) + 4503599627370496.0);
+  }
+  __device__ u64 weight(float v, const double *table) const { return magic_weight(exponent(v), table) - kMagicBits; }
+  __device__ bool keeps(u64 place) const { return place >= cut; }
 };
 
-// What is kept so far: tokens above `key`, and equal ones up to `index`.
-struct Cut {
-  uint32_t key;
-  int index;
-  __device__ bool keeps(uint32_t k, int i) const { return k > key || (k == key && i <= index); }
-};
+__device__ __forceinline__ void fill_table(SampleLds &lds) {
+  for (int j = threadIdx.x; j < 256; j += kSampleThreads) {
+    const double f = j * 0.0027076061740622862;  // ln(2) / 256
+    double p = 1.0;
+#pragma unroll
+    for (int i = 18; i > 0; --i) p = fma(p, f / i, 1.0);  // f below 0.7: the 19th term is under 1e-19
+    lds.table[j] = p * kUnit;
+  }
+}
 
 __device__ __forceinline__ u64 block_sum64(u64 v, SampleLds &lds) {
-  v = lane_of64(wave_scan64(v), 63);
+  v = wave_sum64(v);
   __syncthreads();
   if ((threadIdx.x & 63) == 0) lds.scan[threadIdx.x >> 6] = v;
   __syncthreads();
-  return lds.scan[0] + lds.scan[1] + lds.scan[2] + lds.scan[3];
+  u64 s = lds.scan[0];
+#pragma unroll
+  for (int w = 1; w < kWaves; ++w) s += lds.scan[w];
+  return s;
 }
 
-// The smallest prefix of what `cut` keeps whose measure reaches goal >= 1, as
-// a cut; the whole measure reaches it.  measure(value) is the same for equal values.
-template <typename T, typename M>
-__device__ Cut cut_at(const Row<T> &row, const Cut &cut, u64 goal, M measure, SampleLds &lds) {
+// The first of n <= 4 kSampleThreads entries at which the running sum reaches
+// goal >= 1 into lds.found, the sum before it into lds.found_above; n where
+// none does.  at(i) gives entry i.  Called after a barrier, ends with one.
+template <typename At>
+__device__ __forceinline__ void find_reach(int n, u64 goal, At at, SampleLds &lds) {
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, per = (n + kSampleThreads - 1) / kSampleThreads;
+  u64 sum = 0;
+  for (int i = 0; i < per; ++i) sum += per * tid + i < n ? at(per * tid + i) : 0;
+  u64 incl = wave_scan64(sum);
+  if (lane == 63) lds.scan[wave] = incl;
+  if (tid == 0) lds.found = n;
+  __syncthreads();
+  for (int w = 0; w < wave; ++w) incl += lds.scan[w];
+  u64 before = incl - sum;
+  if (goal > before && goal <= incl) {
+    for (int i = 0; i < per; ++i) {
+      const u64 w = at(per * tid + i);
+      if (goal <= before + w) {
+        lds.found = per * tid + i;
+        lds.found_above = before;
+        break;
+      }
+      before += w;
+    }
+  }
+  __syncthreads();
+}
+
+__device__ __forceinline__ void clear_bins(SampleLds &lds, int n) {
+  for (int i = threadIdx.x; i < n; i += kSampleThreads) lds.bins[i] = 0;
+}
+__device__ __forceinline__ void put(SampleLds &lds, u64 place) {
+  const int at = atomicAdd(&lds.count, 1);
+  if (at < kSampleList) lds.list[at] = place;
+}
+
+// ---------------------------------------------------------------- the passes over a row's segments [s0, s1)
+// Maximum, NaN where there is one, and the maxima of the parts to part(segment, lane value).
+template <typename T, typename Part>
+__device__ __forceinline__ float max_pass(const Row<T> &row, int s0, int s1, SampleLds &lds, Part part) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  constexpr int kPer = kSampleBins / kSampleThreads;
-  uint32_t prefix = 0;  // of the key looked for, the bits above `shift + bits`
-  int shift = 32;
-  for (int pass = 0; pass < 3; ++pass) {
-    const int bits = pass < 2 ? 11 : 10, top = shift;
-    shift -= bits;
-    for (int i = tid; i < kSampleBins; i += kSampleThreads) lds.bins[i] = 0;
-    __syncthreads();
-    row.each([&](float v, int i) {
-      const uint32_t k = sample_key(v);
-      if ((pass == 0 || k >> top == prefix) && cut.keeps(k, i)) atomicAdd(&lds.bins[(k >> shift) & ((1u << bits) - 1)], measure(v));
-    });
-    __syncthreads();
-    // from the largest bin down: thread t has bins n - 1 - kPer t and the ones below
+  if (tid == 0) lds.bad = 0;
+  __syncthreads();
+  float m = -INFINITY;
+  uint32_t largest = 0;  // of the magnitudes' bits: above infinity's there is a NaN
+  row.segments(s0, s1, [&](int s, int, const uint4 *v) {
+    float mine = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < Row<T>::NV; ++i)
+#pragma unroll
+      for (int e = 0; e < Row<T>::VE; ++e) {
+        const float x = Logits<T>::at(v[i], e);
+        mine = fmaxf(mine, x);
+        largest = max(largest, __float_as_uint(x) & 0x7fffffffu);
+      }
+    part(s, mine);
+    m = fmaxf(m, mine);
+  });
+  m = __int_as_float(wave_reduce(__float_as_int(m), (int)0xff800000u,
+                                 [](int a, int b) { return __float_as_int(fmaxf(__int_as_float(a), __int_as_float(b))); }));
+  if (lane == 0) lds.m[wave] = m;
+  if (largest > 0x7f800000u) lds.bad = 1;
+  __syncthreads();
+  m = lds.m[0];
+#pragma unroll
+  for (int w = 1; w < kWaves; ++w) m = fmaxf(m, lds.m[w]);
+  return lds.bad ? __uint_as_float(0x7fc00000u) : m;
+}
+
+// The weights of each segment's tokens that the cut keeps and that are `least` or more, by seg(segment, sum).
+template <typename T, typename Seg>
+__device__ __forceinline__ void mass_pass(const Row<T> &row, int s0, int s1, u64 least, SampleLds &lds, Seg seg) {
+  const bool all = row.cut == 0 && least == 0;
+  row.segments(s0, s1, [&](int s, int first, const uint4 *v) {
+    u64 sum = 0;
+    if (all) {
+#pragma unroll
+      for (int i = 0; i < Row<T>::NV; ++i)
+#pragma unroll
+        for (int e = 0; e < Row<T>::VE; ++e) sum += row.magic_weight(row.exponent(Logits<T>::at(v[i], e)), lds.table);
+      sum -= (u64)(Row<T>::NV * Row<T>::VE) * Row<T>::kMagicBits;
+    } else {
+#pragma unroll
+      for (int i = 0; i < Row<T>::NV; ++i)
+#pragma unroll
+        for (int e = 0; e < Row<T>::VE; ++e) {
+          const float x = Logits<T>::at(v[i], e);
+          if (row.keeps(place_of(x, Row<T>::index(first, i, e)))) {
+            const u64 w = row.weight(x, lds.table);
+            sum += w >= least ? w : 0;
+          }
+        }
+    }
+    sum = wave_sum64(sum);
+    if ((threadIdx.x & 63) == 0) seg(s, sum);
+  });
+}
+
+// The measure of every bin into lds.bins, which are clear: weights or counts of what is kept.
+template <typename T>
+__device__ __forceinline__ void bin_pass(const Row<T> &row, int s0, int s1, bool counts, SampleLds &lds) {
+  row.segments(s0, s1, [&](int, int first, const uint4 *v) {
+#pragma unroll
+    for (int i = 0; i < Row<T>::NV; ++i)
+#pragma unroll
+      for (int e = 0; e < Row<T>::VE; ++e) {
+        const float x = Logits<T>::at(v[i], e);
+        const double t = row.exponent(x);
+        const int b = Row<T>::bin_of(Row<T>::whole(t));
+        if (b < kLowest && (row.cut == 0 || row.keeps(place_of(x, Row<T>::index(first, i, e)))))
+          atomicAdd(&lds.bins[b], counts ? 1ull : row.magic_weight(t, lds.table) - Row<T>::kMagicBits);
+      }
+  });
+}
+
+// put(place) for what is kept of the bins lo .. hi, hi below kLowest.
+template <typename T, typename Put>
+__device__ __forceinline__ void list_pass(const Row<T> &row, int s0, int s1, int lo, int hi, Put put) {
+  row.segments(s0, s1, [&](int, int first, const uint4 *v) {
+#pragma unroll
+    for (int i = 0; i < Row<T>::NV; ++i)
+#pragma unroll
+      for (int e = 0; e < Row<T>::VE; ++e) {
+        const float x = Logits<T>::at(v[i], e);
+        const int b = row.bin(x);
+        if (b >= lo && b <= hi) {
+          const u64 place = place_of(x, Row<T>::index(first, i, e));
+          if (row.keeps(place)) put(place);
+        }
+      }
+  });
+}
+
+// The same for bin b, and the weights of each segment's tokens in the bins above it.
+template <typename T, typename Put, typename Seg>
+__device__ __forceinline__ void list_and_mass_pass(const Row<T> &row, int s0, int s1, int b, SampleLds &lds, Put put, Seg seg) {
+  row.segments(s0, s1, [&](int s, int first, const uint4 *v) {
     u64 sum = 0;
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) sum += lds.bins[kSampleBins - 1 - (kPer * tid + i)];
+    for (int i = 0; i < Row<T>::NV; ++i)
+#pragma unroll
+      for (int e = 0; e < Row<T>::VE; ++e) {
+        const float x = Logits<T>::at(v[i], e);
+        const double t = row.exponent(x);
+        const int its = Row<T>::bin_of(Row<T>::whole(t));
+        if (its <= b) {
+          const u64 place = place_of(x, Row<T>::index(first, i, e));
+          if (row.keeps(place)) {
+            if (its == b) put(place);
+            else {
+              const u64 w = row.magic_weight(t, lds.table) - Row<T>::kMagicBits;
+              sum += w >= row.least ? w : 0;
+            }
+          }
+        }
+      }
+    sum = wave_sum64(sum);
+    if ((threadIdx.x & 63) == 0) seg(s, sum);
+  });
+}
+
+// ---------------------------------------------------------------- cuts
+// The smallest prefix of what the row keeps whose measure reaches goal >= 1,
+// which it does, by histograms over the key's bits: one workgroup, any row.
+template <typename T>
+__device__ void cut_by_bits(Row<T> &row, u64 goal, bool counts, SampleLds &lds) {
+  constexpr int VE = Row<T>::VE, kTile = kSampleThreads * VE;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, tiles = (row.V + row.skew + kTile - 1) / kTile;
+  auto measure = [&](float v) -> u64 { return counts ? 1 : row.weight(v, lds.table); };
+  uint32_t prefix = 0;
+  int shift = 32;
+  for (int pass = 0; pass < 3; ++pass) {
+    const int bits = pass < 2 ? 11 : 10, top = shift, size = 1 << bits;
+    shift -= bits;
+    __syncthreads();
+    for (int i = tid; i < size; i += kSampleThreads) lds.radix[i] = 0;
+    __syncthreads();
+    for (int i = 0; i < tiles; ++i) {
+      const int at = (i * kSampleThreads + tid) * VE - row.skew;
+      const uint4 w = row.load(at);
+#pragma unroll
+      for (int e = 0; e < VE; ++e) {
+        const float v = Logits<T>::at(w, e);
+        const uint32_t k = sample_key(v);
+        if (at + e >= 0 && at + e < row.V && (pass == 0 || k >> top == prefix) && row.keeps(place_of(v, at + e)))
+          atomicAdd(&lds.radix[size - 1 - ((k >> shift) & (size - 1))], measure(v));  // the largest values' bin is the first
+      }
+    }
+    __syncthreads();
+    const int per = size / kSampleThreads;
+    u64 sum = 0;
+    for (int i = 0; i < per; ++i) sum += lds.radix[per * tid + i];
     u64 incl = wave_scan64(sum);
     if (lane == 63) lds.scan[wave] = incl;
     __syncthreads();
     for (int w = 0; w < wave; ++w) incl += lds.scan[w];
-    u64 at = incl - sum;
-    if (goal > at && goal <= incl) {
-      for (int i = 0; i < kPer; ++i) {
-        const int b = kSampleBins - 1 - (kPer * tid + i);
-        const u64 w = lds.bins[b];
-        if (goal <= at + w) {
-          lds.found = b;
-          lds.found_above = at;
+    u64 before = incl - sum;
+    if (goal > before && goal <= incl) {
+      for (int i = 0; i < per; ++i) {
+        const u64 w = lds.radix[per * tid + i];
+        if (goal <= before + w) {
+          lds.found = per * tid + i;
+          lds.found_above = before;
           break;
         }
-        at += w;
+        before += w;
       }
     }
     __syncthreads();
-    prefix = prefix << bits | (uint32_t)lds.found;
+    prefix = prefix << bits | (uint32_t)(size - 1 - lds.found);
     goal -= lds.found_above;
-    __syncthreads();
   }
   // `goal` of the tokens of value `prefix`, each of the same measure: so many of them, in order of index
-  const uint32_t key = prefix;
-  const uint32_t b = key & 0x80000000u ? key ^ 0x80000000u : ~key;
-  const u64 one = measure(__uint_as_float(b));
+  const u64 one = measure(value_of(prefix));
   int left = (int)((goal + one - 1) / one);
-  if (tid == 0) lds.index = INT_MAX;
-  for (int i = 0; i < row.tiles; ++i) {
-    const int at = row.first(i);
+  __syncthreads();
+  for (int i = 0; i < tiles; ++i) {
+    const int at = (i * kSampleThreads + tid) * VE - row.skew;
     const uint4 w = row.load(at);
+    auto counts_one = [&](int e) {
+      const float v = Logits<T>::at(w, e);
+      return at + e >= 0 && at + e < row.V && sample_key(v) == prefix && row.keeps(place_of(v, at + e));
+    };
     int mine = 0;
 #pragma unroll
-    for (int e = 0; e < Row<T>::VE; ++e)
-      if (at + e >= 0 && at + e < row.V) mine += sample_key(Logits<T>::at(w, e)) == key && cut.keeps(key, at + e);
+    for (int e = 0; e < VE; ++e) mine += counts_one(e);
     int incl = wave_incl_scan(mine);
     __syncthreads();
     if (lane == 63) lds.scan[wave] = incl;
     __syncthreads();
-    for (int v = 0; v < wave; ++v) incl += (int)lds.scan[v];
-    const int all = (int)(lds.scan[0] + lds.scan[1] + lds.scan[2] + lds.scan[3]);
+    int all = 0;
+    for (int v = 0; v < kWaves; ++v) {
+      if (v < wave) incl += (int)lds.scan[v];
+      all += (int)lds.scan[v];
+    }
     if (left <= incl && left > incl - mine) {
       int n = incl - mine;
 #pragma unroll
-      for (int e = 0; e < Row<T>::VE; ++e)
-        if (at + e >= 0 && at + e < row.V && sample_key(Logits<T>::at(w, e)) == key && cut.keeps(key, at + e) && ++n == left)
-          lds.index = at + e;
+      for (int e = 0; e < VE; ++e)
+        if (counts_one(e) && ++n == left) lds.index = at + e;
     }
     left -= all;
     if (left <= 0) break;
   }
   __syncthreads();
-  const Cut got = {key, lds.index};
+  row.cut = (u64)prefix << 32 | (uint32_t)~lds.index;
   __syncthreads();
-  return got;
+}
+
+// The cut among the lds.count <= kSampleList listed places of bin b: the
+// smallest prefix of them whose measure reaches goal, which it does.
+template <typename T>
+__device__ __forceinline__ u64 cut_in_list(const Row<T> &row, int b, u64 goal, bool counts, SampleLds &lds) {
+  const int tid = threadIdx.x, n = lds.count;
+  clear_bins(lds, 256);
+  if (tid == 0) lds.picked = 0;
+  __syncthreads();
+  for (int i = tid; i < n; i += kSampleThreads) {
+    const float v = value_of((uint32_t)(lds.list[i] >> 32));
+    const u64 w = counts ? 1 : row.weight(v, lds.table);
+    lds.w[i] = w;
+    atomicAdd(&lds.bins[row.fine_bin(v, b)], w);
+  }
+  __syncthreads();
+  find_reach(256, goal, [&](int i) { return lds.bins[i]; }, lds);
+  const int fine = lds.found;
+  const u64 above = lds.found_above;
+  // the fine bin's places go to the list's front: indexes only, the places stay where they are
+  uint32_t *const pick = (uint32_t *)lds.bins;
+  static_assert(kSampleList * sizeof(uint32_t) <= kBins * sizeof(u64), "picks fit the bins");
+  __syncthreads();
+  for (int i = tid; i < n; i += kSampleThreads)
+    if (row.fine_bin(value_of((uint32_t)(lds.list[i] >> 32)), b) == fine) pick[atomicAdd(&lds.picked, 1)] = i;
+  __syncthreads();
+  const int c = lds.picked;
+  for (int i = tid; i < c; i += kSampleThreads) {
+    const u64 mine = lds.list[pick[i]], w = lds.w[pick[i]];
+    u64 over = above;
+    for (int j = 0; j < c; ++j) {
+      const u64 other = lds.list[pick[j]];
+      over += other > mine ? lds.w[pick[j]] : 0;
+    }
+    if (goal > over && goal <= over + w) lds.found_above = mine;
+  }
+  __syncthreads();
+  const u64 cut = lds.found_above;
+  __syncthreads();
+  return cut;
+}
+
+// ---------------------------------------------------------------- the drawing
+__device__ __forceinline__ u64 goal_of(float u, u64 total) {
+  const double g = floor((double)u * (double)total);
+  return g > 0.0 ? (g < (double)total ? min((u64)g, total - 1) : total - 1) : 0;
+}
+template <typename T>
+__device__ __forceinline__ void write_result(const SampleArgs &a, const Row<T> &row, int r, int id, float v, u64 total) {
+  a.ids[r] = id;
+  if (a.logp)
+    a.logp[r] = row.greedy ? 0.f : (float)(((double)v - (double)row.m) / (double)row.temp - log((double)total * (1.0 / kUnit)));
+}
+__device__ __forceinline__ void write_none(const SampleArgs &a, int r) {
+  if (threadIdx.x == 0) {
+    a.ids[r] = -1;
+    if (a.logp) a.logp[r] = __uint_as_float(0x7fc00000u);
+  }
+}
+
+// By the sums of the row's segments, lds.seg, of what it keeps.
+template <typename T>
+__device__ __forceinline__ void draw_from_segments(const SampleArgs &a, const Row<T> &row, int r, SampleLds &lds) {
+  constexpr int kPer = kSampleSeg / kSampleThreads;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  u64 total = 0;
+  for (int i = tid; i < row.segs; i += kSampleThreads) total += lds.seg[i];
+  total = block_sum64(total, lds);
+  const u64 goal = goal_of(row.u, total);
+  __syncthreads();
+  find_reach(row.segs, goal + 1, [&](int i) { return lds.seg[i]; }, lds);
+  u64 before = lds.found_above;
+  const int at = lds.found * kSampleSeg - row.skew + tid * kPer;
+  __syncthreads();
+  uint4 v[kPer / Row<T>::VE];
+#pragma unroll
+  for (int i = 0; i < kPer / Row<T>::VE; ++i) v[i] = row.load(at + i * Row<T>::VE);
+  u64 w[kPer], sum = 0;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const float x = Logits<T>::at(v[i / Row<T>::VE], i % Row<T>::VE);
+    w[i] = 0;
+    if (row.keeps(place_of(x, at + i))) {
+      w[i] = row.weight(x, lds.table);
+      if (w[i] < row.least) w[i] = 0;
+    }
+    sum += w[i];
+  }
+  u64 incl = wave_scan64(sum);
+  if (lane == 63) lds.scan[wave] = incl;
+  __syncthreads();
+  for (int i = 0; i < wave; ++i) incl += lds.scan[i];
+  before += incl - sum;
+  if (goal >= before && goal < before + sum) {
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      if (goal >= before && goal < before + w[i])
+        write_result(a, row, r, at + i, Logits<T>::at(v[i / Row<T>::VE], i % Row<T>::VE), total);
+      before += w[i];
+    }
+  }
+}
+
+// Among the lds.count <= kSampleList listed places, which hold at least the row's first top_k.
+template <typename T>
+__device__ __forceinline__ void draw_from_list(const SampleArgs &a, const Row<T> &row, int r, SampleLds &lds) {
+  constexpr int kPer = kSampleList / kSampleThreads;
+  const int tid = threadIdx.x, n = lds.count;
+  for (int i = tid; i < n; i += kSampleThreads) lds.w[i] = row.weight(value_of((uint32_t)(lds.list[i] >> 32)), lds.table);
+  __syncthreads();
+  u64 mass = 0, above[kPer];
+  int rank[kPer];
+#pragma unroll
+  for (int p = 0; p < kPer; ++p) {
+    const int i = tid + p * kSampleThreads;
+    rank[p] = 0;
+    above[p] = 0;
+    if (i >= n) continue;
+    const u64 mine = lds.list[i];
+#pragma unroll 4
+    for (int j = 0; j < n; ++j) {
+      const bool over = lds.list[j] > mine;
+      rank[p] += over;
+      above[p] += over ? lds.w[j] : 0;
+    }
+    if (rank[p] < row.top_k) mass += lds.w[i];
+  }
+  mass = block_sum64(mass, lds);
+  const u64 need = row.top_p < 1.f ? (u64)fmax(ceil((double)row.top_p * (double)mass), 0.0) : ~0ull;
+  u64 total = 0;
+#pragma unroll
+  for (int p = 0; p < kPer; ++p) {
+    const int i = tid + p * kSampleThreads;
+    if (i >= n) continue;
+    const u64 w = lds.w[i];
+    const bool stays = rank[p] == 0 || (rank[p] < row.top_k && above[p] < need && w >= row.least);
+    if (!stays) lds.w[i] = 0;
+    total += stays ? w : 0;
+  }
+  total = block_sum64(total, lds);
+  const u64 goal = goal_of(row.u, total);
+#pragma unroll
+  for (int p = 0; p < kPer; ++p) {
+    const int i = tid + p * kSampleThreads;
+    if (i >= n || lds.w[i] == 0) continue;
+    const u64 w = lds.w[i];
+    const uint32_t mine = (uint32_t)lds.list[i];  // the index's complement: larger is earlier
+    u64 before = 0;
+#pragma unroll 4
+    for (int j = 0; j < n; ++j) before += (uint32_t)lds.list[j] > mine ? lds.w[j] : 0;
+    if (goal >= before && goal < before + w) write_result(a, row, r, index_of(lds.list[i]), value_of((uint32_t)(lds.list[i] >> 32)), total);
+  }
+}
+
+// ---------------------------------------------------------------- one workgroup's way through a row
+// The maxima of a row's parts: 32 logits each, neighbouring lanes' together where a row has more than kParts.
+__device__ __forceinline__ int part_shift(int segs) {
+  int shift = 0;
+  while (segs << (6 - shift) > kParts) ++shift;
+  return shift;
+}
+__device__ __forceinline__ void store_part(float *parts, int shift, int seg, float mine) {
+  const int lane = threadIdx.x & 63;
+  for (int i = 0; i < shift; ++i) mine = fmaxf(mine, __shfl_xor(mine, 1 << i, 64));
+  if ((lane & ((1 << shift) - 1)) == 0) parts[(seg << (6 - shift)) + (lane >> shift)] = mine;
+}
+// The bin that top_k of the parts' maxima reach: at least as many logits lie in it and the ones above.
+template <typename T>
+__device__ __forceinline__ int listed_bins(const Row<T> &row, const float *parts, SampleLds &lds) {
+  clear_bins(lds, kBins);
+  __syncthreads();
+  const int n = row.segs << (6 - part_shift(row.segs));
+  for (int i = threadIdx.x; i < n; i += kSampleThreads) {
+    const int b = row.bin(parts[i]);
+    if (b < kLowest) atomicAdd(&lds.bins[b], 1ull);
+  }
+  __syncthreads();
+  find_reach(kBins, (u64)row.top_k, [&](int i) { return lds.bins[i]; }, lds);
+  return min(lds.found, kLowest - 1);  // fewer parts hold anything: all that has a weight
+}
+// The weight that top-p wants of a sum.
+__device__ __forceinline__ u64 wanted(float top_p, u64 mass) {
+  const double goal = ceil((double)top_p * (double)mass);
+  return goal >= 1.0 ? (u64)goal : 1;
+}
+// lds.bins' sum, the bin in which top-p's cut lies and what the cut wants of it.
+template <typename T>
+__device__ __forceinline__ int top_p_bin(const Row<T> &row, u64 *wants, SampleLds &lds) {
+  u64 mass = 0;
+  for (int i = threadIdx.x; i < kBins; i += kSampleThreads) mass += lds.bins[i];
+  mass = block_sum64(mass, lds);
+  const u64 goal = wanted(row.top_p, mass);
+  __syncthreads();
+  find_reach(kBins, goal, [&](int i) { return lds.bins[i]; }, lds);
+  *wants = goal - lds.found_above;
+  return lds.found;
+}
+// Top-p's cut among the listed places of its bin; those that it keeps join their segments' sums.
+template <typename T>
+__device__ __forceinline__ void cut_and_add(Row<T> &row, int b, u64 wants, SampleLds &lds) {
+  row.cut = cut_in_list(row, b, wants, false, lds);
+  for (int i = threadIdx.x; i < lds.count; i += kSampleThreads)
+    if (row.keeps(lds.list[i]) && lds.w[i] >= row.least)
+      atomicAdd(&lds.seg[(index_of(lds.list[i]) + row.skew) / kSampleSeg], lds.w[i]);
+  __syncthreads();
+}
+
+// Whatever a list could not hold.
+template <typename T>
+__device__ void draw_by_bits(const SampleArgs &a, Row<T> &row, int r, SampleLds &lds) {
+  auto to_seg = [&](int s, u64 sum) { lds.seg[s] = sum; };
+  row.cut = 0;
+  if (row.top_k > 0) cut_by_bits(row, (u64)row.top_k, true, lds);
+  if (row.top_p < 1.f) {
+    mass_pass(row, 0, row.segs, 0, lds, to_seg);
+    __syncthreads();
+    u64 mass = 0;
+    for (int i = threadIdx.x; i < row.segs; i += kSampleThreads) mass += lds.seg[i];
+    mass = block_sum64(mass, lds);
+    cut_by_bits(row, wanted(row.top_p, mass), false, lds);
+  }
+  mass_pass(row, 0, row.segs, row.least, lds, to_seg);
+  __syncthreads();
+  draw_from_segments(a, row, r, lds);
+}
+
+// A row that does not go by a list of its first top_k.
+template <typename T>
+__device__ void draw_by_bins(const SampleArgs &a, Row<T> &row, int r, SampleLds &lds) {
+  const int tid = threadIdx.x;
+  auto to_list = [&](u64 place) { put(lds, place); };
+  auto to_seg = [&](int s, u64 sum) { lds.seg[s] = sum; };
+  if (row.top_k > 0) {
+    clear_bins(lds, kBins);
+    if (tid == 0) lds.count = 0;
+    __syncthreads();
+    bin_pass(row, 0, row.segs, true, lds);
+    __syncthreads();
+    find_reach(kBins, (u64)row.top_k, [&](int i) { return lds.bins[i]; }, lds);
+    if (lds.found < kBins) {  // else fewer have a weight
+      const int b = lds.found;
+      const u64 wants = (u64)row.top_k - lds.found_above;
+      list_pass(row, 0, row.segs, b, b, to_list);
+      __syncthreads();
+      if (lds.count > kSampleList) {
+        draw_by_bits(a, row, r, lds);
+        return;
+      }
+      row.cut = cut_in_list(row, b, wants, true, lds);
+    }
+    __syncthreads();
+  }
+  if (row.top_p < 1.f) {
+    clear_bins(lds, kBins);
+    if (tid == 0) lds.count = 0;
+    __syncthreads();
+    bin_pass(row, 0, row.segs, false, lds);
+    __syncthreads();
+    u64 wants;
+    const int b = top_p_bin(row, &wants, lds);
+    list_and_mass_pass(row, 0, row.segs, b, lds, to_list, to_seg);
+    __syncthreads();
+    if (lds.count > kSampleList) {
+      draw_by_bits(a, row, r, lds);
+      return;
+    }
+    cut_and_add(row, b, wants, lds);
+  } else {
+    mass_pass(row, 0, row.segs, row.least, lds, to_seg);
+    __syncthreads();
+  }
+  draw_from_segments(a, row, r, lds);
+}
+
+// Grid: rows.
+template <typename T>
+__global__ __launch_bounds__(kSampleThreads, 4) void sample_kernel(SampleArgs a) {
+  __shared__ SampleLds lds;
+  const int r = blockIdx.x;
+  Row<T> row;
+  row.begin(a, r);
+  fill_table(lds);
+  const bool by_list = row.by_list();
+  const int shift = part_shift(row.segs);
+  const float m = max_pass(row, 0, row.segs, lds, [&](int s, float mine) {
+    if (by_list) store_part(lds.parts, shift, s, mine);
+  });
+  if (!row.set_max(m)) {
+    write_none(a, r);
+    return;
+  }
+  if (!by_list) {
+    draw_by_bins(a, row, r, lds);
+    return;
+  }
+  const int b = listed_bins(row, lds.parts, lds);
+  if (threadIdx.x == 0) lds.count = 0;
+  __syncthreads();
+  list_pass(row, 0, row.segs, 0, b, [&](u64 place) { put(lds, place); });
+  __syncthreads();
+  if (lds.count <= kSampleList) draw_from_list(a, row, r, lds);
+  else draw_by_bits(a, row, r, lds);
+}
+
+// ---------------------------------------------------------------- few rows: a row on several workgroups
+// What the workgroups of a row leave each other; nothing of it is read before it is written.
+struct SampleRow {
+  float max[kSampleMaxChunks];
+  int count, bin;
+  u64 wants;
+  float parts[kParts];
+  u64 list[kSampleList];
+  u64 seg[kSampleMaxSegs];
+  u64 bins[1][kBins];  // a chunk's each
+};
+size_t sample_row_bytes(int chunks) { return sizeof(SampleRow) + (chunks - 1) * kBins * sizeof(u64); }
+__device__ __forceinline__ SampleRow &row_record(const SampleArgs &a, int r) {
+  return *(SampleRow *)((char *)a.rows + r * (sizeof(SampleRow) + (a.chunks - 1) * kBins * sizeof(u64)));
+}
+
+struct Chunk {
+  int r, c, s0, s1;
+  __device__ Chunk(const SampleArgs &a, int segs) {
+    r = blockIdx.x / a.chunks;
+    c = blockIdx.x - r * a.chunks;
+    const int per = (segs + a.chunks - 1) / a.chunks;
+    s0 = min(c * per, segs);
+    s1 = min(s0 + per, segs);
+  }
+};
+template <typename T>
+__device__ __forceinline__ bool max_of_chunks(const SampleArgs &a, const SampleRow &w, Row<T> &row) {
+  float m = -INFINITY;
+  bool nan = false;
+  for (int c = 0; c < a.chunks; ++c) {
+    m = fmaxf(m, w.max[c]);
+    nan |= w.max[c] != w.max[c];
+  }
+  return row.set_max(nan ? __uint_as_float(0x7fc00000u) : m);
+}
+__device__ __forceinline__ void put_global(SampleRow &w, u64 place) {
+  const int at = __hip_atomic_fetch_add(&w.count, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  if (at < kSampleList) w.list[at] = place;
+}
+
+// Grid of these three: rows x chunks.  Maxima.
+template <typename T>
+__global__ __launch_bounds__(kSampleThreads, 4) void sample_max_kernel(SampleArgs a) {
+  __shared__ SampleLds lds;
+  Row<T> row;
+  row.begin(a, blockIdx.x / a.chunks);
+  const Chunk k(a, row.segs);
+  SampleRow &w = row_record(a, k.r);
+  const bool by_list = row.by_list();
+  const int shift = part_shift(row.segs);
+  const float m = max_pass(row, k.s0, k.s1, lds, [&](int s, float mine) {
+    if (by_list) store_part(w.parts, shift, s, mine);
+  });
+  if (threadIdx.x == 0) {
+    w.max[k.c] = m;
+    if (k.c == 0) w.count = 0;
+  }
+}
+
+// The lists of rows that go by one, top-p's bins, the sums of rows without a cut.
+template <typename T>
+__global__ __launch_bounds__(kSampleThreads, 4) void sample_sum_kernel(SampleArgs a) {
+  __shared__ SampleLds lds;
+  Row<T> row;
+  row.begin(a, blockIdx.x / a.chunks);
+  const Chunk k(a, row.segs);
+  SampleRow &w = row_record(a, k.r);
+  if (!max_of_chunks(a, w, row)) return;
+  if (row.by_list()) {
+    const int b = listed_bins(row, w.parts, lds);
+    list_pass(row, k.s0, k.s1, 0, b, [&](u64 place) { put_global(w, place); });
+  } else if (row.top_k == 0) {
+    fill_table(lds);
+    if (row.top_p < 1.f) {
+      clear_bins(lds, kBins);
+      __syncthreads();
+      bin_pass(row, k.s0, k.s1, false, lds);
+      __syncthreads();
+      for (int i = threadIdx.x; i < kBins; i += kSampleThreads) w.bins[k.c][i] = lds.bins[i];
+    } else {
+      __syncthreads();
+      mass_pass(row, k.s0, k.s1, row.least, lds, [&](int s, u64 sum) { w.seg[s] = sum; });
+    }
+  }
+}
+
+// Top-p: the bin of the cut from all chunks' bins, its list, the sums above it.
+template <typename T>
+__global__ __launch_bounds__(kSampleThreads, 4) void sample_list_kernel(SampleArgs a) {
+  __shared__ SampleLds lds;
+  Row<T> row;
+  row.begin(a, blockIdx.x / a.chunks);
+  if (!(row.top_p < 1.f) || row.top_k > 0) return;
+  const Chunk k(a, row.segs);
+  SampleRow &w = row_record(a, k.r);
+  if (!max_of_chunks(a, w, row)) return;
+  fill_table(lds);
+  for (int i = threadIdx.x; i < kBins; i += kSampleThreads) {
+    u64 sum = 0;
+    for (int c = 0; c < a.chunks; ++c) sum += w.bins[c][i];
+    lds.bins[i] = sum;
+  }
+  __syncthreads();
+  u64 wants;
+  const int b = top_p_bin(row, &wants, lds);
+  if (k.c == 0 && threadIdx.x == 0) {
+    w.bin = b;
+    w.wants = wants;
+  }
+  list_and_mass_pass(row, k.s0, k.s1, b, lds, [&](u64 place) { put_global(w, place); }, [&](int s, u64 sum) { w.seg[s] = sum; });
+}
+
+// Grid: rows.  The drawing.
+template <typename T>
+__global__ __launch_bounds__(kSampleThreads, 4) void sample_draw_kernel(SampleArgs a) {
+  __shared__ SampleLds lds;
+  const int r = blockIdx.x, tid = threadIdx.x;
+  Row<T> row;
+  row.begin(a, r);
+  const SampleRow &w = row_record(a, r);
+  if (!max_of_chunks(a, w, row)) {
+    write_none(a, r);
+    return;
+  }
+  fill_table(lds);
+  if (row.top_k > 0 && !row.by_list()) {
+    __syncthreads();
+    draw_by_bins(a, row, r, lds);
+    return;
+  }
+  const bool by_list = row.by_list(), listed = by_list || row.top_p < 1.f;
+  const int n = listed ? w.count : 0;
+  if (n > kSampleList) {
+    __syncthreads();
+    draw_by_bits(a, row, r, lds);
+    return;
+  }
+  if (tid == 0) lds.count = n;
+  for (int i = tid; i < n; i += kSampleThreads) lds.list[i] = w.list[i];
+  if (!by_list)
+    for (int i = tid; i < row.segs; i += kSampleThreads) lds.seg[i] = w.seg[i];
+  __syncthreads();
+  if (by_list) {
+    draw_from_list(a, row, r, lds);
+    return;
+  }
+  if (listed) cut_and_add(row, w.bin, w.wants, lds);
+  draw_from_segments(a, row, r, lds);
+}
+
+// ---------------------------------------------------------------- launcher
+// Workgroups of a row: one where the rows alone fill the card, otherwise
+// enough of them that every wave has a segment.
+int sample_chunks(int n, int n_vocab, int dtype) {
+  const int ve = dtype == 0 ? 4 : 8;
+  const int segs = (n_vocab + ve - 1 + kSampleSeg - 1) / kSampleSeg;  // a row may begin up to ve - 1 elements into its first vector
+  return std::max(1, std::min({(segs + kWaves - 1) / kWaves, 512 / n, kSampleMaxChunks}));
 }
 
 template <typename T>
-__global__ __launch_bounds__(kSampleThreads) void sample_kernel(SampleArgs a) {
-  constexpr int VE = Logits<T>::N;
-  __shared__ SampleLds lds;
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int r = blockIdx.x;
-  Row<T> row;
-  row.x = (const T *)a.logits + (long long)r * a.stride;
-  row.V = a.n_vocab;
-  row.skew = (int)(((uintptr_t)row.x & 15) / sizeof(T));
-  row.tiles = (a.n_vocab + row.skew + VE * kSampleThreads - 1) / (VE * kSampleThreads);
-  const float temp = a.temperature ? a.temperature[r] : 1.f;
-  const float top_p = a.top_p ? a.top_p[r] : 1.f, min_p = a.min_p ? a.min_p[r] : 0.f, u = a.uniform[r];
-  int top_k = a.top_k ? a.top_k[r] : 0;
-
-  float m = -INFINITY;
-  bool nan = false;
-  row.each([&](float v, int) {
-    m = fmaxf(m, v);
-    nan |= v != v;
-  });
-#pragma unroll
-  for (int off = 32; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor(m, off, 64));
-  if (tid == 0) lds.bad = 0;
-  __syncthreads();
-  if (lane == 0) lds.m[wave] = m;
-  if (nan) lds.bad = 1;
-  __syncthreads();
-  m = fmaxf(fmaxf(lds.m[0], lds.m[1]), fmaxf(lds.m[2], lds.m[3]));
-  const bool none = lds.bad || !(fabsf(m) < INFINITY) || !(temp >= 0.f && temp < INFINITY) || top_p != top_p || min_p != min_p || u != u;
-  if (none) {
-    if (tid == 0) {
-      a.ids[r] = -1;
-      if (a.logp) a.logp[r] = __uint_as_float(0x7fc00000u);
-    }
-    return;
+static hipError_t launch(const SampleArgs &a, hipStream_t st) {
+  const dim3 block(kSampleThreads), rows(a.n), parts(a.n * a.chunks);
+  if (a.chunks == 1) {
+    hipLaunchKernelGGL((sample_kernel<T>), rows, block, 0, st, a);
+  } else {
+    hipLaunchKernelGGL((sample_max_kernel<T>), parts, block, 0, st, a);
+    hipLaunchKernelGGL((sample_sum_kernel<T>), parts, block, 0, st, a);
+    if (a.top_p) hipLaunchKernelGGL((sample_list_kernel<T>), parts, block, 0, st, a);
+    hipLaunchKernelGGL((sample_draw_kernel<T>), rows, block, 0, st, a);
   }
-  const bool greedy = temp == 0.f;
-  row.m = m;
-  row.per = 1.4426950408889634 / (greedy ? 1.0 : (double)temp);
-  if (greedy || min_p > 1.f) top_k = 1;
-
-  Cut cut = {0, INT_MAX};
-  if (top_k > 0 && top_k < a.n_vocab) cut = cut_at(row, cut, (u64)top_k, [](float) -> u64 { return 1; }, lds);
-  if (top_p < 1.f && top_k != 1) {
-    u64 mass = 0;
-    row.each([&](float v, int i) {
-      if (cut.keeps(sample_key(v), i)) mass += row.weight(v);
-    });
-    mass = block_sum64(mass, lds);
-    const double goal = ceil((double)top_p * (double)mass);
-    cut = cut_at(row, cut, goal >= 1.0 ? (u64)goal : 1, [&](float v) { return row.weight(v); }, lds);
-  }
-  const u64 least = min_p > 0.f && min_p <= 1.f ? (u64)ceil((double)min_p * 8796093022208.0) : 0;
-  auto kept = [&](float v, int i) -> u64 {
-    const uint32_t k = sample_key(v);
-    if (!cut.keeps(k, i)) return 0;
-    const u64 w = row.weight(v);
-    return w >= least ? w : 0;
-  };
-
-  u64 total = 0;
-  row.each([&](float v, int i) { total += kept(v, i); });
-  total = block_sum64(total, lds);
-  const double g = floor((double)u * (double)total);
-  const u64 goal = g > 0.0 ? (g < (double)total ? (u64)g : total - 1) : 0;
-
-  // by index: the first token at which the running sum exceeds the goal
-  u64 before = 0;
-  for (int i = 0; i < row.tiles; ++i) {
-    const int at = row.first(i);
-    const uint4 w = row.load(at);
-    u64 mine = 0;
-#pragma unroll
-    for (int e = 0; e < VE; ++e)
-      if (at + e >= 0 && at + e < a.n_vocab) mine += kept(Logits<T>::at(w, e), at + e);
-    u64 incl = wave_scan64(mine);
-    __syncthreads();
-    if (lane == 63) lds.scan[wave] = incl;
-    __syncthreads();
-    u64 base = before;
-    for (int v = 0; v < wave; ++v) base += lds.scan[v];
-    incl += base;
-    const u64 all = lds.scan[0] + lds.scan[1] + lds.scan[2] + lds.scan[3];
-    if (goal < incl && goal >= incl - mine) {
-      u64 n = incl - mine;
-#pragma unroll
-      for (int e = 0; e < VE; ++e)
-        if (at + e >= 0 && at + e < a.n_vocab) {
-          const float v = Logits<T>::at(w, e);
-          const u64 one = kept(v, at + e);
-          if (goal >= n && goal < n + one) {
-            a.ids[r] = at + e;
-            if (a.logp)
-              a.logp[r] = greedy ? 0.f : (float)(((double)v - (double)m) / (double)temp - log((double)total * (1.0 / 8796093022208.0)));
-          }
-          n += one;
-        }
-    }
-    before += all;
-    if (goal < before) break;
-  }
-}
-
-hipError_t launch_sample(const SampleArgs &a, int dtype, hipStream_t st) {
-  const dim3 grid(a.n), block(kSampleThreads);
-  if (dtype == 0) hipLaunchKernelGGL((sample_kernel<float>), grid, block, 0, st, a);
-  else hipLaunchKernelGGL((sample_kernel<u16>), grid, block, 0, st, a);
   return hipGetLastError();
 }
+hipError_t launch_sample(const SampleArgs &a, int dtype, hipStream_t st) { return dtype == 0 ? launch<float>(a, st) : launch<u16>(a, st); }
 
 }  // namespace lora

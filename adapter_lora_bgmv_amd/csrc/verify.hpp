@@ -229,6 +229,10 @@ hipError_t launch_score(const ScoreArgs &a, int dtype, hipStream_t st);
 
 // Tokens drawn from rows of logits (k_sample.hip).
 constexpr int kSampleThreads = 256;
+constexpr int kSampleSeg = 2048;       // logits of a segment
+constexpr int kSampleMaxSegs = 516;    // of a row: a vocabulary of 2^20 that begins inside a vector has 513
+constexpr int kSampleList = 1024;      // places of a list
+constexpr int kSampleMaxChunks = 32;   // of a row
 struct SampleArgs {
   const void *logits;  // [n][stride]
   long long stride;
@@ -238,7 +242,11 @@ struct SampleArgs {
   const float *uniform;                      // [n]
   int32_t *ids;                              // [n]
   float *logp;                               // [n] or null
+  int chunks;                                // workgroups of a row
+  void *rows;                                // [n] records for rows of several, see k_sample.hip
 };
+int sample_chunks(int n, int n_vocab, int dtype);
+size_t sample_row_bytes(int chunks);
 hipError_t launch_sample(const SampleArgs &a, int dtype, hipStream_t st);
 
 // Upper bound of the pages that n rows of n_seqs sequences touch: a sequence

@@ -343,7 +343,11 @@ int lora_token_logprobs(int32_t dtype, uint32_t n_vocab, const void *logits, uin
   return timed(what, st, [&] { return launch_score(a, dtype, st); });
 }
 
-size_t lora_token_sample_workspace_bytes(int32_t, uint32_t, uint32_t) { return 0; }
+size_t lora_token_sample_workspace_bytes(int32_t dtype, uint32_t n_vocab, uint32_t n) {
+  if (n == 0 || n > kMaxRows || n_vocab == 0 || n_vocab > LORA_MAX_VOCAB || (dtype != LORA_F32 && dtype != LORA_BF16)) return 0;
+  const int chunks = sample_chunks((int)n, (int)n_vocab, dtype);
+  return chunks > 1 ? n * sample_row_bytes(chunks) : 0;
+}
 
 int lora_token_sample(int32_t dtype, uint32_t n_vocab, const void *logits, uint32_t row_stride, const float *temperature,
                       const int32_t *top_k, const float *top_p, const float *min_p, const float *uniform, uint32_t n, int32_t *ids,
@@ -371,7 +375,8 @@ int lora_token_sample(int32_t dtype, uint32_t n_vocab, const void *logits, uint3
   if (need && !aligned16(workspace))
     return fail(LORA_ERR_UNSUPPORTED, "%s: workspace %p is not 16-byte aligned", what, workspace);
   if (int e = check_device(what)) return e;
-  const SampleArgs a{logits, row_stride, (int)n, (int)n_vocab, temperature, top_p, min_p, top_k, uniform, ids, logp};
+  const SampleArgs a{logits, row_stride, (int)n, (int)n_vocab, temperature, top_p, min_p, top_k, uniform, ids, logp,
+                     sample_chunks((int)n, (int)n_vocab, dtype), workspace};
   hipStream_t st = (hipStream_t)stream;
   return timed(what, st, [&] { return launch_sample(a, dtype, st); });
 }
