@@ -59,6 +59,14 @@ __device__ __forceinline__ float value_of(uint32_t key) { return __uint_as_float
 __device__ __forceinline__ u64 place_of(float x, int index) { return (u64)sample_key(x) << 32 | (uint32_t)~index; }
 __device__ __forceinline__ int index_of(u64 place) { return (int)~(uint32_t)place; }
 
+// The same value in every lane, to be held in scalar registers.
+__device__ __forceinline__ float uniform(float v) { return __int_as_float(__builtin_amdgcn_readfirstlane(__float_as_int(v))); }
+__device__ __forceinline__ u64 uniform(u64 v) {
+  return (u64)(uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)(v >> 32)) << 32 |
+         (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)v);
+}
+__device__ __forceinline__ double uniform(double v) { return __longlong_as_double((long long)uniform((u64)__double_as_longlong(v))); }
+
 template <typename T>
 struct Logits;
 template <>
@@ -128,7 +136,7 @@ struct Row {
   float temp, top_p, min_p, u;
   bool greedy;
 
-  __device__ void begin(const SampleArgs &a, int r) {
+  __device__ __forceinline__ void begin(const SampleArgs &a, int r) {
     x = (const T *)a.logits + (long long)r * a.stride;
     V = a.n_vocab;
     skew = (int)(((uintptr_t)x & 15) / sizeof(T));
@@ -143,17 +151,17 @@ struct Row {
     if (top_k >= V || top_k < 0) top_k = 0;
     if (top_k == 1) top_p = 1.f;
     cut = 0;
-    least = min_p > 0.f && min_p <= 1.f ? (u64)ceil((double)min_p * kUnit) : 0;
+    least = uniform(min_p > 0.f && min_p <= 1.f ? (u64)ceil((double)min_p * kUnit) : 0);
   }
   // False for a row without a distribution; max is NaN where the row holds one.
-  __device__ bool set_max(float max) {
-    m = max;
-    steps = 369.32993046757463228 / (greedy ? 1.0 : (double)temp);
+  __device__ __forceinline__ bool set_max(float max) {
+    m = uniform(max);
+    steps = uniform(369.32993046757463228 / (greedy ? 1.0 : (double)temp));
     return fabsf(max) < INFINITY && temp >= 0.f && temp < INFINITY && top_p == top_p && min_p == min_p && u == u;
   }
   __device__ bool by_list() const { return top_k > 0 && top_k <= kMostListedK; }
 
-  __device__ uint4 load(int at) const {  // elements outside the row: -inf
+  __device__ __forceinline__ uint4 load(int at) const {  // elements outside the row: -inf
     constexpr uint32_t kNegInf = sizeof(T) == 4 ? 0xff800000u : 0xff80ff80u;
     if (at >= 0 && at + VE <= V) return ldg16(x + at);
     uint32_t w[4] = {kNegInf, kNegInf, kNegInf, kNegInf};
@@ -169,8 +177,8 @@ struct Row {
   }
   // f(segment, first index of vector i's elements, the vectors) for the wave's segments of [s0, s1), the next one's loads in flight.
   template <typename F>
-  __device__ void segments(int s0, int s1, F f) const {
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  __device__ __forceinline__ void segments(int s0, int s1, F f) const {
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     int s = s0 + wave;
     if (s >= s1) return;
     auto first = [&](int seg, int i) { return seg * kSampleSeg - skew + (i * 64 + lane) * VE; };
@@ -195,24 +203,29 @@ struct Row {
   static __device__ int whole(double t) { return (int)(uint32_t)__double_as_longlong(t + 6755399441055744.0); }  // + 1.5 2^52
   static __device__ int bin_of(int n) { return -n >> 4; }
   __device__ int bin(float v) const { return bin_of(whole(exponent(v))); }
+  // No logit below it lies in bin b or above: b's own floor less a step, and the next lower float.
+  __device__ float floor_of_bin(int b) const {
+    const float f = (float)((double)m - (16.0 * b + 17.0) / steps);
+    return uniform(f > -INFINITY ? value_of(sample_key(f) - 1) : f);
+  }
   // The place within its bin, in 256 parts: larger weights first.
   __device__ int fine_bin(float v, int b) const {
     return min(max((int)((-exponent(v) - 16.0 * b + 0.5) * 16.0), 0), 255);
   }
-  // 2^n/256 from the table, times e^g for what is left, |g| <= ln(2)/512 = a:
-  // a^2 g^2 / 24 stands for the series' fourth term, which leaves 3.5e-14 at
-  // most; adding 2^52 rounds to nearest even and leaves the number
-  // in the low bits, above which the sum of 2^52's own bits is taken off.
+  // 2^(n/256) from the table, times 2^(h/256) for what is left, |h| <= 1/2: its
+  // series in h, in which a^2 h^2 stands for the fourth term's h^4 at the end
+  // a = 1/2 and leaves 3.5e-14 at most.  Adding 2^52 rounds to nearest even
+  // and leaves the number in the low bits, above which 2^52's own bits are
+  // taken off a sum.
   static constexpr u64 kMagicBits = 0x4330000000000000ull;
-  __device__ u64 magic_weight(double t, const double *table) const {
+  __device__ __forceinline__ u64 magic_weight(double t, const double *table) const {
     const double z = t + 6755399441055744.0;
     const int n = (int)(uint32_t)__double_as_longlong(z);
-    const double g = (t - (z - 6755399441055744.0)) * 0.0027076061740622862;
-    constexpr double a2 = 1.8327827e-6;
-    double p = fma(g, 1.0 / 6.0, 0.5 + a2 / 24.0);
-    p = fma(p, g, 1.0);
-    const double w = table[n & 255];
-    const double r = fma(w, p * g, w);
+    const double h = t - (z - 6755399441055744.0);
+    constexpr double c = 0.0027076061740622862, c4 = c * c * c * c / 24.0;  // c = ln(2) / 256
+    double p = fma(h, c * c * c / 6.0, c * c / 2.0 + c4 / 4.0);
+    p = fma(p, h, c) * h;
+    const double w = table[n & 255], r = fma(w, p, w);
     const u64 bits = (u64)__double_as_longlong(r) + ((u64)((uint32_t)(n >> 8) << 20) << 32);
     return (u64)__double_as_longlong(__longlong_as_double((long long)bits) + 4503599627370496.0);
   }
@@ -225,7 +238,7 @@ __device__ __forceinline__ void fill_table(SampleLds &lds) {
     const double f = j * 0.0027076061740622862;  // ln(2) / 256
     double p = 1.0;
 #pragma unroll
-    for (int i = 18; i > 0; --i) p = fma(p, f / i, 1.0);  // f below 0.7: the 19th term is under 1e-19
+    for (int i = 18; i > 0; --i) p = fma(p, f * (1.0 / i), 1.0);  // f below 0.7: the 19th term is under 1e-19
     lds.table[j] = p * kUnit;
   }
 }
@@ -318,21 +331,24 @@ __device__ __forceinline__ void mass_pass(const Row<T> &row, int s0, int s1, u64
     u64 sum = 0;
     if (all) {
 #pragma unroll
-      for (int i = 0; i < Row<T>::NV; ++i)
+      for (int i = 0; i < Row<T>::NV; ++i) {
 #pragma unroll
         for (int e = 0; e < Row<T>::VE; ++e) sum += row.magic_weight(row.exponent(Logits<T>::at(v[i], e)), lds.table);
+        __builtin_amdgcn_sched_barrier(0);  // a vector's work at a time: all of a segment's takes registers that spill
+      }
       sum -= (u64)(Row<T>::NV * Row<T>::VE) * Row<T>::kMagicBits;
     } else {
 #pragma unroll
-      for (int i = 0; i < Row<T>::NV; ++i)
+      for (int i = 0; i < Row<T>::NV; ++i) {
 #pragma unroll
         for (int e = 0; e < Row<T>::VE; ++e) {
           const float x = Logits<T>::at(v[i], e);
-          if (row.keeps(place_of(x, Row<T>::index(first, i, e)))) {
-            const u64 w = row.weight(x, lds.table);
-            sum += w >= least ? w : 0;
-          }
+          if (!__any(row.keeps(place_of(x, Row<T>::index(first, i, e))))) continue;  // most are kept nowhere in a wave
+          const u64 w = row.weight(x, lds.table);
+          sum += w >= least && row.keeps(place_of(x, Row<T>::index(first, i, e))) ? w : 0;
+          __builtin_amdgcn_sched_barrier(0);
         }
+      }
     }
     sum = wave_sum64(sum);
     if ((threadIdx.x & 63) == 0) seg(s, sum);
@@ -344,7 +360,7 @@ template <typename T>
 __device__ __forceinline__ void bin_pass(const Row<T> &row, int s0, int s1, bool counts, SampleLds &lds) {
   row.segments(s0, s1, [&](int, int first, const uint4 *v) {
 #pragma unroll
-    for (int i = 0; i < Row<T>::NV; ++i)
+    for (int i = 0; i < Row<T>::NV; ++i) {
 #pragma unroll
       for (int e = 0; e < Row<T>::VE; ++e) {
         const float x = Logits<T>::at(v[i], e);
@@ -353,37 +369,42 @@ __device__ __forceinline__ void bin_pass(const Row<T> &row, int s0, int s1, bool
         if (b < kLowest && (row.cut == 0 || row.keeps(place_of(x, Row<T>::index(first, i, e)))))
           atomicAdd(&lds.bins[b], counts ? 1ull : row.magic_weight(t, lds.table) - Row<T>::kMagicBits);
       }
+      __builtin_amdgcn_sched_barrier(0);
+    }
   });
 }
 
-// put(place) for what is kept of the bins lo .. hi, hi below kLowest.
+// put(value, index) for the row's logits from `floor` up, above -infinity.
 template <typename T, typename Put>
-__device__ __forceinline__ void list_pass(const Row<T> &row, int s0, int s1, int lo, int hi, Put put) {
+__device__ __forceinline__ void list_pass(const Row<T> &row, int s0, int s1, float floor, Put put) {
   row.segments(s0, s1, [&](int, int first, const uint4 *v) {
 #pragma unroll
-    for (int i = 0; i < Row<T>::NV; ++i)
+    for (int i = 0; i < Row<T>::NV; ++i) {
+      float most = Logits<T>::at(v[i], 0);
+#pragma unroll
+      for (int e = 1; e < Row<T>::VE; ++e) most = fmaxf(most, Logits<T>::at(v[i], e));
+      if (!__any(most >= floor)) continue;
 #pragma unroll
       for (int e = 0; e < Row<T>::VE; ++e) {
         const float x = Logits<T>::at(v[i], e);
-        const int b = row.bin(x);
-        if (b >= lo && b <= hi) {
-          const u64 place = place_of(x, Row<T>::index(first, i, e));
-          if (row.keeps(place)) put(place);
-        }
+        if (x >= floor && x > -INFINITY) put(x, Row<T>::index(first, i, e));
       }
+    }
   });
 }
 
-// The same for bin b, and the weights of each segment's tokens in the bins above it.
+// put(place) for what the row keeps of bin b, and the weights of each segment's tokens in the bins above it.
 template <typename T, typename Put, typename Seg>
 __device__ __forceinline__ void list_and_mass_pass(const Row<T> &row, int s0, int s1, int b, SampleLds &lds, Put put, Seg seg) {
+  const float floor = row.floor_of_bin(b);
   row.segments(s0, s1, [&](int s, int first, const uint4 *v) {
     u64 sum = 0;
 #pragma unroll
-    for (int i = 0; i < Row<T>::NV; ++i)
+    for (int i = 0; i < Row<T>::NV; ++i) {
 #pragma unroll
       for (int e = 0; e < Row<T>::VE; ++e) {
         const float x = Logits<T>::at(v[i], e);
+        if (!__any(x >= floor)) continue;
         const double t = row.exponent(x);
         const int its = Row<T>::bin_of(Row<T>::whole(t));
         if (its <= b) {
@@ -397,6 +418,8 @@ __device__ __forceinline__ void list_and_mass_pass(const Row<T> &row, int s0, in
           }
         }
       }
+      __builtin_amdgcn_sched_barrier(0);
+    }
     sum = wave_sum64(sum);
     if ((threadIdx.x & 63) == 0) seg(s, sum);
   });
@@ -406,7 +429,7 @@ __device__ __forceinline__ void list_and_mass_pass(const Row<T> &row, int s0, in
 // The smallest prefix of what the row keeps whose measure reaches goal >= 1,
 // which it does, by histograms over the key's bits: one workgroup, any row.
 template <typename T>
-__device__ void cut_by_bits(Row<T> &row, u64 goal, bool counts, SampleLds &lds) {
+__device__ __forceinline__ void cut_by_bits(Row<T> &row, u64 goal, bool counts, SampleLds &lds) {
   constexpr int VE = Row<T>::VE, kTile = kSampleThreads * VE;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, tiles = (row.V + row.skew + kTile - 1) / kTile;
   auto measure = [&](float v) -> u64 { return counts ? 1 : row.weight(v, lds.table); };
@@ -486,52 +509,87 @@ __device__ void cut_by_bits(Row<T> &row, u64 goal, bool counts, SampleLds &lds) 
     if (left <= 0) break;
   }
   __syncthreads();
-  row.cut = (u64)prefix << 32 | (uint32_t)~lds.index;
+  row.cut = uniform((u64)prefix << 32 | (uint32_t)~lds.index);
   __syncthreads();
 }
 
-// The cut among the lds.count <= kSampleList listed places of bin b: the
-// smallest prefix of them whose measure reaches goal, which it does.
+// The weights of the listed places into lds.w.
+template <typename T>
+__device__ __forceinline__ void weigh_list(const Row<T> &row, SampleLds &lds) {
+  for (int i = threadIdx.x; i < lds.count; i += kSampleThreads) lds.w[i] = row.weight(value_of((uint32_t)(lds.list[i] >> 32)), lds.table);
+  __syncthreads();
+}
+// Among the picked ones of the listed places, the one at which the running
+// measure reaches goal.  over(i, j): i comes before j.  The running measure
+// starts at 0; called after a barrier, ends with one.
+template <typename Over, typename Measure, typename Found>
+__device__ __forceinline__ void reach_in_picks(u64 goal, Over over, Measure measure, Found found, SampleLds &lds) {
+  const uint32_t *const pick = (const uint32_t *)lds.bins;
+  const int c = lds.picked;
+  for (int i = threadIdx.x; i < c; i += kSampleThreads) {
+    const int me = pick[i];
+    u64 before = 0;
+    for (int j = 0; j < c; ++j) before += over(pick[j], me) ? measure(pick[j]) : 0;
+    if (goal > before && goal <= before + measure(me)) found(me, before);
+  }
+  __syncthreads();
+}
+// Indexes of the listed places for which in(i) holds, into the bins' space.  Called after a barrier, ends with one.
+template <typename In>
+__device__ __forceinline__ void pick_from_list(In in, SampleLds &lds) {
+  static_assert(kSampleList * sizeof(uint32_t) <= kBins * sizeof(u64), "picks fit the bins");
+  uint32_t *const pick = (uint32_t *)lds.bins;
+  if (threadIdx.x == 0) lds.picked = 0;
+  __syncthreads();
+  for (int i = threadIdx.x; i < lds.count; i += kSampleThreads)
+    if (in(i)) pick[atomicAdd(&lds.picked, 1)] = i;
+  __syncthreads();
+}
+// The cut among the lds.count <= kSampleList listed places that the row
+// keeps, of bin b or, for b < 0, of any: the smallest prefix of them whose
+// measure reaches goal, which it does.  lds.w holds their weights.
 template <typename T>
 __device__ __forceinline__ u64 cut_in_list(const Row<T> &row, int b, u64 goal, bool counts, SampleLds &lds) {
   const int tid = threadIdx.x, n = lds.count;
+  auto value = [&](int i) { return value_of((uint32_t)(lds.list[i] >> 32)); };
+  auto measure = [&](int i) -> u64 { return counts ? 1 : lds.w[i]; };
+  if (b < 0) {
+    clear_bins(lds, kBins);
+    __syncthreads();
+    for (int i = tid; i < n; i += kSampleThreads)
+      if (row.keeps(lds.list[i])) atomicAdd(&lds.bins[row.bin(value(i))], measure(i));
+    __syncthreads();
+    find_reach(kBins, goal, [&](int i) { return lds.bins[i]; }, lds);
+    b = lds.found;
+    goal -= lds.found_above;
+    __syncthreads();
+  }
+  auto fine = [&](int i) { return row.keeps(lds.list[i]) && row.bin(value(i)) == b ? row.fine_bin(value(i), b) : -1; };
   clear_bins(lds, 256);
-  if (tid == 0) lds.picked = 0;
   __syncthreads();
   for (int i = tid; i < n; i += kSampleThreads) {
-    const float v = value_of((uint32_t)(lds.list[i] >> 32));
-    const u64 w = counts ? 1 : row.weight(v, lds.table);
-    lds.w[i] = w;
-    atomicAdd(&lds.bins[row.fine_bin(v, b)], w);
+    const int f = fine(i);
+    if (f >= 0) atomicAdd(&lds.bins[f], measure(i));
   }
   __syncthreads();
   find_reach(256, goal, [&](int i) { return lds.bins[i]; }, lds);
-  const int fine = lds.found;
-  const u64 above = lds.found_above;
-  // the fine bin's places go to the list's front: indexes only, the places stay where they are
-  uint32_t *const pick = (uint32_t *)lds.bins;
-  static_assert(kSampleList * sizeof(uint32_t) <= kBins * sizeof(u64), "picks fit the bins");
+  const int f = lds.found;
+  goal -= lds.found_above;
   __syncthreads();
-  for (int i = tid; i < n; i += kSampleThreads)
-    if (row.fine_bin(value_of((uint32_t)(lds.list[i] >> 32)), b) == fine) pick[atomicAdd(&lds.picked, 1)] = i;
-  __syncthreads();
-  const int c = lds.picked;
-  for (int i = tid; i < c; i += kSampleThreads) {
-    const u64 mine = lds.list[pick[i]], w = lds.w[pick[i]];
-    u64 over = above;
-    for (int j = 0; j < c; ++j) {
-      const u64 other = lds.list[pick[j]];
-      over += other > mine ? lds.w[pick[j]] : 0;
-    }
-    if (goal > over && goal <= over + w) lds.found_above = mine;
-  }
-  __syncthreads();
-  const u64 cut = lds.found_above;
+  pick_from_list([&](int i) { return fine(i) == f; }, lds);
+  reach_in_picks(goal, [&](int i, int j) { return lds.list[i] > lds.list[j]; }, measure,
+                 [&](int i, u64) { lds.found_above = lds.list[i]; }, lds);
+  const u64 cut = uniform(lds.found_above);
   __syncthreads();
   return cut;
 }
 
 // ---------------------------------------------------------------- the drawing
+// The weight that top-p wants of a sum.
+__device__ __forceinline__ u64 wanted(float top_p, u64 mass) {
+  const double goal = ceil((double)top_p * (double)mass);
+  return goal >= 1.0 ? (u64)goal : 1;
+}
 __device__ __forceinline__ u64 goal_of(float u, u64 total) {
   const double g = floor((double)u * (double)total);
   return g > 0.0 ? (g < (double)total ? min((u64)g, total - 1) : total - 1) : 0;
@@ -592,55 +650,43 @@ __device__ __forceinline__ void draw_from_segments(const SampleArgs &a, const Ro
   }
 }
 
-// Among the lds.count <= kSampleList listed places, which hold at least the row's first top_k.
+// Among the lds.count <= kSampleList listed places, which hold at least the
+// row's first top_k or all that have a weight.
 template <typename T>
-__device__ __forceinline__ void draw_from_list(const SampleArgs &a, const Row<T> &row, int r, SampleLds &lds) {
-  constexpr int kPer = kSampleList / kSampleThreads;
+__device__ __forceinline__ void draw_from_list(const SampleArgs &a, Row<T> row, int r, SampleLds &lds) {
   const int tid = threadIdx.x, n = lds.count;
-  for (int i = tid; i < n; i += kSampleThreads) lds.w[i] = row.weight(value_of((uint32_t)(lds.list[i] >> 32)), lds.table);
+  weigh_list(row, lds);
+  if (row.top_k < n) row.cut = cut_in_list(row, -1, (u64)row.top_k, true, lds);
+  if (row.top_p < 1.f) {
+    u64 mass = 0;
+    for (int i = tid; i < n; i += kSampleThreads) mass += row.keeps(lds.list[i]) ? lds.w[i] : 0;
+    mass = block_sum64(mass, lds);
+    __syncthreads();
+    row.cut = cut_in_list(row, -1, wanted(row.top_p, mass), false, lds);
+  }
+  // by index: bins of 2^shift of them
+  const int shift = max(0, 32 - __clz(row.V) - 9);
+  static_assert(kBins >= 512, "a bin for every 2^shift indexes");
+  clear_bins(lds, kBins);
   __syncthreads();
-  u64 mass = 0, above[kPer];
-  int rank[kPer];
-#pragma unroll
-  for (int p = 0; p < kPer; ++p) {
-    const int i = tid + p * kSampleThreads;
-    rank[p] = 0;
-    above[p] = 0;
-    if (i >= n) continue;
-    const u64 mine = lds.list[i];
-#pragma unroll 4
-    for (int j = 0; j < n; ++j) {
-      const bool over = lds.list[j] > mine;
-      rank[p] += over;
-      above[p] += over ? lds.w[j] : 0;
-    }
-    if (rank[p] < row.top_k) mass += lds.w[i];
-  }
-  mass = block_sum64(mass, lds);
-  const u64 need = row.top_p < 1.f ? (u64)fmax(ceil((double)row.top_p * (double)mass), 0.0) : ~0ull;
   u64 total = 0;
-#pragma unroll
-  for (int p = 0; p < kPer; ++p) {
-    const int i = tid + p * kSampleThreads;
-    if (i >= n) continue;
-    const u64 w = lds.w[i];
-    const bool stays = rank[p] == 0 || (rank[p] < row.top_k && above[p] < need && w >= row.least);
-    if (!stays) lds.w[i] = 0;
-    total += stays ? w : 0;
-  }
+  auto stays = [&](int i) { return row.keeps(lds.list[i]) && lds.w[i] >= row.least; };
+  for (int i = tid; i < n; i += kSampleThreads)
+    if (stays(i)) {
+      total += lds.w[i];
+      atomicAdd(&lds.bins[index_of(lds.list[i]) >> shift], lds.w[i]);
+    }
   total = block_sum64(total, lds);
-  const u64 goal = goal_of(row.u, total);
-#pragma unroll
-  for (int p = 0; p < kPer; ++p) {
-    const int i = tid + p * kSampleThreads;
-    if (i >= n || lds.w[i] == 0) continue;
-    const u64 w = lds.w[i];
-    const uint32_t mine = (uint32_t)lds.list[i];  // the index's complement: larger is earlier
-    u64 before = 0;
-#pragma unroll 4
-    for (int j = 0; j < n; ++j) before += (uint32_t)lds.list[j] > mine ? lds.w[j] : 0;
-    if (goal >= before && goal < before + w) write_result(a, row, r, index_of(lds.list[i]), value_of((uint32_t)(lds.list[i] >> 32)), total);
-  }
+  u64 goal = goal_of(row.u, total) + 1;
+  __syncthreads();
+  find_reach(512, goal, [&](int i) { return lds.bins[i]; }, lds);
+  const int b = lds.found;
+  goal -= lds.found_above;
+  __syncthreads();
+  pick_from_list([&](int i) { return stays(i) && index_of(lds.list[i]) >> shift == b; }, lds);
+  reach_in_picks(goal, [&](int i, int j) { return (uint32_t)lds.list[i] > (uint32_t)lds.list[j]; },  // the index's complement
+                 [&](int i) { return lds.w[i]; },
+                 [&](int i, u64) { write_result(a, row, r, index_of(lds.list[i]), value_of((uint32_t)(lds.list[i] >> 32)), total); }, lds);
 }
 
 // ---------------------------------------------------------------- one workgroup's way through a row
@@ -655,24 +701,32 @@ __device__ __forceinline__ void store_part(float *parts, int shift, int seg, flo
   for (int i = 0; i < shift; ++i) mine = fmaxf(mine, __shfl_xor(mine, 1 << i, 64));
   if ((lane & ((1 << shift) - 1)) == 0) parts[(seg << (6 - shift)) + (lane >> shift)] = mine;
 }
-// The bin that top_k of the parts' maxima reach: at least as many logits lie in it and the ones above.
+// A value that at least top_k of the row's logits reach, or all that have a
+// weight: the smallest of the parts' maxima in the bins that top_k of them reach.
 template <typename T>
-__device__ __forceinline__ int listed_bins(const Row<T> &row, const float *parts, SampleLds &lds) {
+__device__ __forceinline__ float list_floor(const Row<T> &row, const float *parts, SampleLds &lds) {
+  const int tid = threadIdx.x, n = row.segs << (6 - part_shift(row.segs));
   clear_bins(lds, kBins);
   __syncthreads();
-  const int n = row.segs << (6 - part_shift(row.segs));
-  for (int i = threadIdx.x; i < n; i += kSampleThreads) {
+  for (int i = tid; i < n; i += kSampleThreads) {
     const int b = row.bin(parts[i]);
     if (b < kLowest) atomicAdd(&lds.bins[b], 1ull);
   }
   __syncthreads();
   find_reach(kBins, (u64)row.top_k, [&](int i) { return lds.bins[i]; }, lds);
-  return min(lds.found, kLowest - 1);  // fewer parts hold anything: all that has a weight
-}
-// The weight that top-p wants of a sum.
-__device__ __forceinline__ u64 wanted(float top_p, u64 mass) {
-  const double goal = ceil((double)top_p * (double)mass);
-  return goal >= 1.0 ? (u64)goal : 1;
+  const int b = __builtin_amdgcn_readfirstlane(lds.found);
+  if (b == kBins) return row.floor_of_bin(kLowest - 1);
+  float f = INFINITY;
+  for (int i = tid; i < n; i += kSampleThreads)
+    if (row.bin(parts[i]) <= b) f = fminf(f, parts[i]);
+  f = __int_as_float(wave_reduce(__float_as_int(f), 0x7f800000,
+                                 [](int a, int b) { return __float_as_int(fminf(__int_as_float(a), __int_as_float(b))); }));
+  if ((tid & 63) == 0) lds.m[tid >> 6] = f;
+  __syncthreads();
+  f = lds.m[0];
+#pragma unroll
+  for (int w = 1; w < kWaves; ++w) f = fminf(f, lds.m[w]);
+  return uniform(f);
 }
 // lds.bins' sum, the bin in which top-p's cut lies and what the cut wants of it.
 template <typename T>
@@ -684,11 +738,12 @@ __device__ __forceinline__ int top_p_bin(const Row<T> &row, u64 *wants, SampleLd
   __syncthreads();
   find_reach(kBins, goal, [&](int i) { return lds.bins[i]; }, lds);
   *wants = goal - lds.found_above;
-  return lds.found;
+  return __builtin_amdgcn_readfirstlane(lds.found);
 }
 // Top-p's cut among the listed places of its bin; those that it keeps join their segments' sums.
 template <typename T>
 __device__ __forceinline__ void cut_and_add(Row<T> &row, int b, u64 wants, SampleLds &lds) {
+  weigh_list(row, lds);
   row.cut = cut_in_list(row, b, wants, false, lds);
   for (int i = threadIdx.x; i < lds.count; i += kSampleThreads)
     if (row.keeps(lds.list[i]) && lds.w[i] >= row.least)
@@ -698,7 +753,10 @@ __device__ __forceinline__ void cut_and_add(Row<T> &row, int b, u64 wants, Sampl
 
 // Whatever a list could not hold.
 template <typename T>
-__device__ void draw_by_bits(const SampleArgs &a, Row<T> &row, int r, SampleLds &lds) {
+__device__ __attribute__((noinline)) void draw_by_bits(const SampleArgs &a, int r, float m, SampleLds &lds) {
+  Row<T> row;
+  row.begin(a, r);
+  row.set_max(m);
   auto to_seg = [&](int s, u64 sum) { lds.seg[s] = sum; };
   row.cut = 0;
   if (row.top_k > 0) cut_by_bits(row, (u64)row.top_k, true, lds);
@@ -715,9 +773,9 @@ __device__ void draw_by_bits(const SampleArgs &a, Row<T> &row, int r, SampleLds 
   draw_from_segments(a, row, r, lds);
 }
 
-// A row that does not go by a list of its first top_k.
+// A row that does not go by a list of its first top_k; false where a list overflows.
 template <typename T>
-__device__ void draw_by_bins(const SampleArgs &a, Row<T> &row, int r, SampleLds &lds) {
+__device__ __forceinline__ bool draw_by_bins(const SampleArgs &a, Row<T> row, int r, SampleLds &lds) {
   const int tid = threadIdx.x;
   auto to_list = [&](u64 place) { put(lds, place); };
   auto to_seg = [&](int s, u64 sum) { lds.seg[s] = sum; };
@@ -731,12 +789,9 @@ __device__ void draw_by_bins(const SampleArgs &a, Row<T> &row, int r, SampleLds 
     if (lds.found < kBins) {  // else fewer have a weight
       const int b = lds.found;
       const u64 wants = (u64)row.top_k - lds.found_above;
-      list_pass(row, 0, row.segs, b, b, to_list);
+      list_and_mass_pass(row, 0, row.segs, b, lds, to_list, [](int, u64) {});
       __syncthreads();
-      if (lds.count > kSampleList) {
-        draw_by_bits(a, row, r, lds);
-        return;
-      }
+      if (lds.count > kSampleList) return false;
       row.cut = cut_in_list(row, b, wants, true, lds);
     }
     __syncthreads();
@@ -751,16 +806,14 @@ __device__ void draw_by_bins(const SampleArgs &a, Row<T> &row, int r, SampleLds 
     const int b = top_p_bin(row, &wants, lds);
     list_and_mass_pass(row, 0, row.segs, b, lds, to_list, to_seg);
     __syncthreads();
-    if (lds.count > kSampleList) {
-      draw_by_bits(a, row, r, lds);
-      return;
-    }
+    if (lds.count > kSampleList) return false;
     cut_and_add(row, b, wants, lds);
   } else {
     mass_pass(row, 0, row.segs, row.least, lds, to_seg);
     __syncthreads();
   }
   draw_from_segments(a, row, r, lds);
+  return true;
 }
 
 // Grid: rows.
@@ -780,17 +833,19 @@ __global__ __launch_bounds__(kSampleThreads, 4) void sample_kernel(SampleArgs a)
     write_none(a, r);
     return;
   }
-  if (!by_list) {
-    draw_by_bins(a, row, r, lds);
-    return;
+  bool done;
+  if (by_list) {
+    const float floor = list_floor(row, lds.parts, lds);
+    if (threadIdx.x == 0) lds.count = 0;
+    __syncthreads();
+    list_pass(row, 0, row.segs, floor, [&](float v, int i) { put(lds, place_of(v, i)); });
+    __syncthreads();
+    done = lds.count <= kSampleList;
+    if (done) draw_from_list(a, row, r, lds);
+  } else {
+    done = draw_by_bins(a, row, r, lds);
   }
-  const int b = listed_bins(row, lds.parts, lds);
-  if (threadIdx.x == 0) lds.count = 0;
-  __syncthreads();
-  list_pass(row, 0, row.segs, 0, b, [&](u64 place) { put(lds, place); });
-  __syncthreads();
-  if (lds.count <= kSampleList) draw_from_list(a, row, r, lds);
-  else draw_by_bits(a, row, r, lds);
+  if (!done) draw_by_bits<T>(a, r, m, lds);
 }
 
 // ---------------------------------------------------------------- few rows: a row on several workgroups
@@ -863,8 +918,8 @@ __global__ __launch_bounds__(kSampleThreads, 4) void sample_sum_kernel(SampleArg
   SampleRow &w = row_record(a, k.r);
   if (!max_of_chunks(a, w, row)) return;
   if (row.by_list()) {
-    const int b = listed_bins(row, w.parts, lds);
-    list_pass(row, k.s0, k.s1, 0, b, [&](u64 place) { put_global(w, place); });
+    const float floor = list_floor(row, w.parts, lds);
+    list_pass(row, k.s0, k.s1, floor, [&](float v, int i) { put_global(w, place_of(v, i)); });
   } else if (row.top_k == 0) {
     fill_table(lds);
     if (row.top_p < 1.f) {
@@ -919,29 +974,26 @@ __global__ __launch_bounds__(kSampleThreads, 4) void sample_draw_kernel(SampleAr
     return;
   }
   fill_table(lds);
-  if (row.top_k > 0 && !row.by_list()) {
-    __syncthreads();
-    draw_by_bins(a, row, r, lds);
-    return;
-  }
   const bool by_list = row.by_list(), listed = by_list || row.top_p < 1.f;
-  const int n = listed ? w.count : 0;
-  if (n > kSampleList) {
-    __syncthreads();
-    draw_by_bits(a, row, r, lds);
-    return;
-  }
+  const int n = listed && (by_list || row.top_k == 0) ? w.count : 0;
   if (tid == 0) lds.count = n;
-  for (int i = tid; i < n; i += kSampleThreads) lds.list[i] = w.list[i];
-  if (!by_list)
-    for (int i = tid; i < row.segs; i += kSampleThreads) lds.seg[i] = w.seg[i];
-  __syncthreads();
-  if (by_list) {
-    draw_from_list(a, row, r, lds);
-    return;
+  bool done = n <= kSampleList;
+  if (row.top_k > 0 && !by_list) {
+    __syncthreads();
+    done = draw_by_bins(a, row, r, lds);
+  } else if (done) {
+    for (int i = tid; i < n; i += kSampleThreads) lds.list[i] = w.list[i];
+    if (!by_list)
+      for (int i = tid; i < row.segs; i += kSampleThreads) lds.seg[i] = w.seg[i];
+    __syncthreads();
+    if (by_list) {
+      draw_from_list(a, row, r, lds);
+    } else {
+      if (listed) cut_and_add(row, w.bin, w.wants, lds);
+      draw_from_segments(a, row, r, lds);
+    }
   }
-  if (listed) cut_and_add(row, w.bin, w.wants, lds);
-  draw_from_segments(a, row, r, lds);
+  if (!done) draw_by_bits<T>(a, r, row.m, lds);
 }
 
 // ---------------------------------------------------------------- launcher
