@@ -407,15 +407,12 @@ __device__ __forceinline__ void list_and_mass_pass(const Row<T> &row, int s0, in
         if (!__any(x >= floor)) continue;
         const double t = row.exponent(x);
         const int its = Row<T>::bin_of(Row<T>::whole(t));
-        if (its <= b) {
+        u64 w = row.magic_weight(t, lds.table) - Row<T>::kMagicBits;
+        if (row.cut | row.least) w = w >= row.least && row.keeps(place_of(x, Row<T>::index(first, i, e))) ? w : 0;
+        sum += its < b ? w : 0;
+        if (__any(its == b) && its == b) {
           const u64 place = place_of(x, Row<T>::index(first, i, e));
-          if (row.keeps(place)) {
-            if (its == b) put(place);
-            else {
-              const u64 w = row.magic_weight(t, lds.table) - Row<T>::kMagicBits;
-              sum += w >= row.least ? w : 0;
-            }
-          }
+          if (row.keeps(place)) put(place);
         }
       }
       __builtin_amdgcn_sched_barrier(0);
@@ -610,7 +607,7 @@ __device__ __forceinline__ void write_none(const SampleArgs &a, int r) {
 // By the sums of the row's segments, lds.seg, of what it keeps.
 template <typename T>
 __device__ __forceinline__ void draw_from_segments(const SampleArgs &a, const Row<T> &row, int r, SampleLds &lds) {
-  constexpr int kPer = kSampleSeg / kSampleThreads;
+  constexpr int kPer = std::max(kSampleSeg / kSampleThreads, Row<T>::VE);
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   u64 total = 0;
   for (int i = tid; i < row.segs; i += kSampleThreads) total += lds.seg[i];
@@ -623,7 +620,7 @@ __device__ __forceinline__ void draw_from_segments(const SampleArgs &a, const Ro
   __syncthreads();
   uint4 v[kPer / Row<T>::VE];
 #pragma unroll
-  for (int i = 0; i < kPer / Row<T>::VE; ++i) v[i] = row.load(at + i * Row<T>::VE);
+  for (int i = 0; i < kPer / Row<T>::VE; ++i) v[i] = row.load(tid * kPer < kSampleSeg ? at + i * Row<T>::VE : INT_MIN);
   u64 w[kPer], sum = 0;
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
@@ -876,13 +873,12 @@ struct Chunk {
 };
 template <typename T>
 __device__ __forceinline__ bool max_of_chunks(const SampleArgs &a, const SampleRow &w, Row<T> &row) {
-  float m = -INFINITY;
-  bool nan = false;
-  for (int c = 0; c < a.chunks; ++c) {
-    m = fmaxf(m, w.max[c]);
-    nan |= w.max[c] != w.max[c];
-  }
-  return row.set_max(nan ? __uint_as_float(0x7fc00000u) : m);
+  const int lane = threadIdx.x & 63;
+  static_assert(kSampleMaxChunks <= 64, "a lane for every chunk");
+  const float mine = lane < a.chunks ? w.max[lane] : -INFINITY;
+  const float m = __int_as_float(wave_reduce(__float_as_int(mine), (int)0xff800000u,
+                                             [](int a, int b) { return __float_as_int(fmaxf(__int_as_float(a), __int_as_float(b))); }));
+  return row.set_max(__any(mine != mine) ? __uint_as_float(0x7fc00000u) : m);
 }
 __device__ __forceinline__ void put_global(SampleRow &w, u64 place) {
   const int at = __hip_atomic_fetch_add(&w.count, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
@@ -948,6 +944,7 @@ __global__ __launch_bounds__(kSampleThreads, 4) void sample_list_kernel(SampleAr
   fill_table(lds);
   for (int i = threadIdx.x; i < kBins; i += kSampleThreads) {
     u64 sum = 0;
+#pragma unroll 8
     for (int c = 0; c < a.chunks; ++c) sum += w.bins[c][i];
     lds.bins[i] = sum;
   }
