@@ -178,86 +178,179 @@ __device__ __forceinline__ void store4(u16 *p, f32x4 v) {
 __device__ __forceinline__ void store4(float *p, f32x4 v) { *(float4 *)p = make_float4(v[0], v[1], v[2], v[3]); }
 
 // ---------------------------------------------------------------- few rows
-// Up to 64 rows: W is streamed once and bounds the call.  A workgroup owns
-// 16 BOF output features and all rows; its eight waves share the columns out
-// by blocks, each straight into registers, and meet in LDS at the end, in the
-// order of the waves.
+// W is streamed once and bounds the call.  128 columns of a row of codes, by
+// a lane's two 16-byte loads; columns past k are zeros.
+__device__ __forceinline__ Codes fetch_block(const uint8_t *row, int block, int k) {
+  const int c0 = ((int)threadIdx.x & 48) + block * kFp8Block;  // lane / 16 * 16
+  Codes c;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) c.h[h] = c0 + 64 * h < k ? ldg16(row + c0 + 64 * h) : z4();
+  return c;
+}
+
+// Up to 16 rows.  A workgroup owns 16 output features; its eight waves share
+// the columns out by blocks, W and x straight into registers, and meet in LDS
+// at the end, in the order of the waves.
 constexpr int kFewWaves = 8;
-template <typename Y, int BOF, int NB>
+template <typename Y>
 __global__ __launch_bounds__(kFewWaves * 64) void matmul_few_kernel(Fp8Args p) {
   constexpr int U = 4;  // blocks of W in flight
-  __shared__ f32x4 part[kFewWaves][BOF][NB][64];
+  __shared__ f32x4 part[kFewWaves][64];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int o0 = blockIdx.x * 16 * BOF, blocks = (p.k + kFp8Block - 1) / kFp8Block;
-  const int c0 = (lane >> 4) * 16;
-  const uint8_t *wrow[BOF], *xrow[NB];
-  const float *xs[NB];
+  const int o0 = blockIdx.x * 16, blocks = (p.k + kFp8Block - 1) / kFp8Block;
+  const int r = min(lane & 15, p.n - 1);
+  const uint8_t *wrow = p.W + min(o0 + (lane & 15), p.n_out - 1) * p.w_stride, *xrow = p.x + r * p.x_stride;
+  const float *xs = p.x_scale + r * p.xs_stride, *ws = p.w_scale + (o0 / kFp8Block) * p.ws_stride;
+  f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+  Codes w[U];
 #pragma unroll
-  for (int b = 0; b < BOF; ++b) wrow[b] = p.W + min(o0 + 16 * b + (lane & 15), p.n_out - 1) * p.w_stride;
-#pragma unroll
-  for (int b = 0; b < NB; ++b) {
-    const int r = min(16 * b + (lane & 15), p.n - 1);
-    xrow[b] = p.x + r * p.x_stride;
-    xs[b] = p.x_scale + r * p.xs_stride;
-  }
-  const float *ws = p.w_scale + (o0 / kFp8Block) * p.ws_stride;
-  auto fetch = [&](const uint8_t *row, int kb) {  // columns past k are zeros
-    Codes c;
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int at = kb * kFp8Block + 64 * h + c0;
-      c.h[h] = at < p.k ? ldg16(row + at) : z4();
-    }
-    return c;
-  };
-  f32x4 acc[BOF][NB];
-#pragma unroll
-  for (int a = 0; a < BOF; ++a)
-#pragma unroll
-    for (int b = 0; b < NB; ++b) acc[a][b] = f32x4{0.f, 0.f, 0.f, 0.f};
-  Codes w[U][BOF];
-#pragma unroll
-  for (int u = 0; u < U; ++u)
-#pragma unroll
-    for (int a = 0; a < BOF; ++a) w[u][a] = fetch(wrow[a], wave + u * kFewWaves);
+  for (int u = 0; u < U; ++u) w[u] = fetch_block(wrow, wave + u * kFewWaves, p.k);
   for (int kb = wave; kb < blocks; kb += U * kFewWaves) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int at = kb + u * kFewWaves;
       if (at >= blocks) break;
-      Codes x[NB];
-      float s[NB];
-      const float wsc = ws[at];
+      const Codes x = fetch_block(xrow, at, p.k);
+      const float s = xs[at] * ws[at];
+      const Operand<Y> wo(w[u]);
+      w[u] = fetch_block(wrow, at + U * kFewWaves, p.k);
+      const f32x4 v = Operand<Y>::product(wo, Operand<Y>(x));
 #pragma unroll
-      for (int b = 0; b < NB; ++b) {
-        x[b] = fetch(xrow[b], at);
-        s[b] = xs[b][at] * wsc;
+      for (int i = 0; i < 4; ++i) acc[i] = fmaf(v[i], s, acc[i]);
+    }
+  }
+  part[wave][lane] = acc;
+  __syncthreads();
+  if (tid >= 64) return;
+  f32x4 v = part[0][lane];
+#pragma unroll
+  for (int s = 1; s < kFewWaves; ++s) v += part[s][lane];
+  const int row = lane & 15, o = o0 + (lane >> 4) * 4;
+  if (row < p.n && o < p.n_out) store4((Y *)p.y + row * p.y_stride + o, v);
+}
+
+// Up to 16 NB rows.  Every workgroup reads all of x, a part of 64 KB at a time
+// (1024 columns of 64 rows), through registers into the half of LDS that the
+// part before the last has left, while W streams into registers, eight blocks
+// of a wave ahead and across the parts.  Of the eight waves RG take 16 output
+// features each and KG = 8 / RG share the columns out by blocks, as many of
+// the former as leave every CU a workgroup.  Rows of a block lie as in the
+// tiles below.  Loads return in order, so that x straight into the operands'
+// registers makes every wait for x one for W (64 rows by 32000 x 4096: 68 us;
+// 40 with both operands through LDS).
+template <typename Y, int NB, int RG>
+__global__ __launch_bounds__(512) void matmul_rows_kernel(Fp8Args p) {
+  constexpr int KG = 8 / RG, U = 8, kRows = 16 * NB;
+  constexpr int kPart = 512 / kRows;  // blocks of a part
+  constexpr int kEach = kPart / KG;   // of a wave
+  constexpr int kIns = 512 * 8 / 512; // 16-byte chunks that a thread brings
+  static_assert(kPart * kRows == 512 && kEach * KG == kPart && (U % kEach == 0 || kEach % U == 0), "parts of 512 rows of a block");
+  __shared__ __attribute__((aligned(16))) uint4 xl[2][512 * 8];
+  __shared__ float sl[2][512];
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int rg = wave % RG, kg = wave / RG;
+  const int o0 = (blockIdx.x * RG + rg) * 16, blocks = (p.k + kFp8Block - 1) / kFp8Block;
+  const uint8_t *wrow = p.W + min(o0 + (lane & 15), p.n_out - 1) * p.w_stride;
+  const float *ws = p.w_scale + (min(o0, p.n_out - 1) / kFp8Block) * p.ws_stride;
+
+  // This thread's chunks of a part: chunk tid % 8 of rows tid / 8 + 64 i, and the scale of row tid.
+  uint4 xr[kIns];
+  float sr;
+  auto fetch_x = [&](int part) {
+#pragma unroll
+    for (int i = 0; i < kIns; ++i) {
+      const int rr = (tid >> 3) + 64 * i, row = min(rr % kRows, p.n - 1);
+      const int at = (part * kPart + rr / kRows) * kFp8Block + (tid & 7) * 16;
+      xr[i] = ldg16(p.x + row * p.x_stride + (at < p.k ? at : 0));
+    }
+    sr = p.x_scale[min(tid % kRows, p.n - 1) * p.xs_stride + min(part * kPart + tid / kRows, blocks - 1)];
+  };
+  // Columns past k are zeros, by masks: loads inside a branch make the wave wait for all of them where it ends.
+  auto keep_x = [&](int part) {
+    uint4 *const to = xl[part & 1];
+#pragma unroll
+    for (int i = 0; i < kIns; ++i) {
+      const int rr = (tid >> 3) + 64 * i, slot = (tid & 7) ^ ((rr >> 1) & 7);
+      const uint32_t m = (part * kPart + rr / kRows) * kFp8Block + (tid & 7) * 16 < p.k ? ~0u : 0u;
+      to[rr * 8 + slot] = make_uint4(xr[i].x & m, xr[i].y & m, xr[i].z & m, xr[i].w & m);
+    }
+    sl[part & 1][tid] = sr;
+  };
+  // W's columns past k are any others of the row: x is 0 there.
+  auto fetch_w = [&](int block) {
+    Codes c;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int at = block * kFp8Block + 64 * h + (lane >> 4) * 16;
+      c.h[h] = ldg16(wrow + (at < p.k ? at : 0));
+    }
+    return c;
+  };
+
+  f32x4 acc[NB];
+#pragma unroll
+  for (int b = 0; b < NB; ++b) acc[b] = f32x4{0.f, 0.f, 0.f, 0.f};
+  const int parts = (blocks + kPart - 1) / kPart, all = parts * kEach;  // blocks of a wave, the last part's empty ones too
+  fetch_x(0);
+  // W's scales, 64 blocks' in the lanes: a scalar load of each is a wait of its own
+  auto fetch_ws = [&](int first) { return ws[min(first + lane, blocks - 1)]; };
+  float wl = fetch_ws(0);
+  Codes w[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) w[u] = fetch_w(kg + u * KG);
+  keep_x(0);
+  __syncthreads();
+  for (int j0 = 0; j0 < all; j0 += U) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int j = j0 + u, part = j / kEach;
+      if (j >= all) break;
+      if (j % kEach == 0) {
+        if (part + 1 < parts) fetch_x(part + 1);
+        if (part && part * kPart % 64 == 0) wl = fetch_ws(part * kPart);
       }
-#pragma unroll
-      for (int a = 0; a < BOF; ++a) {
-        const Operand<Y> wo(w[u][a]);
-        w[u][a] = fetch(wrow[a], at + U * kFewWaves);
+      const int kb = kg + j * KG;
+      if (kb < blocks) {  // the branch keeps blocks apart: their reads of LDS side by side take registers that spill
+        const float wsc = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(wl), kb & 63));
+        const Operand<Y> wo(w[u]);
+        const uint4 *const xp = xl[part & 1] + kb % kPart * kRows * 8;
+        const float *const sp = sl[part & 1] + kb % kPart * kRows;
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
-          const f32x4 r = Operand<Y>::product(wo, Operand<Y>(x[b]));
+          const int row = 16 * b + (lane & 15), c = lane >> 4, x = (row >> 1) & 7;
+          Codes v;
+          v.h[0] = xp[row * 8 + (c ^ x)];
+          v.h[1] = xp[row * 8 + ((4 + c) ^ x)];
+          const float s = sp[row] * wsc;
+          const f32x4 r = Operand<Y>::product(wo, Operand<Y>(v));
 #pragma unroll
-          for (int i = 0; i < 4; ++i) acc[a][b][i] = fmaf(r[i], s[b], acc[a][b][i]);
+          for (int i = 0; i < 4; ++i) acc[b][i] = fmaf(r[i], s, acc[b][i]);
         }
+      }
+      w[u] = fetch_w(kg + (j + U) * KG);
+      if (j % kEach == kEach - 1 && part + 1 < parts) {
+        keep_x(part + 1);
+        __syncthreads();
       }
     }
   }
+  const int o = o0 + (lane >> 4) * 4;
+  if constexpr (KG > 1) {
+    f32x4 *const sums = (f32x4 *)xl;  // [KG][RG][NB][64]
+    __syncthreads();  // every wave is done with x
 #pragma unroll
-  for (int a = 0; a < BOF; ++a)
+    for (int b = 0; b < NB; ++b) sums[(wave * NB + b) * 64 + lane] = acc[b];
+    __syncthreads();
+    if (kg) return;
 #pragma unroll
-    for (int b = 0; b < NB; ++b) part[wave][a][b][lane] = acc[a][b];
-  __syncthreads();
-  for (int i = tid; i < BOF * NB * 64; i += kFewWaves * 64) {
-    const int l = i & 63, ab = i >> 6, a = ab / NB, b = ab % NB;
-    f32x4 v = part[0][a][b][l];
+    for (int b = 0; b < NB; ++b)
 #pragma unroll
-    for (int s = 1; s < kFewWaves; ++s) v += part[s][a][b][l];
-    const int row = 16 * b + (l & 15), o = o0 + 16 * a + (l >> 4) * 4;
-    if (row < p.n && o < p.n_out) store4((Y *)p.y + row * p.y_stride + o, v);
+      for (int g = 1; g < KG; ++g) acc[b] += sums[((g * RG + rg) * NB + b) * 64 + lane];
+  }
+#pragma unroll
+  for (int b = 0; b < NB; ++b) {
+    const int row = 16 * b + (lane & 15);
+    if (row < p.n && o < p.n_out) store4((Y *)p.y + row * p.y_stride + o, acc[b]);
   }
 }
 
@@ -365,14 +458,37 @@ __global__ __launch_bounds__(WGO *WGR * 64) void matmul_tile_kernel(Fp8Args p, i
   }
 }
 
+template <typename Y, int NB>
+static void launch_rows(const Fp8Args &a, hipStream_t st) {
+#define LORA_ROWS(RG) \
+  hipLaunchKernelGGL((matmul_rows_kernel<Y, NB, RG>), dim3((a.n_out + 16 * RG - 1) / (16 * RG)), dim3(512), 0, st, a)
+  // A CU takes in W at about 25 bytes a ns and x, from L2, at about 45, and has
+  // room for one workgroup: the rounds of workgroups times what one brings.
+  // 64 rows by k of 4096, us with RG of 8, 4, 2, 1: n_out 32000 31.7 39.6 55.7
+  // 94; 22016 26.1 34.2 40.3 68; 11008 24.8 17.5 26.9 36; 6144 24.3 17.0 14.1 24.
+  const int groups = (a.n_out + 15) / 16;
+  int best = 0;
+  float least = 0.f;
+  for (int rg = 8; rg >= (NB < 8 ? 1 : 2); rg /= 2) {
+    const int rounds = ((groups + rg - 1) / rg + 255) / 256;
+    const float cost = rounds * (rg / 25.f + NB / 45.f);
+    if (!best || cost < least) {
+      best = rg;
+      least = cost;
+    }
+  }
+  if (best == 8) LORA_ROWS(8);
+  else if (best == 4) LORA_ROWS(4);
+  else if (NB == 8 || best == 2) LORA_ROWS(2);
+  else if constexpr (NB < 8) LORA_ROWS(1);
+#undef LORA_ROWS
+}
 template <typename Y>
 static void launch_few(const Fp8Args &a, hipStream_t st) {
-#define LORA_FEW(BOF, NB) \
-  hipLaunchKernelGGL((matmul_few_kernel<Y, BOF, NB>), dim3((a.n_out + 16 * BOF - 1) / (16 * BOF)), dim3(kFewWaves * 64), 0, st, a)
-  if (a.n <= 16) LORA_FEW(1, 1);
-  else if (a.n <= 32) LORA_FEW(1, 2);
-  else LORA_FEW(2, 4);
-#undef LORA_FEW
+  if (a.n <= 16) hipLaunchKernelGGL((matmul_few_kernel<Y>), dim3((a.n_out + 15) / 16), dim3(kFewWaves * 64), 0, st, a);
+  else if (a.n <= 32) launch_rows<Y, 2>(a, st);
+  else if (a.n <= 64) launch_rows<Y, 4>(a, st);
+  else launch_rows<Y, 8>(a, st);
 }
 template <typename Y>
 static void launch_tiles(const Fp8Args &a, hipStream_t st) {
@@ -389,7 +505,7 @@ static void launch_tiles(const Fp8Args &a, hipStream_t st) {
 }
 
 hipError_t launch_matmul_fp8(const Fp8Args &a, int dtype, hipStream_t st) {
-  if (a.n <= 64) {
+  if (a.n <= 128) {
     if (dtype == 0) launch_few<float>(a, st);
     else launch_few<u16>(a, st);
   } else {
