@@ -15,6 +15,7 @@ using namespace lora;
 namespace {
 
 constexpr uint32_t kMaxOut = 1u << 26;
+constexpr uint32_t kMaxStride = 1u << 22;  // of a product's rows: a tile's offsets stay within 32 bits
 
 uint32_t blocks_of(uint32_t k) { return (k + kFp8Block - 1) / kFp8Block; }
 
@@ -85,6 +86,9 @@ int lora_matmul_fp8(int32_t dtype, uint32_t n_out, uint32_t k_in, const void *W,
   if (int e = check_codes(what, "W", W, w_row_stride, k_in, w_scale, w_scale_stride, n)) return e;
   if (int e = check_codes(what, "x", x, x_row_stride, k_in, x_scale, x_scale_stride, n)) return e;
   if (int e = check_rows(what, dtype, "y", y, y_row_stride, n_out, n)) return e;
+  if (w_row_stride > kMaxStride || x_row_stride > kMaxStride || x_scale_stride > kMaxStride)
+    return fail(LORA_ERR_STRIDE, "%s: row strides of W %u, x %u and x's scales %u must be at most %u", what, w_row_stride, x_row_stride,
+                x_scale_stride, kMaxStride);
   if (n == 0) return LORA_OK;
   const size_t need = lora_matmul_fp8_workspace_bytes(dtype, n_out, k_in, n);
   if (need && (!workspace || workspace_bytes < need))

@@ -355,11 +355,26 @@ __global__ __launch_bounds__(512) void matmul_rows_kernel(Fp8Args p) {
 }
 
 // ---------------------------------------------------------------- many rows
+// The rows from `first` on of an n-row matrix of `stride` bytes a row and `width` of them in use.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t tile_rsrc(const void *base, int first, int n, long long stride, int width) {
+  const long long bytes = (n - first - 1) * stride + width;
+  return __builtin_amdgcn_make_buffer_rsrc((void *)((uintptr_t)base + first * stride), 0, (int)min(bytes, 0xffffffffll), 0x00020000);
+}
+// dma16 and dma4 (common.hpp) through a buffer resource.
+__device__ __forceinline__ void dma16_buffer(__amdgpu_buffer_rsrc_t r, uint32_t voff, uint32_t soff, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %3\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, %2 offen lds" : : "v"(voff), "s"(r), "s"(soff), "s"(lds) : "memory");
+}
+__device__ __forceinline__ void dma4_buffer(__amdgpu_buffer_rsrc_t r, uint32_t voff, uint32_t soff, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %3\n\ts_nop 0\n\tbuffer_load_dword %0, %1, %2 offen lds" : : "v"(voff), "s"(r), "s"(soff), "s"(lds) : "memory");
+}
+
 // A workgroup owns BO output features x BR rows.  A stage is one block of 128
 // columns of every row of the tile, brought to LDS by LDS-DMA: 128 bytes a
 // row, its eight 16-byte chunks at slot c ^ ((r >> 1) & 7), so that the
-// operands' reads hit distinct banks, and the scales of the tile's rows
-// behind them.  NS stages form a ring with NS - 1 in flight; the waits are
+// operands' reads hit distinct banks.  The rows' scales come by eight blocks
+// at a time, a part of the next eight with every stage: a scale a row and
+// stage is as many cache lines as the codes are (4096 x 22016 x 4096: 529 us
+// that way).  NS stages form a ring with NS - 1 in flight; the waits are
 // explicit, and a stage is read only after every wave's share of it landed.
 // Rows past the ends load a valid row and are not stored; chunks past k are
 // zeroed once they have landed.
@@ -372,8 +387,9 @@ __global__ __launch_bounds__(WGO *WGR * 64) void matmul_tile_kernel(Fp8Args p, i
   static_assert(BR % 64 == 0 && BR / 64 <= NW, "a wave's lanes bring 64 rows' scales");
   static_assert(NS >= 2 && (NS - 2) * (LPW + 1) < 64, "ring depth / vmcnt range");
   static_assert(WO <= kFp8Block && kFp8Block % WO == 0, "a wave's outputs share their scales");
+  constexpr bool kSpread = NBO >= 8;  // small tiles have little to spread them over (512 x 4096 x 4096: 22 us, 27 spread)
   __shared__ __attribute__((aligned(16))) uint4 ring[NS][RS * 8];
-  __shared__ float xs[NS][BR];
+  __shared__ float xs[3][BR * 8];  // [row][block] of the eight blocks in use, the next and, for waves behind, the last
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wo = wave % WGO, wr = wave / WGO;
   // An XCD's workgroups take neighbouring tiles, which its L2 then serves:
@@ -384,22 +400,34 @@ __global__ __launch_bounds__(WGO *WGR * 64) void matmul_tile_kernel(Fp8Args p, i
   const int r0 = (g0 + tg % gsz) * BR, o0 = tg / gsz * BO;
   const int nst = (p.k + kFp8Block - 1) / kFp8Block;
 
-  const uint8_t *src[LPW];
+  // Operands through buffer resources that begin at the tile and end with the
+  // last row's k columns: what lies past their ends is not read, and the
+  // address of a transfer is a lane's offset and a scalar one.
+  const __amdgpu_buffer_rsrc_t wsrc = tile_rsrc(p.W, o0, p.n_out, p.w_stride, p.k), xsrc = tile_rsrc(p.x, r0, p.n, p.x_stride, p.k);
+  const __amdgpu_buffer_rsrc_t ssrc = tile_rsrc(p.x_scale, r0, p.n, 4 * p.xs_stride, 4 * nst);
   const int chunk = ((lane & 7) ^ (((wave * 8 + (lane >> 3)) >> 1) & 7)) * 16;  // this lane's place in the stage's rows
-#pragma unroll
-  for (int j = 0; j < LPW; ++j) {
-    const int rr = (wave + NW * j) * 8 + (lane >> 3);
-    src[j] = j < JW ? p.W + min(o0 + rr, p.n_out - 1) * p.w_stride : p.x + min(r0 + rr - BO, p.n - 1) * p.x_stride;
-  }
-  const int srow = wave % (BR / 64) * 64;
-  const float *ssrc = p.x_scale + min(r0 + srow + lane, p.n - 1) * p.xs_stride;
-  auto issue = [&](int st) {
-    const int k0 = st * kFp8Block, kk = k0 + chunk < p.k ? k0 + chunk : 0;
-#pragma unroll
-    for (int j = 0; j < LPW; ++j) dma16(src[j] + kk, lds_addr(&ring[st % NS][(wave + NW * j) * 64]));
-    dma4(ssrc + st, lds_addr(&xs[st % NS][srow]));
+  const uint32_t woff = (wave * 8 + (lane >> 3)) * (uint32_t)p.w_stride + chunk, xoff = (wave * 8 + (lane >> 3)) * (uint32_t)p.x_stride + chunk;
+  // part i of 8 of the scales of blocks 8 g .. 8 g + 7: BR / 8 rows, a wave 8 of them
+  const uint32_t soff = (wave % (BR / 64) * 8 + (lane >> 3)) * 4 * (uint32_t)p.xs_stride + 4 * (lane & 7);
+  auto bring_scales = [&](int g, int i) {
+    dma4_buffer(ssrc, soff, 4 * (i * (BR / 8) * (uint32_t)p.xs_stride + 8 * g), lds_addr(&xs[g % 3][(i * (BR / 8) + wave % (BR / 64) * 8) * 8]));
   };
-  for (int st = 0; st < NS - 1 && st < nst; ++st) issue(st);
+  // Stages past the last bring the last again, into places that nothing reads
+  // any more, so that the waits count the same in every stage.
+  auto issue = [&](int st, int from, int to) {
+    const uint32_t k0 = min(st, nst - 1) * kFp8Block;
+#pragma unroll
+    for (int j = from; j < to; ++j) {
+      const uint32_t lds = lds_addr(&ring[st % NS][(wave + NW * j) * 64]);
+      if (j < JW) dma16_buffer(wsrc, woff, k0 + 8 * NW * j * (uint32_t)p.w_stride, lds);
+      else dma16_buffer(xsrc, xoff, k0 + 8 * NW * (j - JW) * (uint32_t)p.x_stride, lds);
+    }
+  };
+  for (int i = 0; i < 8; ++i) bring_scales(0, i);
+  for (int st = 0; st < NS - 1; ++st) {
+    issue(st, 0, LPW);
+    bring_scales(st / 8 + 1, st % 8);
+  }
 
   f32x4 acc[NBO][NBR];
 #pragma unroll
@@ -415,9 +443,11 @@ __global__ __launch_bounds__(WGO *WGR * 64) void matmul_tile_kernel(Fp8Args p, i
     v.h[1] = sl[r * 8 + ((4 + c) ^ x)];
     return v;
   };
+  float wl = 0.f;  // the scales of 64 blocks in the lanes
   for (int st = 0; st < nst; ++st) {
-    const float wsc = ws[st];
-    wait_stages<LPW + 1, (NS > 2 ? NS - 2 : 0)>(min(NS - 2, nst - 1 - st));
+    if (st % 64 == 0) wl = ws[min(st + lane, nst - 1)];
+    const float wsc = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(wl), st & 63));
+    wait_vmcnt<(NS - 2) * (LPW + 1)>();
     if ((st + 1) * kFp8Block > p.k) {
       if (st * kFp8Block + chunk >= p.k)
 #pragma unroll
@@ -426,25 +456,32 @@ __global__ __launch_bounds__(WGO *WGR * 64) void matmul_tile_kernel(Fp8Args p, i
     // zeros are there, and the last stage's reads have returned before its place is written again
     __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0)
     block_barrier();
-    // every wave is done with stage st - 1: its place takes stage st + NS - 1
-    if (st + NS - 1 < nst) issue(st + NS - 1);
+    // Every wave is done with stage st - 1: its place takes stage st + NS - 1,
+    // whose transfers go out among the products, as all of them together hold
+    // the waves up.
     float s[NBR];
 #pragma unroll
-    for (int c = 0; c < NBR; ++c) s[c] = xs[st % NS][wr * WR + c * 16 + (lane & 15)] * wsc;
-    Codes xf[NBR];
+    for (int c = 0; c < NBR; ++c) s[c] = xs[st / 8 % 3][(wr * WR + c * 16 + (lane & 15)) * 8 + st % 8] * wsc;
+    Codes xf[NBR], wf = read(st, wo * WO + (lane & 15)), next;
 #pragma unroll
     for (int c = 0; c < NBR; ++c) xf[c] = read(st, BO + wr * WR + c * 16 + (lane & 15));
 #pragma unroll
     for (int a = 0; a < NBO; ++a) {
-      const Operand<Y> w(read(st, wo * WO + a * 16 + (lane & 15)));
+      if (a + 1 < NBO) next = read(st, wo * WO + (a + 1) * 16 + (lane & 15));
+      issue(st + NS - 1, kSpread ? a * LPW / NBO : 0, kSpread ? (a + 1) * LPW / NBO : a ? 0 : LPW);
+      if (a + 1 == NBO) bring_scales((st + NS - 1) / 8 + 1, (st + NS - 1) % 8);
+      const Operand<Y> w(wf);
 #pragma unroll
       for (int c = 0; c < NBR; ++c) {
         const f32x4 r = Operand<Y>::product(w, Operand<Y>(xf[c]));
 #pragma unroll
         for (int i = 0; i < 4; ++i) acc[a][c][i] = fmaf(r[i], s[c], acc[a][c][i]);
       }
+      wf = next;
+      __builtin_amdgcn_sched_barrier(0);
     }
   }
+  wait_vmcnt<0>();  // nothing is on its way into LDS when the workgroup ends
 #pragma unroll
   for (int c = 0; c < NBR; ++c) {
     const int row = r0 + wr * WR + c * 16 + (lane & 15);

@@ -628,7 +628,7 @@ int lora_quantize_fp8(int32_t dtype, uint32_t n_rows, uint32_t k, const void *x,
  * term joins through lora_shrink and lora_expand_fold.  k_in is a multiple of
  * 16, at most 65536, n_out of 8, strides of codes of 16, y_row_stride of 8
  * (bf16) or 4 (f32), and codes and y are 16-byte aligned; n is limited to
- * 16384.  The scaled sums of the blocks add up in f32 and y is rounded once.
+ * 16384, strides of codes and x_scale to 2^22.  The scaled sums of the blocks add up in f32 and y is rounded once.
  * Within a block f32 calls keep f32 sums of the exact products, bf16 calls
  * sums that are off by up to 2^-10 of the sum of the products' magnitudes,
  * 2^-16 typically (what the 8-bit matrix instruction keeps).  The order of every sum follows

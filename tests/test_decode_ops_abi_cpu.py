@@ -66,7 +66,8 @@ def test_matmul_refusals(L):
                            (dict(W=FAKE + 8), -5, "W"), (dict(x=FAKE + 1), -5, "x"), (dict(wsc=FAKE + 2), -5, "aligned"),
                            (dict(yst=56), -3, "y row stride 56"), (dict(yst=68), -5, "multiple of 8"),
                            (dict(yst=66, dtype=B.LORA_F32), -5, "multiple of 4"), (dict(y=None), -2, "y must"),
-                           (dict(y=FAKE + 4), -5, "aligned")]:
+                           (dict(y=FAKE + 4), -5, "aligned"), (dict(wst=2 ** 22 + 16), -3, "W 4194320"),
+                           (dict(xst=2 ** 22 + 16), -3, "x 4194320"), (dict(xss=2 ** 22 + 1), -3, "scales 4194305")]:
         rc, msg = matmul(L, **kw)
         assert rc == code and text in msg and msg.startswith("lora_matmul_fp8"), (kw, rc, msg)
     assert matmul(L, n=0, W=None, wsc=None, x=None, xsc=None, y=None, ws=None, ws_bytes=0)[0] == 0
