@@ -401,8 +401,9 @@ __global__ __launch_bounds__(WGO *WGR * 64) void matmul_tile_kernel(Fp8Args p, i
   const int nst = (p.k + kFp8Block - 1) / kFp8Block;
 
   // Operands through buffer resources that begin at the tile and end with the
-  // last row's k columns: what lies past their ends is not read, and the
-  // address of a transfer is a lane's offset and a scalar one.
+  // last row's k columns: what lies past their ends is not read.  A lane's
+  // offset carries the row, which may lie past the end, and the scalar one the
+  // stage's first column, which does not.
   const __amdgpu_buffer_rsrc_t wsrc = tile_rsrc(p.W, o0, p.n_out, p.w_stride, p.k), xsrc = tile_rsrc(p.x, r0, p.n, p.x_stride, p.k);
   const __amdgpu_buffer_rsrc_t ssrc = tile_rsrc(p.x_scale, r0, p.n, 4 * p.xs_stride, 4 * nst);
   const int chunk = ((lane & 7) ^ (((wave * 8 + (lane >> 3)) >> 1) & 7)) * 16;  // this lane's place in the stage's rows
@@ -410,7 +411,7 @@ __global__ __launch_bounds__(WGO *WGR * 64) void matmul_tile_kernel(Fp8Args p, i
   // part i of 8 of the scales of blocks 8 g .. 8 g + 7: BR / 8 rows, a wave 8 of them
   const uint32_t soff = (wave % (BR / 64) * 8 + (lane >> 3)) * 4 * (uint32_t)p.xs_stride + 4 * (lane & 7);
   auto bring_scales = [&](int g, int i) {
-    dma4_buffer(ssrc, soff, 4 * (i * (BR / 8) * (uint32_t)p.xs_stride + 8 * g), lds_addr(&xs[g % 3][(i * (BR / 8) + wave % (BR / 64) * 8) * 8]));
+    dma4_buffer(ssrc, soff + 4 * (i * (BR / 8) * (uint32_t)p.xs_stride + 8 * g), 0, lds_addr(&xs[g % 3][(i * (BR / 8) + wave % (BR / 64) * 8) * 8]));
   };
   // Stages past the last bring the last again, into places that nothing reads
   // any more, so that the waits count the same in every stage.
@@ -419,8 +420,8 @@ __global__ __launch_bounds__(WGO *WGR * 64) void matmul_tile_kernel(Fp8Args p, i
 #pragma unroll
     for (int j = from; j < to; ++j) {
       const uint32_t lds = lds_addr(&ring[st % NS][(wave + NW * j) * 64]);
-      if (j < JW) dma16_buffer(wsrc, woff, k0 + 8 * NW * j * (uint32_t)p.w_stride, lds);
-      else dma16_buffer(xsrc, xoff, k0 + 8 * NW * (j - JW) * (uint32_t)p.x_stride, lds);
+      if (j < JW) dma16_buffer(wsrc, woff + 8 * NW * j * (uint32_t)p.w_stride, k0, lds);
+      else dma16_buffer(xsrc, xoff + 8 * NW * (j - JW) * (uint32_t)p.x_stride, k0, lds);
     }
   };
   for (int i = 0; i < 8; ++i) bring_scales(0, i);
@@ -459,6 +460,10 @@ __global__ __launch_bounds__(WGO *WGR * 64) void matmul_tile_kernel(Fp8Args p, i
     // Every wave is done with stage st - 1: its place takes stage st + NS - 1,
     // whose transfers go out among the products, as all of them together hold
     // the waves up.
+    if constexpr (!kSpread) {
+      issue(st + NS - 1, 0, LPW);
+      bring_scales((st + NS - 1) / 8 + 1, (st + NS - 1) % 8);
+    }
     float s[NBR];
 #pragma unroll
     for (int c = 0; c < NBR; ++c) s[c] = xs[st / 8 % 3][(wr * WR + c * 16 + (lane & 15)) * 8 + st % 8] * wsc;
@@ -468,8 +473,10 @@ __global__ __launch_bounds__(WGO *WGR * 64) void matmul_tile_kernel(Fp8Args p, i
 #pragma unroll
     for (int a = 0; a < NBO; ++a) {
       if (a + 1 < NBO) next = read(st, wo * WO + (a + 1) * 16 + (lane & 15));
-      issue(st + NS - 1, kSpread ? a * LPW / NBO : 0, kSpread ? (a + 1) * LPW / NBO : a ? 0 : LPW);
-      if (a + 1 == NBO) bring_scales((st + NS - 1) / 8 + 1, (st + NS - 1) % 8);
+      if constexpr (kSpread) {
+        if (a < 4) issue(st + NS - 1, a * LPW / 4, (a + 1) * LPW / 4);
+        if (a == 3) bring_scales((st + NS - 1) / 8 + 1, (st + NS - 1) % 8);
+      }
       const Operand<Y> w(wf);
 #pragma unroll
       for (int c = 0; c < NBR; ++c) {
