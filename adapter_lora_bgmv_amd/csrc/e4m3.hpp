@@ -36,6 +36,12 @@ struct Raw4<u16> {
   }
 };
 
+// Two f32 as bf16, rounded to nearest even, by one instruction (f2bf takes five for each).
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  const f32x2 v = {lo, hi};
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, bf16x2));
+}
+
 // |x|'s bits where x is finite, 0 elsewhere: unsigned order is magnitude order.
 __device__ __forceinline__ uint32_t finite_bits(float x) {
   const uint32_t b = __float_as_uint(x) & 0x7fffffffu;
@@ -54,10 +60,10 @@ __device__ __forceinline__ int exp_for(uint32_t amax_bits) {
 // and nothing exceeds 448.
 __device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d, float inv) {
   const float qnan = __uint_as_float(0x7fc00000u);
-  a = finite_bits(a) || a == 0.f ? a * inv : qnan;
-  b = finite_bits(b) || b == 0.f ? b * inv : qnan;
-  c = finite_bits(c) || c == 0.f ? c * inv : qnan;
-  d = finite_bits(d) || d == 0.f ? d * inv : qnan;
+  a = __builtin_isfinite(a) ? a * inv : qnan;
+  b = __builtin_isfinite(b) ? b * inv : qnan;
+  c = __builtin_isfinite(c) ? c * inv : qnan;
+  d = __builtin_isfinite(d) ? d * inv : qnan;
   int w = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
   return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(c, d, w, true);
 }

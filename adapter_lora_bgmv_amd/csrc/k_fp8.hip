@@ -173,7 +173,7 @@ struct Operand<float> {
 };
 // Four neighbouring outputs of a row.
 __device__ __forceinline__ void store4(u16 *p, f32x4 v) {
-  *(uint2 *)p = make_uint2(pack2(f2bf(v[0]), f2bf(v[1])), pack2(f2bf(v[2]), f2bf(v[3])));
+  *(uint2 *)p = make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
 }
 __device__ __forceinline__ void store4(float *p, f32x4 v) { *(float4 *)p = make_float4(v[0], v[1], v[2], v[3]); }
 

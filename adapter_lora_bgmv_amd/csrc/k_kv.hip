@@ -156,7 +156,16 @@ __device__ __forceinline__ void write_page(const KvDev &a, int u, int h, bool is
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) big = max(big, finite_bits(x[j][i].at(e)));
+      for (int e = 0; e < 4; ++e) big = max(big, __float_as_uint(x[j][i].at(e)) & 0x7fffffffu);
+  if (__any(big >= 0x7f800000u)) {  // infinities and NaN do not count
+    big = 0;
+#pragma unroll
+    for (int j = 0; j < IT; ++j)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) big = max(big, finite_bits(x[j][i].at(e)));
+  }
   big = (uint32_t)wave_reduce((int)big, 0, [](int a, int b) { return max(a, b); });  // bits of finite numbers: no sign
   if (lane == 0) wave_max[tid >> 6] = big;
   __syncthreads();
@@ -249,17 +258,21 @@ struct Raw8 {
   }
 };
 
-// cos and sin by Taylor's series on [-pi/4, pi/4], to 1e-16: quarter turns are
-// taken off first, pi/2 in two parts so that up to 2^30 of them lose nothing.
+// An angle's quarter turns k (their two low bits) and what is left, within
+// pi/4: pi/2 in two parts loses nothing below 2^50, from where an angle in 64
+// bits is no longer known to a quarter of a radian; such angles count as 0,
+// and infinities and NaN as NaN.
+__device__ __forceinline__ double off_quarters(double a, int *k) {
+  a = fabs(a) < 1125899906842624.0 ? a : a * 0.0;
+  const double z = fma(a, 0.63661977236758134308, 6755399441055744.0);  // + 1.5 2^52: a whole number in the low bits
+  const double n = z - 6755399441055744.0;
+  *k = (int)(uint32_t)__double_as_longlong(z);
+  return fma(-n, 6.12323399573676603587e-17, fma(-n, 1.57079632679489655800, a));
+}
+// cos and sin by Taylor's series, to 1e-16.
 __device__ __forceinline__ void cos_sin(double a, double *c, double *s) {
-  if (!(fabs(a) < 1073741824.0)) {
-    sincos(a, s, c);
-    return;
-  }
-  const double n = rint(a * 0.63661977236758134308);
-  double r = fma(-n, 1.57079632679489655800, a);
-  r = fma(-n, 6.12323399573676603587e-17, r);
-  const double q = r * r;
+  int k;
+  const double r = off_quarters(a, &k), q = r * r;
   double sp = -1.0 / 1307674368000.0, cp = 1.0 / 20922789888000.0;
   sp = fma(sp, q, 1.0 / 6227020800.0);
   cp = fma(cp, q, -1.0 / 87178291200.0);
@@ -276,8 +289,25 @@ __device__ __forceinline__ void cos_sin(double a, double *c, double *s) {
   cp = fma(cp, q, -0.5);
   sp = fma(sp * q, r, r);
   cp = fma(cp, q, 1.0);
-  const int k = (int)n;
   const double x = k & 1 ? sp : cp, y = k & 1 ? cp : sp;
+  *c = (k + 1) & 2 ? -x : x;
+  *s = k & 2 ? -y : y;
+}
+// The same to f32's last bits: the series run in 32.
+__device__ __forceinline__ void cos_sin(double a, float *c, float *s) {
+  int k;
+  const float r = (float)off_quarters(a, &k), q = r * r;
+  float sp = 1.f / 362880.f, cp = -1.f / 3628800.f;
+  cp = fmaf(cp, q, 1.f / 40320.f);
+  sp = fmaf(sp, q, -1.f / 5040.f);
+  cp = fmaf(cp, q, -1.f / 720.f);
+  sp = fmaf(sp, q, 1.f / 120.f);
+  cp = fmaf(cp, q, 1.f / 24.f);
+  sp = fmaf(sp, q, -1.f / 6.f);
+  cp = fmaf(cp, q, -0.5f);
+  sp = fmaf(sp * q, r, r);
+  cp = fmaf(cp, q, 1.f);
+  const float x = k & 1 ? sp : cp, y = k & 1 ? cp : sp;
   *c = (k + 1) & 2 ? -x : x;
   *s = k & 2 ? -y : y;
 }
@@ -291,8 +321,11 @@ __device__ __forceinline__ bool item_dims(const RotaryDev &rot, int c, int *d0, 
   return turns;
 }
 
-template <typename T, int D, int IT>
-__device__ __forceinline__ void write_turned_page(const KvDev &a, const RotaryDev &rot, int u, int h, const T *krows, int k_stride,
+// K of `heads` heads of a page from h on, whose cosines are formed once: they
+// are most of the arithmetic (4096 rows of 8 heads, 32 query heads: 31.2 us
+// with those of each head anew, 23.3 with two heads to a workgroup of K and eight to one of queries).
+template <typename T, int D, int IT, int HB>
+__device__ __forceinline__ void write_turned_page(const KvDev &a, const RotaryDev &rot, int u, int h0, const T *krows, int k_stride,
                                                   uint32_t *wave_max) {
   const int tid = threadIdx.x, lane = tid & 63;
   SeqDev s;
@@ -303,80 +336,95 @@ __device__ __forceinline__ void write_turned_page(const KvDev &a, const RotaryDe
   const int P = 1 << a.page_shift, t_page = lp << a.page_shift;
   const int t0 = max(s.start - t_page, 0), t1 = min(s.len - t_page, P);
   const long long row0 = (long long)s.row0 + (t_page - s.start);  // row of the page's token 0, were it new
-  uint8_t *codes = a.k + ((size_t)page * a.H + h) * ((size_t)P * D);
-  uint8_t *ep = a.ke + (size_t)page * a.H + h;
-  const int before = t0 > 0 ? *ep : 0;
-  const T *src = krows + (size_t)h * D;
   const int items = P * D / 16;
   // 256 is a multiple of a token's D / 16 items: a thread has the same dims of every token
   static_assert(kKvThreads % (D / 16) == 0, "a thread's items share their dims");
   const int c = tid % (D / 16);
   int d0, d1;
   const bool turns = item_dims(rot, c, &d0, &d1);
+  auto token = [&](int j) { return (tid + j * kKvThreads) / (D / 16); };
+  auto live = [&](int j) { return tid + j * kKvThreads < items && token(j) >= t0 && token(j) < t1; };
 
   Raw8<T> raw[IT][2];
+  auto fetch = [&](int h) {
 #pragma unroll
-  for (int j = 0; j < IT; ++j) {
-    const int it = tid + j * kKvThreads, t = it / (D / 16);
-    if (it < items && t >= t0 && t < t1) {
-      const T *p = src + (size_t)(row0 + t) * k_stride;
-      raw[j][0].load(p + d0);
-      raw[j][1].load(p + d1);
-    }
+    for (int j = 0; j < IT; ++j)
+      if (live(j)) {
+        const T *p = krows + (size_t)h * D + (size_t)(row0 + token(j)) * k_stride;
+        raw[j][0].load(p + d0);
+        raw[j][1].load(p + d1);
+      }
+  };
+  fetch(h0);
+  double cs[IT][8], sn[IT][8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const double f = turns ? (double)rot.inv_freq[8 * c + i] : 0.0;
+#pragma unroll
+    for (int j = 0; j < IT; ++j) cos_sin((double)(t_page + token(j)) * f, &cs[j][i], &sn[j][i]);
   }
-  double f[8];
+#pragma unroll 1
+  for (int h = h0; h < min(h0 + HB, a.H); ++h) {
+    uint8_t *codes = a.k + ((size_t)page * a.H + h) * ((size_t)P * D);
+    uint8_t *ep = a.ke + (size_t)page * a.H + h;
+    const int before = t0 > 0 ? *ep : 0;
+    float x[IT][16];
+    uint32_t big = 0;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) f[i] = turns ? (double)rot.inv_freq[8 * c + i] : 0.0;
-  float x[IT][16];
-  uint32_t big = 0;
+    for (int j = 0; j < IT; ++j) {
+      const bool on = live(j);
 #pragma unroll
-  for (int j = 0; j < IT; ++j) {
-    const int it = tid + j * kKvThreads, t = it / (D / 16);
-    const bool live = it < items && t >= t0 && t < t1;
+      for (int e = 0; e < 16; ++e) x[j][e] = on ? raw[j][e / 8].at(e % 8) : 0.f;
+      if (on && turns) {
 #pragma unroll
-    for (int e = 0; e < 16; ++e) x[j][e] = live ? raw[j][e / 8].at(e % 8) : 0.f;
-    if (live && turns) {
-      const double p = (double)(t_page + t);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        double cs, sn;
-        cos_sin(p * f[i], &cs, &sn);
-        if (rot.interleaved) {
-          const double v = x[j][2 * i], w = x[j][2 * i + 1];
-          x[j][2 * i] = (float)(v * cs - w * sn);
-          x[j][2 * i + 1] = (float)(w * cs + v * sn);
-        } else {
-          const double v = x[j][i], w = x[j][i + 8];
-          x[j][i] = (float)(v * cs - w * sn);
-          x[j][i + 8] = (float)(w * cs + v * sn);
+        for (int i = 0; i < 8; ++i) {
+          const double cc = cs[j][i], ss = sn[j][i];
+          if (rot.interleaved) {
+            const double v = x[j][2 * i], w = x[j][2 * i + 1];
+            x[j][2 * i] = (float)(v * cc - w * ss);
+            x[j][2 * i + 1] = (float)(w * cc + v * ss);
+          } else {
+            const double v = x[j][i], w = x[j][i + 8];
+            x[j][i] = (float)(v * cc - w * ss);
+            x[j][i + 8] = (float)(w * cc + v * ss);
+          }
         }
       }
+#pragma unroll
+      for (int e = 0; e < 16; ++e) big = max(big, __float_as_uint(x[j][e]) & 0x7fffffffu);
     }
+    if (__any(big >= 0x7f800000u)) {  // infinities and NaN do not count
+      big = 0;
 #pragma unroll
-    for (int e = 0; e < 16; ++e) big = max(big, finite_bits(x[j][e]));
-  }
-  big = (uint32_t)wave_reduce((int)big, 0, [](int a, int b) { return max(a, b); });  // bits of finite numbers: no sign
-  if (lane == 0) wave_max[tid >> 6] = big;
-  __syncthreads();
+      for (int j = 0; j < IT; ++j)
 #pragma unroll
-  for (int w = 0; w < kKvThreads / 64; ++w) big = max(big, wave_max[w]);
-  const int e = min(max(before, exp_for(big)), kExpMax);
-  const int by = before - e;  // old tokens move by 2^by
-  const bool move = t0 > 0 && by != 0;
-  const float inv = __uint_as_float((uint32_t)(254 - e) << 23);
-  if (tid == 0) *ep = (uint8_t)e;
+        for (int e = 0; e < 16; ++e) big = max(big, finite_bits(x[j][e]));
+    }
+    if (HB > 1 && h + 1 < min(h0 + HB, a.H)) fetch(h + 1);
+    big = (uint32_t)wave_reduce((int)big, 0, [](int a, int b) { return max(a, b); });  // bits of finite numbers: no sign
+    if (HB > 1 && h > h0) __syncthreads();  // the head before has been read
+    if (lane == 0) wave_max[tid >> 6] = big;
+    __syncthreads();
 #pragma unroll
-  for (int j = 0; j < IT; ++j) {
-    const int it = tid + j * kKvThreads, t = it / (D / 16);
-    if (it >= items) continue;
-    uint8_t *row = codes + (t >> 4) * (16 * D) + ((t >> 2) & 3) * (4 * D) + (t & 3) * 16;
+    for (int w = 0; w < kKvThreads / 64; ++w) big = max(big, wave_max[w]);
+    const int e = min(max(before, exp_for(big)), kExpMax);
+    const int by = before - e;  // old tokens move by 2^by
+    const bool move = t0 > 0 && by != 0;
+    const float inv = __uint_as_float((uint32_t)(254 - e) << 23);
+    if (tid == 0) *ep = (uint8_t)e;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int d = i ? d1 : d0;
-      uint2 *p = (uint2 *)(row + d / 16 * 64 + d % 16);
-      const float *y = x[j] + 8 * i;
-      if (t >= t0 && t < t1) *p = make_uint2(codes4(y[0], y[1], y[2], y[3], inv), codes4(y[4], y[5], y[6], y[7], inv));
-      else if (move && t < t0) *p = make_uint2(moved4(p->x, by), moved4(p->y, by));
+    for (int j = 0; j < IT; ++j) {
+      const int it = tid + j * kKvThreads, t = token(j);
+      if (it >= items) continue;
+      uint8_t *row = codes + (t >> 4) * (16 * D) + ((t >> 2) & 3) * (4 * D) + (t & 3) * 16;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int d = i ? d1 : d0;
+        uint2 *p = (uint2 *)(row + d / 16 * 64 + d % 16);
+        const float *y = x[j] + 8 * i;
+        if (t >= t0 && t < t1) *p = make_uint2(codes4(y[0], y[1], y[2], y[3], inv), codes4(y[4], y[5], y[6], y[7], inv));
+        else if (move && t < t0) *p = make_uint2(moved4(p->x, by), moved4(p->y, by));
+      }
     }
   }
 }
@@ -404,10 +452,9 @@ __device__ __forceinline__ void turn_queries(const KvDev &a, const RotaryDev &ro
   float cs[8], sn[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    double x = 1.0, y = 0.0;
-    if (turns) cos_sin((double)p * (double)rot.inv_freq[8 * c + i], &x, &y);
-    cs[i] = (float)x;
-    sn[i] = (float)y;
+    cs[i] = 1.f;
+    sn[i] = 0.f;
+    if (turns) cos_sin((double)p * (double)rot.inv_freq[8 * c + i], &cs[i], &sn[i]);
   }
   const T *src = (const T *)q.q + (size_t)r * q.q_stride;
   T *dst = (T *)q.out + (size_t)r * q.out_stride;
@@ -441,15 +488,14 @@ __device__ __forceinline__ void turn_queries(const KvDev &a, const RotaryDev &ro
         ((float4 *)to)[0] = make_float4(y[0], y[1], y[2], y[3]);
         ((float4 *)to)[1] = make_float4(y[4], y[5], y[6], y[7]);
       } else {
-        *(uint4 *)to = make_uint4(pack2(f2bf(y[0]), f2bf(y[1])), pack2(f2bf(y[2]), f2bf(y[3])), pack2(f2bf(y[4]), f2bf(y[5])),
-                                  pack2(f2bf(y[6]), f2bf(y[7])));
+        *(uint4 *)to = make_uint4(pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]), pack_bf16(y[4], y[5]), pack_bf16(y[6], y[7]));
       }
     }
   }
 }
 
-// Grid: touched pages x {K, V} x heads, heads fastest, then the queries' workgroups.
-template <typename T, int D, int IT>
+// Grid: touched pages x (groups of HB heads for K, heads for V), then the queries' workgroups.
+template <typename T, int D, int IT, int HB>
 __global__ __launch_bounds__(kKvThreads) void kv_write_rotary_kernel(KvDev a, RotaryDev rot, TurnArgs q, const T *krows,
                                                                      int k_stride, const T *vrows, int v_stride) {
   __shared__ uint32_t wave_max[kKvThreads / 64];
@@ -458,9 +504,9 @@ __global__ __launch_bounds__(kKvThreads) void kv_write_rotary_kernel(KvDev a, Ro
     turn_queries<T, D>(a, rot, q, blockIdx.x - q.first, pos);
     return;
   }
-  const int both = blockIdx.x / a.H, h = blockIdx.x - both * a.H;
-  if (both & 1) write_page<T, D, IT>(a, both >> 1, h, true, krows, k_stride, vrows, v_stride, wave_max);
-  else write_turned_page<T, D, IT>(a, rot, both >> 1, h, krows, k_stride, wave_max);
+  const int k_groups = (a.H + HB - 1) / HB, per = k_groups + a.H, u = blockIdx.x / per, h = blockIdx.x - u * per;
+  if (h < k_groups) write_turned_page<T, D, IT, HB>(a, rot, u, h * HB, krows, k_stride, wave_max);
+  else write_page<T, D, IT>(a, u, h - k_groups, true, krows, k_stride, vrows, v_stride, wave_max);
 }
 
 // ---------------------------------------------------------------- read
@@ -579,17 +625,22 @@ struct ReadK {
       hipLaunchKernelGGL((kv_read_kernel<T, D, IT>), dim3(grid.y, grid.x, 2), dim3(kKvThreads), 0, st, kv, (T *)k, ks, (T *)v, vs);
   }
 };
-// Heads of a queries' workgroup: as many as leave the card enough of them.
+// Heads of a queries' workgroup: as many as leave the card two of them a CU.
+// Heads of a workgroup of K: two where pages are small enough for their
+// cosines to stay in registers and pages and heads still fill the card.
 template <typename T, int D, int IT>
 struct RotaryK {
   static void go(dim3 grid, hipStream_t st, const KvDev &kv, RotaryDev rot, TurnArgs q, const void *k, int ks, const void *v, int vs) {
     if constexpr (IT * kKvThreads * 16 <= D * 128) {
       const int rows = kKvThreads / (D / 16), row_blocks = (kv.n + rows - 1) / rows;
-      q.per = std::max(1, std::min(q.heads, q.heads * row_blocks / 1024));
+      q.per = std::max(1, std::min(q.heads, q.heads * row_blocks / 512));
       q.groups = (q.heads + q.per - 1) / q.per;
-      q.first = (int)(grid.x * grid.y * 2);
-      hipLaunchKernelGGL((kv_write_rotary_kernel<T, D, IT>), dim3(q.first + row_blocks * q.groups), dim3(kKvThreads), 0, st, kv, rot,
-                         q, (const T *)k, ks, (const T *)v, vs);
+      constexpr int HB = IT <= 2 ? 2 : 1;
+      const bool two = HB == 2 && (long long)grid.x * grid.y >= 512;
+      q.first = (int)grid.x * (two ? (kv.H + 1) / 2 + kv.H : 2 * kv.H);
+      const dim3 all(q.first + row_blocks * q.groups), block(kKvThreads);
+      if (two) hipLaunchKernelGGL((kv_write_rotary_kernel<T, D, IT, HB>), all, block, 0, st, kv, rot, q, (const T *)k, ks, (const T *)v, vs);
+      else hipLaunchKernelGGL((kv_write_rotary_kernel<T, D, IT, 1>), all, block, 0, st, kv, rot, q, (const T *)k, ks, (const T *)v, vs);
     }
   }
 };

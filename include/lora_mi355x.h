@@ -482,7 +482,8 @@ int lora_kv_write(const lora_kv_cache *cache, const lora_kv_seqs *seqs, int32_t 
  * row's position p,  (a, b) -> (a cos - b sin, b cos + a sin).  Pairs are (i,
  * i + rot_dim/2) or, interleaved, (2i, 2i + 1); dims from rot_dim on stay.
  * inv_freq is [dev] f32 [rot_dim/2], any numbers: a caller scales positions
- * through them.  The struct itself is [host].
+ * through them.  Angles of 2^50 and more count as 0, and an infinite or NaN
+ * frequency makes its pair NaN.  The struct itself is [host].
  */
 typedef struct lora_rotary {
   const float *inv_freq; /* [dev] [rot_dim / 2] */

@@ -158,8 +158,15 @@ def test_zero_frequencies_leave_rows_and_special_values():
     x[7, 128:192] = 3e38
     Call(s, "f32", 2, 64, x=x).check()
     s = Setup(14, [(12, 12)], 1, 64, 16)
-    Call(s, "f32", 2, 64, inv=np.full(32, 1e30, np.float32)).run()  # angles far past every reduction stay numbers
+    c = Call(s, "f32", 2, 64, inv=np.full(32, 1e30, np.float32))  # angles of 2^50 and more count as 0
+    c.inv = np.zeros(32, np.float32)
+    c.check()
+    s = Setup(17, [(12, 12)], 1, 64, 16)
+    c = Call(s, "f32", 2, 64, inv=np.array([np.inf, np.nan] + [2.0 ** -7] * 30, np.float32))
+    c.run()
     torch.cuda.synchronize()
+    bad = np.isnan(host(c.out)[:, :128].reshape(12, 2, 64)).any((0, 1))
+    assert np.array_equal(np.flatnonzero(bad), [0, 1, 32, 33])
 
 
 def test_turns_keep_lengths_and_relative_angles():
