@@ -108,7 +108,10 @@ __device__ __forceinline__ u64 wave_sum64(u64 v) { return lane_of64(wave_scan64(
 
 struct SampleLds {
   double table[256];  // 2^43 2^(j/256)
-  u64 bins[kBins];
+  union {
+    u64 bins[kBins];
+    ulonglong2 picks[kSampleList];  // of a list: place and measure
+  };
   u64 seg[kSampleMaxSegs];
   union {
     struct {
@@ -323,33 +326,48 @@ __device__ __forceinline__ float max_pass(const Row<T> &row, int s0, int s1, Sam
   return lds.bad ? __uint_as_float(0x7fc00000u) : m;
 }
 
+// Eight logits of a lane at a time: enough of their chains side by side, and
+// branches for eight together, so that the chains are not cut.
+template <typename T, typename F>
+__device__ __forceinline__ void eights(const Row<T> &row, int first, const uint4 *v, F f) {
+  constexpr int kVectors = 8 / Row<T>::VE;
+#pragma unroll
+  for (int i = 0; i < Row<T>::NV; i += kVectors) {
+    float x[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] = Logits<T>::at(v[i + e / Row<T>::VE], e % Row<T>::VE);
+    f(x, [&](int e) { return Row<T>::index(first, i + e / Row<T>::VE, e % Row<T>::VE); });
+    __builtin_amdgcn_sched_barrier(0);  // more of them side by side take registers that spill
+  }
+}
+
 // The weights of each segment's tokens that the cut keeps and that are `least` or more, by seg(segment, sum).
 template <typename T, typename Seg>
 __device__ __forceinline__ void mass_pass(const Row<T> &row, int s0, int s1, u64 least, SampleLds &lds, Seg seg) {
   const bool all = row.cut == 0 && least == 0;
   row.segments(s0, s1, [&](int s, int first, const uint4 *v) {
     u64 sum = 0;
-    if (all) {
+    eights(row, first, v, [&](const float *x, auto index) {
+      if (all) {
 #pragma unroll
-      for (int i = 0; i < Row<T>::NV; ++i) {
+        for (int e = 0; e < 8; ++e) sum += row.magic_weight(row.exponent(x[e]), lds.table);
+        sum -= 8 * Row<T>::kMagicBits;
+      } else {
+        u64 places[8];
+        bool some = false;
 #pragma unroll
-        for (int e = 0; e < Row<T>::VE; ++e) sum += row.magic_weight(row.exponent(Logits<T>::at(v[i], e)), lds.table);
-        __builtin_amdgcn_sched_barrier(0);  // a vector's work at a time: all of a segment's takes registers that spill
-      }
-      sum -= (u64)(Row<T>::NV * Row<T>::VE) * Row<T>::kMagicBits;
-    } else {
+        for (int e = 0; e < 8; ++e) {
+          places[e] = place_of(x[e], index(e));
+          some |= row.keeps(places[e]);
+        }
+        if (!__any(some)) return;
 #pragma unroll
-      for (int i = 0; i < Row<T>::NV; ++i) {
-#pragma unroll
-        for (int e = 0; e < Row<T>::VE; ++e) {
-          const float x = Logits<T>::at(v[i], e);
-          if (!__any(row.keeps(place_of(x, Row<T>::index(first, i, e))))) continue;  // most are kept nowhere in a wave
-          const u64 w = row.weight(x, lds.table);
-          sum += w >= least && row.keeps(place_of(x, Row<T>::index(first, i, e))) ? w : 0;
-          __builtin_amdgcn_sched_barrier(0);
+        for (int e = 0; e < 8; ++e) {
+          const u64 w = row.weight(x[e], lds.table);
+          sum += w >= least && row.keeps(places[e]) ? w : 0;
         }
       }
-    }
+    });
     sum = wave_sum64(sum);
     if ((threadIdx.x & 63) == 0) seg(s, sum);
   });
@@ -359,18 +377,26 @@ __device__ __forceinline__ void mass_pass(const Row<T> &row, int s0, int s1, u64
 template <typename T>
 __device__ __forceinline__ void bin_pass(const Row<T> &row, int s0, int s1, bool counts, SampleLds &lds) {
   row.segments(s0, s1, [&](int, int first, const uint4 *v) {
+    eights(row, first, v, [&](const float *x, auto index) {
+      int b[8];
+      u64 w[8];
 #pragma unroll
-    for (int i = 0; i < Row<T>::NV; ++i) {
-#pragma unroll
-      for (int e = 0; e < Row<T>::VE; ++e) {
-        const float x = Logits<T>::at(v[i], e);
-        const double t = row.exponent(x);
-        const int b = Row<T>::bin_of(Row<T>::whole(t));
-        if (b < kLowest && (row.cut == 0 || row.keeps(place_of(x, Row<T>::index(first, i, e)))))
-          atomicAdd(&lds.bins[b], counts ? 1ull : row.magic_weight(t, lds.table) - Row<T>::kMagicBits);
+      for (int e = 0; e < 8; ++e) {
+        const double t = row.exponent(x[e]);
+        b[e] = Row<T>::bin_of(Row<T>::whole(t));
+        w[e] = row.magic_weight(t, lds.table) - Row<T>::kMagicBits;
       }
-      __builtin_amdgcn_sched_barrier(0);
-    }
+      if (counts) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) w[e] = b[e] < kLowest;  // the lowest bin's logits may lie outside the row
+      }
+      if (row.cut) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) w[e] = row.keeps(place_of(x[e], index(e))) ? w[e] : 0;
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) atomicAdd(&lds.bins[b[e]], w[e]);
+    });
   });
 }
 
@@ -399,24 +425,35 @@ __device__ __forceinline__ void list_and_mass_pass(const Row<T> &row, int s0, in
   const float floor = row.floor_of_bin(b);
   row.segments(s0, s1, [&](int s, int first, const uint4 *v) {
     u64 sum = 0;
+    eights(row, first, v, [&](const float *x, auto index) {
+      float most = x[0];
 #pragma unroll
-    for (int i = 0; i < Row<T>::NV; ++i) {
+      for (int e = 1; e < 8; ++e) most = fmaxf(most, x[e]);
+      if (!__any(most >= floor)) return;
+      int its[8];
+      u64 w[8];
+      bool here = false;
 #pragma unroll
-      for (int e = 0; e < Row<T>::VE; ++e) {
-        const float x = Logits<T>::at(v[i], e);
-        if (!__any(x >= floor)) continue;
-        const double t = row.exponent(x);
-        const int its = Row<T>::bin_of(Row<T>::whole(t));
-        u64 w = row.magic_weight(t, lds.table) - Row<T>::kMagicBits;
-        if (row.cut | row.least) w = w >= row.least && row.keeps(place_of(x, Row<T>::index(first, i, e))) ? w : 0;
-        sum += its < b ? w : 0;
-        if (__any(its == b) && its == b) {
-          const u64 place = place_of(x, Row<T>::index(first, i, e));
-          if (row.keeps(place)) put(place);
+      for (int e = 0; e < 8; ++e) {
+        const double t = row.exponent(x[e]);
+        its[e] = Row<T>::bin_of(Row<T>::whole(t));
+        w[e] = row.magic_weight(t, lds.table) - Row<T>::kMagicBits;
+        here |= its[e] == b;
+      }
+      if (row.cut | row.least) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) w[e] = w[e] >= row.least && row.keeps(place_of(x[e], index(e))) ? w[e] : 0;
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) sum += its[e] < b ? w[e] : 0;
+      if (__any(here)) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const u64 place = place_of(x[e], index(e));
+          if (its[e] == b && row.keeps(place)) put(place);
         }
       }
-      __builtin_amdgcn_sched_barrier(0);
-    }
+    });
     sum = wave_sum64(sum);
     if ((threadIdx.x & 63) == 0) seg(s, sum);
   });
@@ -516,30 +553,31 @@ __device__ __forceinline__ void weigh_list(const Row<T> &row, SampleLds &lds) {
   for (int i = threadIdx.x; i < lds.count; i += kSampleThreads) lds.w[i] = row.weight(value_of((uint32_t)(lds.list[i] >> 32)), lds.table);
   __syncthreads();
 }
-// Among the picked ones of the listed places, the one at which the running
-// measure reaches goal.  over(i, j): i comes before j.  The running measure
-// starts at 0; called after a barrier, ends with one.
-template <typename Over, typename Measure, typename Found>
-__device__ __forceinline__ void reach_in_picks(u64 goal, Over over, Measure measure, Found found, SampleLds &lds) {
-  const uint32_t *const pick = (const uint32_t *)lds.bins;
-  const int c = lds.picked;
-  for (int i = threadIdx.x; i < c; i += kSampleThreads) {
-    const int me = pick[i];
-    u64 before = 0;
-    for (int j = 0; j < c; ++j) before += over(pick[j], me) ? measure(pick[j]) : 0;
-    if (goal > before && goal <= before + measure(me)) found(me, before);
-  }
-  __syncthreads();
-}
-// Indexes of the listed places for which in(i) holds, into the bins' space.  Called after a barrier, ends with one.
-template <typename In>
-__device__ __forceinline__ void pick_from_list(In in, SampleLds &lds) {
-  static_assert(kSampleList * sizeof(uint32_t) <= kBins * sizeof(u64), "picks fit the bins");
-  uint32_t *const pick = (uint32_t *)lds.bins;
+// The listed places for which in(i) holds, each with its measure(i), side by
+// side into lds.picks.  Called after a barrier, ends with one.
+template <typename In, typename Measure>
+__device__ __forceinline__ void pick_from_list(In in, Measure measure, SampleLds &lds) {
   if (threadIdx.x == 0) lds.picked = 0;
   __syncthreads();
   for (int i = threadIdx.x; i < lds.count; i += kSampleThreads)
-    if (in(i)) pick[atomicAdd(&lds.picked, 1)] = i;
+    if (in(i)) lds.picks[atomicAdd(&lds.picked, 1)] = ulonglong2{lds.list[i], measure(i)};
+  __syncthreads();
+}
+// Among the picked places, the one at which the running measure reaches goal;
+// over(a, b): place a comes before b.  Ends with a barrier.
+template <typename Over, typename Found>
+__device__ __forceinline__ void reach_in_picks(u64 goal, Over over, Found found, SampleLds &lds) {
+  const int c = lds.picked;
+  for (int i = threadIdx.x; i < c; i += kSampleThreads) {
+    const ulonglong2 me = lds.picks[i];
+    u64 before = 0;
+#pragma unroll 8
+    for (int j = 0; j < c; ++j) {
+      const ulonglong2 other = lds.picks[j];
+      before += over(other.x, me.x) ? other.y : 0;
+    }
+    if (goal > before && goal <= before + me.y) found(me.x);
+  }
   __syncthreads();
 }
 // The cut among the lds.count <= kSampleList listed places that the row
@@ -573,9 +611,8 @@ __device__ __forceinline__ u64 cut_in_list(const Row<T> &row, int b, u64 goal, b
   const int f = lds.found;
   goal -= lds.found_above;
   __syncthreads();
-  pick_from_list([&](int i) { return fine(i) == f; }, lds);
-  reach_in_picks(goal, [&](int i, int j) { return lds.list[i] > lds.list[j]; }, measure,
-                 [&](int i, u64) { lds.found_above = lds.list[i]; }, lds);
+  pick_from_list([&](int i) { return fine(i) == f; }, measure, lds);
+  reach_in_picks(goal, [](u64 a, u64 b) { return a > b; }, [&](u64 place) { lds.found_above = place; }, lds);
   const u64 cut = uniform(lds.found_above);
   __syncthreads();
   return cut;
@@ -680,10 +717,9 @@ __device__ __forceinline__ void draw_from_list(const SampleArgs &a, Row<T> row, 
   const int b = lds.found;
   goal -= lds.found_above;
   __syncthreads();
-  pick_from_list([&](int i) { return stays(i) && index_of(lds.list[i]) >> shift == b; }, lds);
-  reach_in_picks(goal, [&](int i, int j) { return (uint32_t)lds.list[i] > (uint32_t)lds.list[j]; },  // the index's complement
-                 [&](int i) { return lds.w[i]; },
-                 [&](int i, u64) { write_result(a, row, r, index_of(lds.list[i]), value_of((uint32_t)(lds.list[i] >> 32)), total); }, lds);
+  pick_from_list([&](int i) { return stays(i) && index_of(lds.list[i]) >> shift == b; }, [&](int i) { return lds.w[i]; }, lds);
+  reach_in_picks(goal, [](u64 a, u64 b) { return (uint32_t)a > (uint32_t)b; },  // the index's complement
+                 [&](u64 place) { write_result(a, row, r, index_of(place), value_of((uint32_t)(place >> 32)), total); }, lds);
 }
 
 // ---------------------------------------------------------------- one workgroup's way through a row
@@ -880,9 +916,15 @@ __device__ __forceinline__ bool max_of_chunks(const SampleArgs &a, const SampleR
                                              [](int a, int b) { return __float_as_int(fmaxf(__int_as_float(a), __int_as_float(b))); }));
   return row.set_max(__any(mine != mine) ? __uint_as_float(0x7fc00000u) : m);
 }
-__device__ __forceinline__ void put_global(SampleRow &w, u64 place) {
-  const int at = __hip_atomic_fetch_add(&w.count, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-  if (at < kSampleList) w.list[at] = place;
+// The workgroup's list joins the row's: one reservation, as every trip to
+// memory's counter is a microsecond.  Called after a barrier.
+__device__ __forceinline__ void join_list(SampleRow &w, SampleLds &lds) {
+  const int n = lds.count;
+  if (n == 0) return;
+  if (threadIdx.x == 0) lds.index = __hip_atomic_fetch_add(&w.count, n, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  __syncthreads();
+  for (int i = threadIdx.x; i < min(n, kSampleList); i += kSampleThreads)
+    if (lds.index + i < kSampleList) w.list[lds.index + i] = lds.list[i];
 }
 
 // Grid of these three: rows x chunks.  Maxima.
@@ -915,7 +957,11 @@ __global__ __launch_bounds__(kSampleThreads, 4) void sample_sum_kernel(SampleArg
   if (!max_of_chunks(a, w, row)) return;
   if (row.by_list()) {
     const float floor = list_floor(row, w.parts, lds);
-    list_pass(row, k.s0, k.s1, floor, [&](float v, int i) { put_global(w, place_of(v, i)); });
+    if (threadIdx.x == 0) lds.count = 0;
+    __syncthreads();
+    list_pass(row, k.s0, k.s1, floor, [&](float v, int i) { put(lds, place_of(v, i)); });
+    __syncthreads();
+    join_list(w, lds);
   } else if (row.top_k == 0) {
     fill_table(lds);
     if (row.top_p < 1.f) {
@@ -955,7 +1001,11 @@ __global__ __launch_bounds__(kSampleThreads, 4) void sample_list_kernel(SampleAr
     w.bin = b;
     w.wants = wants;
   }
-  list_and_mass_pass(row, k.s0, k.s1, b, lds, [&](u64 place) { put_global(w, place); }, [&](int s, u64 sum) { w.seg[s] = sum; });
+  if (threadIdx.x == 0) lds.count = 0;
+  __syncthreads();
+  list_and_mass_pass(row, k.s0, k.s1, b, lds, [&](u64 place) { put(lds, place); }, [&](int s, u64 sum) { w.seg[s] = sum; });
+  __syncthreads();
+  join_list(w, lds);
 }
 
 // Grid: rows.  The drawing.
