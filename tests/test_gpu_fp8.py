@@ -203,3 +203,27 @@ def test_quantize_then_multiply():
     off = ex @ np.abs(hw).T + np.abs(hx) @ ew.T + ex @ ew.T
     y, mag = D.matmul(xc, xs, wc, wsc)
     assert (np.abs(got - hx @ hw.T) <= off + D.matmul_bound("bf16", y, mag, k)).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("n,n_out,k", [(20, 22016, 144), (33, 32000, 128), (60, 11008, 272), (100, 22016, 16), (128, 32000, 144), (128, 8192, 1040),
+                                       (1, 40, 16384), (16, 136, 8336), (40, 136, 8336), (128, 264, 16384), (200, 136, 8336), (2000, 2056, 1168)])
+def test_matmul_of_wide_and_deep_weights(n, n_out, k, dtype):
+    Product(n + n_out + k, n, n_out, k, dtype=dtype).check()
+
+
+@pytest.mark.parametrize("n", [2, 40, 150, 1000])
+def test_products_at_once(n):
+    """Calls on two streams that share weights and rows."""
+    p, q = (Product(n, n, 1032, 400) for _ in range(2))
+    p.upload()
+    q.upload()
+    q.dw, q.dws, q.dx, q.dxs = p.dw, p.dws, p.dx, p.dxs
+    torch.cuda.synchronize()
+    a, b = torch.cuda.Stream(), torch.cuda.Stream()
+    for _ in range(20):
+        p.call(a)
+        q.call(b)
+    y, mag = D.matmul(p.x, p.xs, p.w, p.ws)
+    for c in (p, q):
+        assert (np.abs(c.result() - y) <= D.matmul_bound("bf16", y, mag, 400)).all()

@@ -194,3 +194,55 @@ def test_captured_and_on_another_stream(n, V):
     d.run(s)
     s.synchronize()
     assert np.array_equal(d.result()[0], want[0])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("V,n,skew", [(1 << 20, 4, 3), ((1 << 20) - 5, 3, 0), (9001, 520, 1), (33000, 130, 5)])
+def test_large_vocabularies_and_many_rows(V, n, skew, dtype):
+    rng = np.random.default_rng(V + n)
+    x = rng.standard_normal((n, V)) * 3
+    Draw(x, dtype, skew=skew, pad=3, **settings(rng, n, V)).check()
+
+
+@pytest.mark.parametrize("n", [12, 900])
+def test_bad_logits_in_any_part_of_a_long_row(n):
+    """One NaN or infinity at the row's ends and between them; a row whose only
+    finite logit lies there; the rows beside draw as ever."""
+    V = 20011
+    rng = np.random.default_rng(n)
+    x = rng.standard_normal((n, V))
+    for i, at in enumerate((0, 2047, 2048, V - 1)):
+        x[i, at] = np.nan
+        x[4 + i, at] = np.inf
+        x[8 + i] = -np.inf
+        x[8 + i, at] = -3.0
+    d = Draw(x[:12], "f32", skew=1, k=[0, 7] * 6, p=[1.0, 1.0, 0.9] * 4, u=rng.random(12))
+    ids = d.check()
+    assert (ids[:8] == -1).all() and ids[8:].tolist() == [0, 2047, 2048, V - 1]
+    e = Draw(x, "f32", skew=1, k=5, u=0.5)
+    e.run()
+    ids, logp = e.result()
+    assert (ids[:8] == -1).all() and np.isnan(logp[:8]).all() and ids[8:12].tolist() == [0, 2047, 2048, V - 1]
+    assert (ids[12:] >= 0).all()
+
+
+def test_a_workspace_used_again_and_calls_at_once():
+    """A workspace that a larger call left full, and two streams with one each."""
+    rng = np.random.default_rng(12)
+    big = Draw(rng.standard_normal((80, 32000)) * 3, "bf16", **settings(rng, 80, 32000))
+    small = Draw(rng.standard_normal((3, 9000)) * 3, "f32", **settings(rng, 3, 9000))
+    many = Draw(rng.standard_normal((600, 700)) * 3, "f32", **settings(rng, 600, 700))
+    want = [d.check() for d in (big, small, many)]
+    small.ws = many.ws = big.ws
+    for d, w in ((big, want[0]), (small, want[1]), (many, want[2]), (big, want[0])):
+        if B.lora_token_sample_workspace_bytes(DT[d.dtype][0], d.V, d.n) > big.need:
+            continue
+        assert np.array_equal(d.check(), w)
+    small.ws = torch.full_like(big.ws, 255)
+    assert np.array_equal(small.check(), want[1])
+    a, b = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(20):
+        big.run(a)
+        small.run(b)
+    assert np.array_equal(big.result()[0], want[0]) and np.array_equal(small.result()[0], want[1])
