@@ -16,8 +16,11 @@
 // first at which the running sum exceeds floor(u sum) is the row's.
 //
 // The exponent's whole steps, n = rint(256 log2(e) (x - m) / T), serve twice:
-// they pick 2^(n/256) from a table, and 16 of them are a bin.  Rows go by what
-// they ask for:
+// they pick 2^(n/256) from a table, and some of them are a bin: 1 up to 512, 2
+// up to 1536, 4 up to 3584 and so on, as a flat row's tokens lie in the first
+// powers of two.  (16 throughout: 131071 normally distributed logits put 2300 into
+// top-p's bin, more than a list holds, and the draw took 328 us.)  Rows go by
+// what they ask for:
 //   top-k up to 512: the row's maximum comes with those of its parts, 32
 //     logits each.  The bin that k of these maxima reach bounds the k-th
 //     largest logit from below, so the few logits from there up are listed
@@ -35,6 +38,7 @@
 // row is needed: maxima, sums and lists, lists of top-p's bin, the drawing.
 #include <algorithm>
 #include <climits>
+#include <type_traits>
 
 #include "common.hpp"
 #include "verify.hpp"
@@ -43,8 +47,10 @@ namespace lora {
 
 typedef unsigned long long u64;
 constexpr int kRadixBins = 2048;
-constexpr int kBins = 768;           // of 16 steps, 1/16 of a power of two: 48 powers, beyond which weights are 0
-constexpr int kLowest = kBins - 1;   // holds weights of 0 only
+constexpr int kBins = 2274;          // of 44 powers of two and the step below, beyond which weights are 0
+constexpr int kSteps = 44 * 256 + 32;
+constexpr int kLowest = kBins - 1;   // holds weights of 0 only: its first step is 11280, 2^(43 - 44.06)
+constexpr int kBinsEach = (kBins + kSampleThreads - 1) / kSampleThreads;  // of a thread
 constexpr int kMostListedK = 512;    // top-k that goes by the parts' maxima
 constexpr int kParts = 4096;         // maxima that a row keeps at most
 constexpr int kWaves = kSampleThreads / 64;
@@ -106,7 +112,7 @@ __device__ __forceinline__ u64 lane_of64(u64 v, int lane) {
 }
 __device__ __forceinline__ u64 wave_sum64(u64 v) { return lane_of64(wave_scan64(v), 63); }
 
-struct SampleLds {
+struct alignas(16) SampleLds {
   double table[256];  // 2^43 2^(j/256)
   union {
     u64 bins[kBins];
@@ -201,19 +207,23 @@ struct Row {
   }
   static __device__ int index(int first, int i, int e) { return first + i * 64 * VE + e; }
 
-  // 256 log2 of the weight's share, at least -16 kBins + 1: from there on weights are 0.
-  __device__ double exponent(float v) const { return fmax(((double)v - (double)m) * steps, (double)(1 - 16 * kBins)); }
+  // 256 log2 of the weight's share, at least 1 - kSteps: from there on weights are 0.
+  __device__ double exponent(float v) const { return fmax(((double)v - (double)m) * steps, (double)(1 - kSteps)); }
   static __device__ int whole(double t) { return (int)(uint32_t)__double_as_longlong(t + 6755399441055744.0); }  // + 1.5 2^52
-  static __device__ int bin_of(int n) { return -n >> 4; }
+  // 512 bins for every doubling of 512 - n: nine digits of it as a float
+  static constexpr int kBinBits = 14, kBin0 = (127 + 9) << (23 - kBinBits);
+  static __device__ int bin_of(int n) { return (int)(__float_as_uint((float)(512 - n)) >> kBinBits) - kBin0; }
+  static __device__ int first_step(int b) { return (int)__uint_as_float((uint32_t)(b + kBin0) << kBinBits) - 512; }
   __device__ int bin(float v) const { return bin_of(whole(exponent(v))); }
   // No logit below it lies in bin b or above: b's own floor less a step, and the next lower float.
   __device__ float floor_of_bin(int b) const {
-    const float f = (float)((double)m - (16.0 * b + 17.0) / steps);
+    const float f = (float)((double)m - (first_step(b + 1) + 1) / steps);
     return uniform(f > -INFINITY ? value_of(sample_key(f) - 1) : f);
   }
   // The place within its bin, in 256 parts: larger weights first.
   __device__ int fine_bin(float v, int b) const {
-    return min(max((int)((-exponent(v) - 16.0 * b + 0.5) * 16.0), 0), 255);
+    const int first = first_step(b);
+    return min(max((int)((-exponent(v) - first + 0.5) * (256.0 / (first_step(b + 1) - first))), 0), 255);
   }
   // 2^(n/256) from the table, times 2^(h/256) for what is left, |h| <= 1/2: its
   // series in h, in which a^2 h^2 stands for the fourth term's h^4 at the end
@@ -257,14 +267,16 @@ __device__ __forceinline__ u64 block_sum64(u64 v, SampleLds &lds) {
   return s;
 }
 
-// The first of n <= 4 kSampleThreads entries at which the running sum reaches
-// goal >= 1 into lds.found, the sum before it into lds.found_above; n where
-// none does.  at(i) gives entry i.  Called after a barrier, ends with one.
-template <typename At>
-__device__ __forceinline__ void find_reach(int n, u64 goal, At at, SampleLds &lds) {
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, per = (n + kSampleThreads - 1) / kSampleThreads;
+// The first of n entries at which the running sum reaches goal >= 1 into
+// lds.found, the sum before it into lds.found_above; n where none does.  at(i)
+// gives entry i < n.  Called after a barrier, ends with one.
+template <typename N, typename At>
+__device__ __forceinline__ void find_reach(N n, u64 goal, At at, SampleLds &lds) {
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int per = (n + kSampleThreads - 1) / kSampleThreads | 1, first = per * tid;  // odd: distinct banks
   u64 sum = 0;
-  for (int i = 0; i < per; ++i) sum += per * tid + i < n ? at(per * tid + i) : 0;
+#pragma unroll
+  for (int i = 0; i < per; ++i) sum += first + i < n ? at(first + i) : 0;
   u64 incl = wave_scan64(sum);
   if (lane == 63) lds.scan[wave] = incl;
   if (tid == 0) lds.found = n;
@@ -273,9 +285,9 @@ __device__ __forceinline__ void find_reach(int n, u64 goal, At at, SampleLds &ld
   u64 before = incl - sum;
   if (goal > before && goal <= incl) {
     for (int i = 0; i < per; ++i) {
-      const u64 w = at(per * tid + i);
+      const u64 w = at(first + i);
       if (goal <= before + w) {
-        lds.found = per * tid + i;
+        lds.found = first + i;
         lds.found_above = before;
         break;
       }
@@ -284,9 +296,15 @@ __device__ __forceinline__ void find_reach(int n, u64 goal, At at, SampleLds &ld
   }
   __syncthreads();
 }
+// As many entries as are known when this is compiled: their reads go out together.
+template <int N>
+using Bins = std::integral_constant<int, N>;
 
-__device__ __forceinline__ void clear_bins(SampleLds &lds, int n) {
-  for (int i = threadIdx.x; i < n; i += kSampleThreads) lds.bins[i] = 0;
+template <typename N>
+__device__ __forceinline__ void clear_bins(SampleLds &lds, N n) {
+#pragma unroll
+  for (int e = 0; e < (n + kSampleThreads - 1) / kSampleThreads; ++e)
+    if (threadIdx.x + e * kSampleThreads < n) lds.bins[threadIdx.x + e * kSampleThreads] = 0;
 }
 __device__ __forceinline__ void put(SampleLds &lds, u64 place) {
   const int at = atomicAdd(&lds.count, 1);
@@ -589,25 +607,25 @@ __device__ __forceinline__ u64 cut_in_list(const Row<T> &row, int b, u64 goal, b
   auto value = [&](int i) { return value_of((uint32_t)(lds.list[i] >> 32)); };
   auto measure = [&](int i) -> u64 { return counts ? 1 : lds.w[i]; };
   if (b < 0) {
-    clear_bins(lds, kBins);
+    clear_bins(lds, Bins<kBins>());
     __syncthreads();
     for (int i = tid; i < n; i += kSampleThreads)
       if (row.keeps(lds.list[i])) atomicAdd(&lds.bins[row.bin(value(i))], measure(i));
     __syncthreads();
-    find_reach(kBins, goal, [&](int i) { return lds.bins[i]; }, lds);
+    find_reach(Bins<kBins>(), goal, [&](int i) { return lds.bins[i]; }, lds);
     b = lds.found;
     goal -= lds.found_above;
     __syncthreads();
   }
   auto fine = [&](int i) { return row.keeps(lds.list[i]) && row.bin(value(i)) == b ? row.fine_bin(value(i), b) : -1; };
-  clear_bins(lds, 256);
+  clear_bins(lds, Bins<256>());
   __syncthreads();
   for (int i = tid; i < n; i += kSampleThreads) {
     const int f = fine(i);
     if (f >= 0) atomicAdd(&lds.bins[f], measure(i));
   }
   __syncthreads();
-  find_reach(256, goal, [&](int i) { return lds.bins[i]; }, lds);
+  find_reach(Bins<256>(), goal, [&](int i) { return lds.bins[i]; }, lds);
   const int f = lds.found;
   goal -= lds.found_above;
   __syncthreads();
@@ -701,7 +719,7 @@ __device__ __forceinline__ void draw_from_list(const SampleArgs &a, Row<T> row, 
   // by index: bins of 2^shift of them
   const int shift = max(0, 32 - __clz(row.V) - 9);
   static_assert(kBins >= 512, "a bin for every 2^shift indexes");
-  clear_bins(lds, kBins);
+  clear_bins(lds, Bins<512>());
   __syncthreads();
   u64 total = 0;
   auto stays = [&](int i) { return row.keeps(lds.list[i]) && lds.w[i] >= row.least; };
@@ -713,7 +731,7 @@ __device__ __forceinline__ void draw_from_list(const SampleArgs &a, Row<T> row, 
   total = block_sum64(total, lds);
   u64 goal = goal_of(row.u, total) + 1;
   __syncthreads();
-  find_reach(512, goal, [&](int i) { return lds.bins[i]; }, lds);
+  find_reach(Bins<512>(), goal, [&](int i) { return lds.bins[i]; }, lds);
   const int b = lds.found;
   goal -= lds.found_above;
   __syncthreads();
@@ -739,14 +757,14 @@ __device__ __forceinline__ void store_part(float *parts, int shift, int seg, flo
 template <typename T>
 __device__ __forceinline__ float list_floor(const Row<T> &row, const float *parts, SampleLds &lds) {
   const int tid = threadIdx.x, n = row.segs << (6 - part_shift(row.segs));
-  clear_bins(lds, kBins);
+  clear_bins(lds, Bins<kBins>());
   __syncthreads();
   for (int i = tid; i < n; i += kSampleThreads) {
     const int b = row.bin(parts[i]);
     if (b < kLowest) atomicAdd(&lds.bins[b], 1ull);
   }
   __syncthreads();
-  find_reach(kBins, (u64)row.top_k, [&](int i) { return lds.bins[i]; }, lds);
+  find_reach(Bins<kBins>(), (u64)row.top_k, [&](int i) { return lds.bins[i]; }, lds);
   const int b = __builtin_amdgcn_readfirstlane(lds.found);
   if (b == kBins) return row.floor_of_bin(kLowest - 1);
   float f = INFINITY;
@@ -765,11 +783,15 @@ __device__ __forceinline__ float list_floor(const Row<T> &row, const float *part
 template <typename T>
 __device__ __forceinline__ int top_p_bin(const Row<T> &row, u64 *wants, SampleLds &lds) {
   u64 mass = 0;
-  for (int i = threadIdx.x; i < kBins; i += kSampleThreads) mass += lds.bins[i];
+#pragma unroll
+  for (int e = 0; e < kBinsEach; ++e) {
+    const int i = threadIdx.x + e * kSampleThreads;
+    mass += i < kBins ? lds.bins[i] : 0;
+  }
   mass = block_sum64(mass, lds);
   const u64 goal = wanted(row.top_p, mass);
   __syncthreads();
-  find_reach(kBins, goal, [&](int i) { return lds.bins[i]; }, lds);
+  find_reach(Bins<kBins>(), goal, [&](int i) { return lds.bins[i]; }, lds);
   *wants = goal - lds.found_above;
   return __builtin_amdgcn_readfirstlane(lds.found);
 }
@@ -813,12 +835,12 @@ __device__ __forceinline__ bool draw_by_bins(const SampleArgs &a, Row<T> row, in
   auto to_list = [&](u64 place) { put(lds, place); };
   auto to_seg = [&](int s, u64 sum) { lds.seg[s] = sum; };
   if (row.top_k > 0) {
-    clear_bins(lds, kBins);
+    clear_bins(lds, Bins<kBins>());
     if (tid == 0) lds.count = 0;
     __syncthreads();
     bin_pass(row, 0, row.segs, true, lds);
     __syncthreads();
-    find_reach(kBins, (u64)row.top_k, [&](int i) { return lds.bins[i]; }, lds);
+    find_reach(Bins<kBins>(), (u64)row.top_k, [&](int i) { return lds.bins[i]; }, lds);
     if (lds.found < kBins) {  // else fewer have a weight
       const int b = lds.found;
       const u64 wants = (u64)row.top_k - lds.found_above;
@@ -830,7 +852,7 @@ __device__ __forceinline__ bool draw_by_bins(const SampleArgs &a, Row<T> row, in
     __syncthreads();
   }
   if (row.top_p < 1.f) {
-    clear_bins(lds, kBins);
+    clear_bins(lds, Bins<kBins>());
     if (tid == 0) lds.count = 0;
     __syncthreads();
     bin_pass(row, 0, row.segs, false, lds);
@@ -965,7 +987,7 @@ __global__ __launch_bounds__(kSampleThreads, 4) void sample_sum_kernel(SampleArg
   } else if (row.top_k == 0) {
     fill_table(lds);
     if (row.top_p < 1.f) {
-      clear_bins(lds, kBins);
+      clear_bins(lds, Bins<kBins>());
       __syncthreads();
       bin_pass(row, k.s0, k.s1, false, lds);
       __syncthreads();
@@ -988,12 +1010,14 @@ __global__ __launch_bounds__(kSampleThreads, 4) void sample_list_kernel(SampleAr
   SampleRow &w = row_record(a, k.r);
   if (!max_of_chunks(a, w, row)) return;
   fill_table(lds);
-  for (int i = threadIdx.x; i < kBins; i += kSampleThreads) {
-    u64 sum = 0;
-#pragma unroll 8
-    for (int c = 0; c < a.chunks; ++c) sum += w.bins[c][i];
-    lds.bins[i] = sum;
-  }
+  u64 sums[kBinsEach] = {};
+#pragma unroll 3
+  for (int c = 0; c < a.chunks; ++c)
+#pragma unroll
+    for (int e = 0; e < kBinsEach; ++e) sums[e] += w.bins[c][min((int)threadIdx.x + e * kSampleThreads, kBins - 1)];
+#pragma unroll
+  for (int e = 0; e < kBinsEach; ++e)
+    if (threadIdx.x + e * kSampleThreads < kBins) lds.bins[threadIdx.x + e * kSampleThreads] = sums[e];
   __syncthreads();
   u64 wants;
   const int b = top_p_bin(row, &wants, lds);
@@ -1049,7 +1073,8 @@ __global__ __launch_bounds__(kSampleThreads, 4) void sample_draw_kernel(SampleAr
 int sample_chunks(int n, int n_vocab, int dtype) {
   const int ve = dtype == 0 ? 4 : 8;
   const int segs = (n_vocab + ve - 1 + kSampleSeg - 1) / kSampleSeg;  // a row may begin up to ve - 1 elements into its first vector
-  return std::max(1, std::min({(segs + kWaves - 1) / kWaves, 512 / n, kSampleMaxChunks}));
+  const int fill = n_vocab <= 65536 ? 256 : 512;
+  return std::max(1, std::min({(segs + kWaves - 1) / kWaves, fill / n, kSampleMaxChunks}));
 }
 
 template <typename T>

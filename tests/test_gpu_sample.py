@@ -246,3 +246,18 @@ def test_a_workspace_used_again_and_calls_at_once():
         big.run(a)
         small.run(b)
     assert np.array_equal(big.result()[0], want[0]) and np.array_equal(small.result()[0], want[1])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("V,n", [(131071, 4), (32000, 70), (16000, 600)])
+def test_flat_rows(V, n, dtype):
+    """Rows whose tokens lie within few powers of two, by any cut."""
+    rng = np.random.default_rng(V + n)
+    x = rng.standard_normal((n, V)) * rng.choice([0.01, 0.1, 0.2, 0.5, 1.0, 1.5], (n, 1))
+    kw = settings(rng, n, V)
+    rows = np.arange(n) if n < 100 else rng.integers(0, n, 80)
+    d = Draw(x, dtype, **kw)
+    d.run()
+    ids, logp = d.result()
+    e = Draw(x[rows], dtype, **{a: v[rows] for a, v in kw.items()})
+    assert np.array_equal(e.check(), ids[rows]) and np.array_equal(e.result()[1], logp[rows], equal_nan=True)
