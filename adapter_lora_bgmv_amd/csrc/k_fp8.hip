@@ -11,8 +11,14 @@
 // 2^-13 of it lose digits.  Of normally distributed values 1.4e-5 of the result
 // is lost, of random codes up to 1.6e-4 of the sum of magnitudes, and at worst
 // 2^-10.2 of it (one product 2^14 times the size of all others), against the
-// 2^-9 to which a bf16 y is rounded and the 2^-4 of the codes themselves.  f32 calls therefore bring the codes to bf16, exactly, and run
+// 2^-9 to which a bf16 y is rounded and the 2^-4 of the codes themselves.  f32
+// calls therefore bring the codes to bf16, exactly, and run
 // v_mfma_f32_16x16x32_bf16, which keeps f32 sums.
+//
+// The quantisation reads a row once and keeps it in registers between its
+// maximum and its codes; memory bounds it (22016 x 4096 bf16 in blocks of 128 x
+// 128: 52 us, 5.2 TB/s).  The product has three forms, by its rows: few of
+// them stream W into registers, more share x through LDS, and many are tiles.
 #include <algorithm>
 #include <type_traits>
 
@@ -178,7 +184,7 @@ __device__ __forceinline__ void store4(u16 *p, f32x4 v) {
 __device__ __forceinline__ void store4(float *p, f32x4 v) { *(float4 *)p = make_float4(v[0], v[1], v[2], v[3]); }
 
 // ---------------------------------------------------------------- few rows
-// W is streamed once and bounds the call.  128 columns of a row of codes, by
+// W is streamed once and bounds the call: 4.7 TB/s at 22016 x 4096, one row.  128 columns of a row of codes, by
 // a lane's two 16-byte loads; columns past k are zeros.
 __device__ __forceinline__ Codes fetch_block(const uint8_t *row, int block, int k) {
   const int c0 = ((int)threadIdx.x & 48) + block * kFp8Block;  // lane / 16 * 16
@@ -229,7 +235,8 @@ __global__ __launch_bounds__(kFewWaves * 64) void matmul_few_kernel(Fp8Args p) {
   if (row < p.n && o < p.n_out) store4((Y *)p.y + row * p.y_stride + o, v);
 }
 
-// Up to 16 NB rows.  Every workgroup reads all of x, a part of 64 KB at a time
+// Up to 16 NB rows, W's stream again the bound (64 rows by 32000 x 4096: 30 us,
+// 4.4 TB/s of W).  Every workgroup reads all of x, a part of 64 KB at a time
 // (1024 columns of 64 rows), through registers into the half of LDS that the
 // part before the last has left, while W streams into registers, eight blocks
 // of a wave ahead and across the parts.  Of the eight waves RG take 16 output
@@ -376,8 +383,10 @@ __device__ __forceinline__ void dma4_buffer(__amdgpu_buffer_rsrc_t r, uint32_t v
 // stage is as many cache lines as the codes are (4096 x 22016 x 4096: 529 us
 // that way).  NS stages form a ring with NS - 1 in flight; the waits are
 // explicit, and a stage is read only after every wave's share of it landed.
-// Rows past the ends load a valid row and are not stored; chunks past k are
-// zeroed once they have landed.
+// Rows past the ends read as nothing and are not stored; chunks past k are
+// zeroed once they have landed.  The matrix instruction bounds the largest
+// tiles: 4096 x 22016 x 4096 in 390 us, 1.9 PFLOP/s, with a multiply-add for
+// each of its results into the accumulators beside it.
 template <typename Y, int BO, int BR, int WGO, int WGR, int NS>
 __global__ __launch_bounds__(WGO *WGR * 64) void matmul_tile_kernel(Fp8Args p, int n_otiles, int n_rtiles) {
   constexpr int NW = WGO * WGR;
@@ -502,37 +511,54 @@ __global__ __launch_bounds__(WGO *WGR * 64) void matmul_tile_kernel(Fp8Args p, i
   }
 }
 
+// Of matmul_rows_kernel: a CU takes in W at about 25 bytes a ns and x, from
+// L2, at about 45, and has room for one workgroup: the rounds of workgroups
+// times what one brings and a little to begin with.  64 rows by k of 4096, us with RG of 8, 4, 2, 1:
+// n_out 32000 31.7 39.6 55.7 94; 22016 26.1 34.2 40.3 68; 11008 24.8 17.5 26.9
+// 36; 6144 24.3 17.0 14.1 24.
+static float rows_cost(int groups, int nb, int *best) {
+  float least = 0.f;
+  *best = 0;
+  for (int rg = 8; rg >= 1; rg /= 2) {
+    const int rounds = ((groups + rg - 1) / rg + 255) / 256;
+    const float cost = rounds * (rg / 25.f + nb / 45.f + 0.02f);
+    if (*best && cost >= least) continue;
+    *best = rg;
+    least = cost;
+  }
+  return least;
+}
 template <typename Y, int NB>
-static void launch_rows(const Fp8Args &a, hipStream_t st) {
+static void launch_rows(const Fp8Args &a, int rg, hipStream_t st) {
 #define LORA_ROWS(RG) \
   hipLaunchKernelGGL((matmul_rows_kernel<Y, NB, RG>), dim3((a.n_out + 16 * RG - 1) / (16 * RG)), dim3(512), 0, st, a)
-  // A CU takes in W at about 25 bytes a ns and x, from L2, at about 45, and has
-  // room for one workgroup: the rounds of workgroups times what one brings.
-  // 64 rows by k of 4096, us with RG of 8, 4, 2, 1: n_out 32000 31.7 39.6 55.7
-  // 94; 22016 26.1 34.2 40.3 68; 11008 24.8 17.5 26.9 36; 6144 24.3 17.0 14.1 24.
-  const int groups = (a.n_out + 15) / 16;
-  int best = 0;
-  float least = 0.f;
-  for (int rg = 8; rg >= (NB < 8 ? 1 : 2); rg /= 2) {
-    const int rounds = ((groups + rg - 1) / rg + 255) / 256;
-    const float cost = rounds * (rg / 25.f + NB / 45.f);
-    if (!best || cost < least) {
-      best = rg;
-      least = cost;
-    }
-  }
-  if (best == 8) LORA_ROWS(8);
-  else if (best == 4) LORA_ROWS(4);
-  else if (NB == 8 || best == 2) LORA_ROWS(2);
-  else if constexpr (NB < 8) LORA_ROWS(1);
+  if (rg == 8) LORA_ROWS(8);
+  else if (rg == 4) LORA_ROWS(4);
+  else if (rg == 2) LORA_ROWS(2);
+  else LORA_ROWS(1);
 #undef LORA_ROWS
 }
+// Up to 64 rows.  Up to 16 of them by matmul_few_kernel where it takes less:
+// several of its workgroups fit a CU, so that there are no rounds, but each
+// reads its rows of x again, and no wave has W of its own in flight behind
+// them.  Us with it and with matmul_rows_kernel, k of 4096: 1 row n_out 4096
+// 5.3 8.4, 32000 26.1 23.4; 16 rows 4096 7.0 8.6, 11008 16.1 14.1, 32000 38 24.
 template <typename Y>
 static void launch_few(const Fp8Args &a, hipStream_t st) {
-  if (a.n <= 16) hipLaunchKernelGGL((matmul_few_kernel<Y>), dim3((a.n_out + 15) / 16), dim3(kFewWaves * 64), 0, st, a);
-  else if (a.n <= 32) launch_rows<Y, 2>(a, st);
-  else if (a.n <= 64) launch_rows<Y, 4>(a, st);
-  else launch_rows<Y, 8>(a, st);
+  const int groups = (a.n_out + 15) / 16;
+  int rg;
+  if (a.n <= 16) {
+    const float few = 1.25f * (groups / 256.f) * (1.f / 25.f + a.n / 16.f / 45.f);
+    if (few <= rows_cost(groups, 1, &rg))
+      hipLaunchKernelGGL((matmul_few_kernel<Y>), dim3((a.n_out + 15) / 16), dim3(kFewWaves * 64), 0, st, a);
+    else launch_rows<Y, 1>(a, rg, st);
+  } else if (a.n <= 32) {
+    rows_cost(groups, 2, &rg);
+    launch_rows<Y, 2>(a, rg, st);
+  } else {
+    rows_cost(groups, 4, &rg);
+    launch_rows<Y, 4>(a, rg, st);
+  }
 }
 template <typename Y>
 static void launch_tiles(const Fp8Args &a, hipStream_t st) {
@@ -540,16 +566,27 @@ static void launch_tiles(const Fp8Args &a, hipStream_t st) {
   hipLaunchKernelGGL((matmul_tile_kernel<Y, BO, BR, WGO, WGR, NS>),                                                      \
                      dim3(((a.n_out + BO - 1) / BO) * ((a.n + BR - 1) / BR)), dim3(WGO * WGR * 64), 0, st, a,             \
                      (a.n_out + BO - 1) / BO, (a.n + BR - 1) / BR)
-  const long long big = (long long)((a.n_out + 255) / 256) * ((a.n + 255) / 256);
-  const long long mid = (long long)((a.n_out + 127) / 128) * ((a.n + 127) / 128);
-  if (big >= 256) LORA_TILE(256, 256, 2, 4, 2);
-  else if (mid >= 192) LORA_TILE(128, 128, 2, 2, 3);
-  else LORA_TILE(64, 64, 2, 2, 4);
+  // Time in units of what a CU takes for a round of the largest tiles (k of
+  // 4096: 62 us).  A CU holds one workgroup of 256 x 256, two of 128 x 128 and
+  // two of 64 x 64, of which the first alone takes as long as both.  Us with
+  // tiles of 64, 128, 256, k of 4096: 129 x 4096 17.7 25.0 51.6, 1024 x 4096
+  // 40 28 57, 512 x 22016 105 63 60, 4096 x 4096 144 82 72, 4096 x 22016 757
+  // 460 400.
+  auto tiles = [&](int e) { return (long long)((a.n_out + e - 1) / e) * ((a.n + e - 1) / e); };
+  auto rounds = [](long long n, int of) { return (n + of - 1) / of; };
+  const float big = 1.f * rounds(tiles(256), 256), small = 0.33f * rounds(tiles(64), 512);
+  const float mid = 0.67f * (tiles(128) / 512) + (tiles(128) % 512 == 0 ? 0.f : tiles(128) % 512 <= 256 ? 0.43f : 0.67f);
+  if (small <= mid && small <= big) LORA_TILE(64, 64, 2, 2, 4);
+  else if (mid < big) LORA_TILE(128, 128, 2, 4, 2);
+  else LORA_TILE(256, 256, 2, 4, 2);
 #undef LORA_TILE
 }
 
 hipError_t launch_matmul_fp8(const Fp8Args &a, int dtype, hipStream_t st) {
-  if (a.n <= 128) {
+  // Tiles from 65 rows on: 100 rows by k of 4096 at n_out 4096, 11008, 22016,
+  // 32000 take 17 21 27 28 us with them, 19 27 39 41 with eight blocks of 16 in
+  // matmul_rows_kernel; 64 rows 17 21 26 27 and 13 17 26 29.
+  if (a.n <= 64) {
     if (dtype == 0) launch_few<float>(a, st);
     else launch_few<u16>(a, st);
   } else {

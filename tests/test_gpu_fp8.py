@@ -207,7 +207,7 @@ def test_quantize_then_multiply():
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("n,n_out,k", [(20, 22016, 144), (33, 32000, 128), (60, 11008, 272), (100, 22016, 16), (128, 32000, 144), (128, 8192, 1040),
-                                       (1, 40, 16384), (16, 136, 8336), (40, 136, 8336), (128, 264, 16384), (200, 136, 8336), (2000, 2056, 1168)])
+                                       (1, 40, 16384), (1, 32000, 144), (9, 32000, 1040), (16, 11008, 400), (16, 136, 8336), (300, 11008, 144), (40, 136, 8336), (128, 264, 16384), (200, 136, 8336), (2000, 2056, 1168)])
 def test_matmul_of_wide_and_deep_weights(n, n_out, k, dtype):
     Product(n + n_out + k, n, n_out, k, dtype=dtype).check()
 
