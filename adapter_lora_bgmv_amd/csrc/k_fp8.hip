@@ -19,6 +19,8 @@
 // maximum and its codes; memory bounds it (22016 x 4096 bf16 in blocks of 128 x
 // 128: 52 us, 5.2 TB/s).  The product has three forms, by its rows: few of
 // them stream W into registers, more share x through LDS, and many are tiles.
+// Times below are of two weights in turn; 64 rows by 32000 x 4096 take 39 us
+// among weights of which no cache holds anything.
 #include <algorithm>
 #include <type_traits>
 
@@ -184,7 +186,7 @@ __device__ __forceinline__ void store4(u16 *p, f32x4 v) {
 __device__ __forceinline__ void store4(float *p, f32x4 v) { *(float4 *)p = make_float4(v[0], v[1], v[2], v[3]); }
 
 // ---------------------------------------------------------------- few rows
-// W is streamed once and bounds the call: 4.7 TB/s at 22016 x 4096, one row.  128 columns of a row of codes, by
+// W is streamed once and bounds the call: one row by 22016 x 4096 19 us.  128 columns of a row of codes, by
 // a lane's two 16-byte loads; columns past k are zeros.
 __device__ __forceinline__ Codes fetch_block(const uint8_t *row, int block, int k) {
   const int c0 = ((int)threadIdx.x & 48) + block * kFp8Block;  // lane / 16 * 16
@@ -235,8 +237,7 @@ __global__ __launch_bounds__(kFewWaves * 64) void matmul_few_kernel(Fp8Args p) {
   if (row < p.n && o < p.n_out) store4((Y *)p.y + row * p.y_stride + o, v);
 }
 
-// Up to 16 NB rows, W's stream again the bound (64 rows by 32000 x 4096: 30 us,
-// 4.4 TB/s of W).  Every workgroup reads all of x, a part of 64 KB at a time
+// Up to 16 NB rows, W's stream again the bound (64 rows by 32000 x 4096: 30 us).  Every workgroup reads all of x, a part of 64 KB at a time
 // (1024 columns of 64 rows), through registers into the half of LDS that the
 // part before the last has left, while W streams into registers, eight blocks
 // of a wave ahead and across the parts.  Of the eight waves RG take 16 output

@@ -24,6 +24,15 @@
 // byte permutes (the two layouts differ by exactly that transpose), the
 // quad's index fastest over the lanes so that four lanes store 16 bytes side
 // by side.
+//
+// With the rotation (lora_kv_write_rotary) keys turn between their load and the
+// maximum, pairs within a thread's registers or a neighbour's, and queries in
+// workgroups of their own behind those of the pages.  Angles are f64 products
+// of position and frequency, brought to an eighth of the circle, cosine and
+// sine series: in 64 bits for keys, whose f32 results decide codes, in f32 for
+// queries, and once for all heads that a workgroup turns.  Latency bounds small calls as it does the plain write's (8.0 us for
+// 64 rows), vector instructions next to HBM large ones (8 x 512 rows of 32 + 2
+// x 8 heads x 128: 23 to 26 us, 3.6 to 4.0 TB/s).
 #include <algorithm>
 #include <climits>
 

@@ -36,6 +36,12 @@
 //
 // Few rows are spread over workgroups by kernels that each end where all of a
 // row is needed: maxima, sums and lists, lists of top-p's bin, the drawing.
+//
+// Vector instructions bound many rows, 64-bit ones above all: 4096 rows of
+// 32000 in bf16 take 148 us without a cut (a weight is 14 f64 instructions and
+// HBM would take 50), 262 with top-p, which goes through the row twice, 119
+// with top-k.  Chains of launches, round trips and barriers bound few: 64 such
+// rows take 17, 33 and 24 us, one of 131071 in f32 with top-p 32.
 #include <algorithm>
 #include <climits>
 #include <type_traits>
@@ -1069,7 +1075,10 @@ __global__ __launch_bounds__(kSampleThreads, 4) void sample_draw_kernel(SampleAr
 
 // ---------------------------------------------------------------- launcher
 // Workgroups of a row: one where the rows alone fill the card, otherwise
-// enough of them that every wave has a segment.
+// enough of them that every wave has a segment.  With one and with more, us:
+// top-p of 64 rows of 32000 37 30, of 128 37 35, of 200 38 42, without a cut 17
+// 17, 17 19, 17 22, top-p of one row of 131071 152 31.  A second workgroup of a
+// row is worth its launches up to 256 rows where rows are long.
 int sample_chunks(int n, int n_vocab, int dtype) {
   const int ve = dtype == 0 ? 4 : 8;
   const int segs = (n_vocab + ve - 1 + kSampleSeg - 1) / kSampleSeg;  // a row may begin up to ve - 1 elements into its first vector
