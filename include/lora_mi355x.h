@@ -187,8 +187,9 @@ size_t lora_workspace_bytes(int32_t op, int32_t dtype, uint32_t n_rows, uint32_t
  * later fused call on the calling thread (lora_apply, lora_apply_segmented,
  * lora_apply_moe_gather, lora_apply_moe_grouped, lora_apply_stack,
  * lora_embed_rows, lora_kv_write, lora_kv_read, lora_kv_attend,
- * lora_token_logprobs, lora_kv_write_rotary, lora_token_sample, lora_quantize_fp8, lora_matmul_fp8) records on its stream events[0] before its first kernel, events[1] right before
- * its main kernel (after the route plan and shrink kernel where there is
+ * lora_token_logprobs, lora_kv_write_rotary, lora_token_sample,
+ * lora_quantize_fp8, lora_matmul_fp8) records on its stream events[0] before
+ * its first kernel, events[1] right before its main kernel (after the route plan and shrink kernel where there is
  * one), events[2] right after the main kernel, and events[3] after its last
  * kernel (the decode epilogue, or a stack's further levels, where there are
  * any).  n == 0 switches it off.  events is [host]; the events themselves
@@ -615,7 +616,8 @@ int lora_token_sample(int32_t dtype, uint32_t n_vocab, const void *logits, uint3
  * finite values, within 2^-117 .. 2^120; codes are x / s, rounded once to
  * nearest even, infinities and NaN as NaN.  k is a multiple of 16,
  * codes_row_stride too, x_row_stride of 8 (bf16) or 4 (f32), x and codes
- * 16-byte aligned.  No workspace.
+ * 16-byte aligned; codes and scale overlap neither x nor each other.  No
+ * workspace.
  */
 int lora_quantize_fp8(int32_t dtype, uint32_t n_rows, uint32_t k, const void *x, uint32_t x_row_stride, uint32_t block_rows,
                       void *codes, uint32_t codes_row_stride, float *scale, uint32_t scale_row_stride, void *stream);
@@ -629,11 +631,11 @@ int lora_quantize_fp8(int32_t dtype, uint32_t n_rows, uint32_t k, const void *x,
  * term joins through lora_shrink and lora_expand_fold.  k_in is a multiple of
  * 16, at most 65536, n_out of 8, strides of codes of 16, y_row_stride of 8
  * (bf16) or 4 (f32), and codes and y are 16-byte aligned; n is limited to
- * 16384, strides of codes and x_scale to 2^22.  The scaled sums of the blocks add up in f32 and y is rounded once.
- * Within a block f32 calls keep f32 sums of the exact products, bf16 calls
- * sums that are off by up to 2^-10 of the sum of the products' magnitudes,
- * 2^-16 typically (what the 8-bit matrix instruction keeps).  The order of every sum follows
- * from the sizes alone.  workspace [dev] of at least
+ * 16384, strides of codes and x_scale to 2^22.  The scaled sums of the blocks
+ * add up in f32 and y is rounded once.  Within a block f32 calls keep f32 sums
+ * of the exact products, bf16 calls sums that are off by up to 2^-10 of the sum of the products' magnitudes,
+ * 2^-16 typically (what the 8-bit matrix instruction keeps).  The order of
+ * every sum follows from the sizes alone.  workspace [dev] of at least
  * lora_matmul_fp8_workspace_bytes(...) bytes, which may be 0, zero-filled
  * before its first use with a shape; calls that may run at the same time need
  * one each.
