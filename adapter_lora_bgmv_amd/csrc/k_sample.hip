@@ -812,12 +812,15 @@ __device__ __forceinline__ void cut_and_add(Row<T> &row, int b, u64 wants, Sampl
   __syncthreads();
 }
 
-// Whatever a list could not hold.
+// Whatever a list could not hold.  Begins with a barrier: a caller may have
+// filled the table and come straight here, and every wave reads what all of
+// them wrote.
 template <typename T>
 __device__ __attribute__((noinline)) void draw_by_bits(const SampleArgs &a, int r, float m, SampleLds &lds) {
   Row<T> row;
   row.begin(a, r);
   row.set_max(m);
+  __syncthreads();
   auto to_seg = [&](int s, u64 sum) { lds.seg[s] = sum; };
   row.cut = 0;
   if (row.top_k > 0) cut_by_bits(row, (u64)row.top_k, true, lds);

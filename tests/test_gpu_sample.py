@@ -261,3 +261,26 @@ def test_flat_rows(V, n, dtype):
     ids, logp = d.result()
     e = Draw(x[rows], dtype, **{a: v[rows] for a, v in kw.items()})
     assert np.array_equal(e.check(), ids[rows]) and np.array_equal(e.result()[1], logp[rows], equal_nan=True)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("V,n", [(9001, 1), (70001, 5), (131071, 1), (32000, 33), (5000, 700)])
+def test_top_p_alone_among_more_equal_logits_than_a_list_holds(V, n, dtype):
+    """Top-p without top-k where its bin holds every logit, on rows of several
+    workgroups and of one: equal weights, so the cut is at ceil(p V) and the
+    number picks among those, draw after draw the same."""
+    rng = np.random.default_rng(V)
+    p, u = rng.uniform(0.2, 0.95, n).astype(np.float32), rng.random(n).astype(np.float32)
+    d = Draw(np.full((n, V), -1.25), dtype, p=p, u=u)
+    stay = np.ceil(p.astype(np.float64) * V)
+    want = np.floor(u.astype(np.float64) * stay)
+    other = Draw(rng.standard_normal((n, V)) * 3, dtype, p=0.9, u=u)  # other weights in LDS and workspace
+    for _ in range(5):
+        other.run()
+        d.ids.fill_(77)
+        d.logp.fill_(77.0)
+        d.run()
+        ids, logp = d.result()
+        assert np.array_equal(ids, want)
+        # log of 1/stay, rounded once
+        assert (np.abs(logp + np.log(stay)) <= 2.0 ** -24 * np.log(stay) + 1e-12).all()
