@@ -164,7 +164,7 @@ struct Row {
     greedy = temp == 0.f;
     if (greedy || min_p > 1.f) top_k = 1;
     if (top_k >= V || top_k < 0) top_k = 0;
-    if (top_k == 1) top_p = 1.f;
+    if (top_k == 1 && top_p == top_p) top_p = 1.f;  // a NaN stays for set_max to find
     cut = 0;
     least = uniform(min_p > 0.f && min_p <= 1.f ? (u64)ceil((double)min_p * kUnit) : 0);
   }

@@ -284,3 +284,29 @@ def test_top_p_alone_among_more_equal_logits_than_a_list_holds(V, n, dtype):
         assert np.array_equal(ids, want)
         # log of 1/stay, rounded once
         assert (np.abs(logp + np.log(stay)) <= 2.0 ** -24 * np.log(stay) + 1e-12).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("V,n", [(1, 6), (2, 6), (500, 18), (9001, 18), (131071, 6), (5003, 600)])
+def test_settings_that_are_nan_beside_ones_that_need_no_draw(V, n, dtype):
+    """A NaN among top_p, min_p and uniform leaves a row without a token also
+    where T = 0, top_k = 1 or min_p above 1 take the first one anyway."""
+    rng = np.random.default_rng(V + n)
+    x = rng.standard_normal((n, V)) * 3
+    kind, bad = np.arange(n) % 6, np.arange(n) // 6 % 3
+    t, k, p, m, u = np.full(n, 0.9), np.zeros(n, int), np.full(n, 0.8), np.zeros(n), rng.random(n)
+    t[kind == 0] = 0.0
+    k[kind == 1] = 1
+    m[kind == 2] = 7.0
+    k[kind == 3], m[kind == 3] = 1, 7.0
+    t[kind == 4], k[kind == 4] = 0.0, 40
+    hurt = kind < 5  # the sixth kind draws
+    p[hurt & (bad == 0)], m[hurt & (bad == 1)], u[hurt & (bad == 2)] = np.nan, np.nan, np.nan
+    rows = np.arange(n) if n < 100 else np.arange(36)
+    d = Draw(x, dtype, t=t, k=k, p=p, m=m, u=u)
+    d.run()
+    ids, logp = d.result()
+    assert (ids[hurt] == -1).all() and np.isnan(logp[hurt]).all(), np.flatnonzero(hurt & (ids >= 0))
+    assert (ids[~hurt] >= 0).all()
+    e = Draw(x[rows], dtype, t=t[rows], k=k[rows], p=p[rows], m=m[rows], u=u[rows])
+    assert np.array_equal(e.check(), ids[rows])
