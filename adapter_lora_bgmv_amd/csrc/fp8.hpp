@@ -4,12 +4,12 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "fp8_stage.hpp"
 #include "verify.hpp"
 
 namespace lora {
 
-constexpr int kFp8Block = 128;          // columns of a scale, and rows of a weight's
-constexpr uint32_t kFp8MaxK = 65536;    // columns of a product
+constexpr uint32_t kFp8MaxK = 65536;  // columns of a product
 struct QuantArgs {
   const void *x;  // [n][x_stride]
   uint8_t *codes; // [n][c_stride]

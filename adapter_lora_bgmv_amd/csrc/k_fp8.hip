@@ -411,17 +411,24 @@ __global__ __launch_bounds__(WGO *WGR * 64) void matmul_tile_kernel(Fp8Args p, i
   const int nst = (p.k + kFp8Block - 1) / kFp8Block;
 
   // Operands through buffer resources that begin at the tile and end with the
-  // last row's k columns: what lies past their ends is not read.  A lane's
-  // offset carries the row, which may lie past the end, and the scalar one the
-  // stage's first column, which does not.
+  // last row's k columns.  A lane's offset, which is checked against that end,
+  // carries the row, which may lie past it and is then not read; the scalar
+  // offset, which need not be checked, carries the stage's first column, and
+  // in the last stage lanes past k step back to it (stage_column).
   const __amdgpu_buffer_rsrc_t wsrc = tile_rsrc(p.W, o0, p.n_out, p.w_stride, p.k), xsrc = tile_rsrc(p.x, r0, p.n, p.x_stride, p.k);
   const __amdgpu_buffer_rsrc_t ssrc = tile_rsrc(p.x_scale, r0, p.n, 4 * p.xs_stride, 4 * nst);
-  const int chunk = ((lane & 7) ^ (((wave * 8 + (lane >> 3)) >> 1) & 7)) * 16;  // this lane's place in the stage's rows
-  const uint32_t woff = (wave * 8 + (lane >> 3)) * (uint32_t)p.w_stride + chunk, xoff = (wave * 8 + (lane >> 3)) * (uint32_t)p.x_stride + chunk;
+  const int chunk = stage_chunk(wave * 8 + (lane >> 3), lane & 7);  // this lane's place in the stage's rows
+  uint32_t woff = (wave * 8 + (lane >> 3)) * (uint32_t)p.w_stride + chunk, xoff = (wave * 8 + (lane >> 3)) * (uint32_t)p.x_stride + chunk;
   // part i of 8 of the scales of blocks 8 g .. 8 g + 7: BR / 8 rows, a wave 8 of them
   const uint32_t soff = (wave % (BR / 64) * 8 + (lane >> 3)) * 4 * (uint32_t)p.xs_stride + 4 * (lane & 7);
   auto bring_scales = [&](int g, int i) {
     dma4_buffer(ssrc, soff + 4 * (i * (BR / 8) * (uint32_t)p.xs_stride + 8 * g), 0, lds_addr(&xs[g % 3][(i * (BR / 8) + wave % (BR / 64) * 8) * 8]));
+  };
+  // Before the last stage's first transfer.
+  auto step_back = [&] {
+    const uint32_t by = chunk - stage_column(chunk, (nst - 1) * kFp8Block, p.k);
+    woff -= by;
+    xoff -= by;
   };
   // Stages past the last bring the last again, into places that nothing reads
   // any more, so that the waits count the same in every stage.
@@ -436,6 +443,7 @@ __global__ __launch_bounds__(WGO *WGR * 64) void matmul_tile_kernel(Fp8Args p, i
   };
   for (int i = 0; i < 8; ++i) bring_scales(0, i);
   for (int st = 0; st < NS - 1; ++st) {
+    if (st == nst - 1) step_back();
     issue(st, 0, LPW);
     bring_scales(st / 8 + 1, st % 8);
   }
@@ -470,6 +478,7 @@ __global__ __launch_bounds__(WGO *WGR * 64) void matmul_tile_kernel(Fp8Args p, i
     // Every wave is done with stage st - 1: its place takes stage st + NS - 1,
     // whose transfers go out among the products, as all of them together hold
     // the waves up.
+    if (st + NS - 1 == nst - 1) step_back();
     if constexpr (!kSpread) {
       issue(st + NS - 1, 0, LPW);
       bring_scales((st + NS - 1) / 8 + 1, (st + NS - 1) % 8);

@@ -227,3 +227,12 @@ def test_products_at_once(n):
     y, mag = D.matmul(p.x, p.xs, p.w, p.ws)
     for c in (p, q):
         assert (np.abs(c.result() - y) <= D.matmul_bound("bf16", y, mag, 400)).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("n,n_out,k", [(65, 64, 144), (66, 72, 16), (130, 1032, 400), (1030, 1032, 240), (1030, 4104, 272), (4100, 4104, 144), (4100, 4104, 112)])
+def test_matmul_of_rows_that_end_with_their_storage(n, n_out, k, dtype):
+    """Rows side by side, the last one's codes the storage's last, and a last block that is cut."""
+    p = Product(n + n_out, n, n_out, k, pad=0, dtype=dtype)
+    p.check()
+    assert p.dw.untyped_storage().nbytes() == n_out * k and p.dx.untyped_storage().nbytes() == n * k
