@@ -236,3 +236,10 @@ def test_matmul_of_rows_that_end_with_their_storage(n, n_out, k, dtype):
     p = Product(n + n_out, n, n_out, k, pad=0, dtype=dtype)
     p.check()
     assert p.dw.untyped_storage().nbytes() == n_out * k and p.dx.untyped_storage().nbytes() == n * k
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("n,n_out,k", [(4000, 4040, 272), (4090, 4096, 16), (3900, 4088, 1424)])
+def test_matmul_by_the_largest_tiles(n, n_out, k, dtype):
+    """256 tiles of 256 x 256 or a few more: one round of them is less than what smaller ones take."""
+    Product(n + k, n, n_out, k, dtype=dtype, pad=16 * (k % 32 == 0)).check()
