@@ -632,10 +632,13 @@ int lora_quantize_fp8(int32_t dtype, uint32_t n_rows, uint32_t k, const void *x,
  * 16, at most 65536, n_out of 8, strides of codes of 16, y_row_stride of 8
  * (bf16) or 4 (f32), and codes and y are 16-byte aligned; n is limited to
  * 16384, strides of codes and x_scale to 2^22.  The scaled sums of the blocks
- * add up in f32 and y is rounded once.  Within a block f32 calls keep f32 sums
- * of the exact products, bf16 calls sums that are off by up to 2^-10 of the sum of the products' magnitudes,
- * 2^-16 typically (what the 8-bit matrix instruction keeps).  The order of
- * every sum follows from the sizes alone.  workspace [dev] of at least
+ * add up in f32 and y is rounded once.  A block's two scales apply as their
+ * f32 product, which below 2^-126 is a multiple of 2^-149; where it would be
+ * infinite of finite scales, they apply one after the other.  Within a block
+ * f32 calls keep f32 sums of the exact products, bf16 calls sums that are off
+ * by up to 2^-10 of the sum of the products' magnitudes, 2^-16 typically (what
+ * the 8-bit matrix instruction keeps).  The order of every sum follows from
+ * the sizes alone.  workspace [dev] of at least
  * lora_matmul_fp8_workspace_bytes(...) bytes, which may be 0, zero-filled
  * before its first use with a shape; calls that may run at the same time need
  * one each.

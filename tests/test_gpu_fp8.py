@@ -243,3 +243,51 @@ def test_matmul_of_rows_that_end_with_their_storage(n, n_out, k, dtype):
 def test_matmul_by_the_largest_tiles(n, n_out, k, dtype):
     """256 tiles of 256 x 256 or a few more: one round of them is less than what smaller ones take."""
     Product(n + k, n, n_out, k, dtype=dtype, pad=16 * (k % 32 == 0)).check()
+
+
+def code(v):
+    return int(R.encode(np.array([float(v)]))[0])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("n,n_out", [(8, 264), (8, 32000), (20, 264), (64, 264), (64, 11008), (70, 264), (1030, 2056), (4000, 4040)])
+def test_matmul_of_scales_whose_product_f32_does_not_hold(n, n_out, dtype):
+    """Two scales of a block whose product is beyond f32, over sums that bring
+    the result back into its range or leave it beyond, or is below its normal
+    numbers."""
+    p = Product(n, n, n_out, 784, dtype=dtype)
+    p.ws[0, :6] = 2.0 ** 30, 2.0 ** 40, 1.37 * 2.0 ** -60, 2.0 ** 30, 1.0, 0.0
+    ordinary = p.x[:8].copy(), p.xs[:8].copy()
+    at = lambda b: np.s_[b * 128:(b + 1) * 128]
+    p.x[:8] = 0
+    p.xs[0, 0] = 2.0 ** 120                        # a sum of 0
+    p.xs[1, 1] = 2.0 ** 100                        # one of 2^-18
+    p.x[1, 128 + 9], p.w[:128, 128 + 9] = code(2.0 ** -9), code(2.0 ** -9)
+    p.w[:16, at(2)] = code(448.0)
+    p.x[2:4, at(2)] = code(448.0)                  # ones of up to 2^24.6
+    p.xs[2, 2], p.xs[3, 2] = 1.21 * 2.0 ** -85, 1.21 * 2.0 ** -93
+    p.x[4, at(3)], p.xs[4, 3] = code(1.0), 2.0 ** 120  # beyond f32 in the end
+    p.x[5, at(4)], p.xs[5, 4] = code(3.0), np.inf
+    p.x[6, at(5)], p.xs[6, 5] = code(448.0), 2.0 ** 127  # by a scale of 0
+    p.xs[7] = 0.0
+    p.upload()
+    p.call()
+    got = p.result()
+    with np.errstate(over="ignore"):
+        want, mag = D.matmul(p.x, p.xs.astype(float), p.w, p.ws.astype(float))
+        # matmul_bound's, with half a step of the type's smallest numbers in the place of its absolute term, and
+        # half a step of 2^-149 of the scales' product by sums of up to 128 448^2 in each of the blocks
+        bound = D.matmul_bound(dtype, want, mag, p.k) - 1e-37 + (2.0 ** -134 if dtype == "bf16" else 2.0 ** -150)
+        bound += 2.0 ** -150 * 128 * 448.0 ** 2 * 7
+    beyond = np.abs(want) > 3.4e38
+    assert beyond[4].any() and np.isinf(want[5]).any() and (want[6, :128] == 0).all()
+    assert np.array_equal(np.isnan(got), np.isnan(want))
+    assert np.array_equal(got[beyond], np.sign(want[beyond]) * np.inf)
+    live = np.isfinite(want) & ~beyond
+    bad = np.abs(got[live] - want[live]) > bound[live]
+    assert not bad.any(), f"{int(bad.sum())} of {bad.size} in rows {sorted(set(np.argwhere(live)[bad][:, 0].tolist()))[:9]}"
+    # the rows beside are the same bits where none of these rows is there
+    p.x[:8], p.xs[:8] = ordinary
+    p.upload()
+    p.call()
+    assert np.array_equal(p.result()[8:], got[8:])
