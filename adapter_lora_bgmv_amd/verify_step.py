@@ -23,6 +23,7 @@ sizes below and prints the time of each part.
 """
 from __future__ import annotations
 
+import contextlib
 from dataclasses import dataclass
 
 import numpy as np
@@ -91,7 +92,7 @@ class VerifyStep:
             need[0] = B.lora_matmul_fp8_workspace_bytes(B.LORA_BF16, self.row, s.hidden, self.n)
             need[2] = B.lora_matmul_fp8_workspace_bytes(B.LORA_BF16, s.vocab, self.q_dim, self.n)
             self.w_qkv8, self.w_vocab8 = (self._codes(w, 128) for w in (self.w_qkv, self.w_vocab))
-            self.x8, self.out8 = (self._room(self.n, k, 1) for k in (s.hidden, self.q_dim))
+            self.x8, self.out8 = (self._room(self.n, k, 1, device) for k in (s.hidden, self.q_dim))
             self.t = zeros(self.n, s.rank, dtype=torch.float32)
         if s.theta:
             i = torch.arange(0, s.head_dim, 2, dtype=torch.float64, device=device)
@@ -104,19 +105,21 @@ class VerifyStep:
             self.scores |= {"token": zeros(self.n, dtype=torch.int32), "token_logp": zeros(self.n, dtype=torch.float32)}
         self.ws = [(zeros(max(b, 256), dtype=torch.uint8), b) for b in need]
         if self.out.is_cuda:  # all of the above is there whatever stream the first step runs on
-            torch.cuda.current_stream().synchronize()
+            torch.cuda.current_stream(self.out.device).synchronize()
 
     @staticmethod
-    def _room(n, k, block):
+    def _room(n, k, block, device):
         """Codes and scales of n rows of k columns, not filled."""
         import torch
-        return (torch.zeros(n, k, dtype=torch.uint8, device="cuda"),
-                torch.zeros(-(-n // block), -(-k // 128), device="cuda"))
+        return (torch.zeros(n, k, dtype=torch.uint8, device=device),
+                torch.zeros(-(-n // block), -(-k // 128), device=device))
 
     @classmethod
     def _codes(cls, w, block):
-        codes, scale = cls._room(*w.shape, block)
-        cls._quantize(w, w.shape[1], block, (codes, scale), w.shape[0])
+        import torch
+        codes, scale = cls._room(*w.shape, block, w.device)
+        with torch.cuda.device(w.device) if w.is_cuda else contextlib.nullcontext():
+            cls._quantize(w, w.shape[1], block, (codes, scale), w.shape[0])
         return codes, scale
 
     @staticmethod

@@ -83,3 +83,31 @@ def test_first_stream_lookup_from_two_threads(monkeypatch):
     for t in threads:
         t.join(30)
     assert got == [103, 103] and fresh._stream(None) == 103
+
+
+def small(**options):
+    return V.Sizes(hidden=272, heads=4, kv_heads=2, head_dim=64, vocab=1000, page_tokens=16, slots=3, rank=16, top=4, **options)
+
+
+def tensors(o, at="step"):
+    """(where, tensor) of everything that an object holds."""
+    if isinstance(o, torch.Tensor):
+        yield at, o
+    elif isinstance(o, dict):
+        for k, v in o.items():
+            yield from tensors(v, f"{at}[{k!r}]")
+    elif isinstance(o, (list, tuple)):
+        for i, v in enumerate(o):
+            yield from tensors(v, f"{at}[{i}]")
+    elif type(o).__module__.startswith("adapter_lora_bgmv_amd") and hasattr(o, "__dict__"):
+        for k, v in vars(o).items():
+            yield from tensors(v, f"{at}.{k}")
+
+
+def test_a_step_with_all_options_lies_on_its_device(monkeypatch):
+    """Here the CPU, with the quantisation of the weights left out; no array goes to the default GPU."""
+    monkeypatch.setattr(V.VerifyStep, "_quantize", staticmethod(lambda *a, **k: None))
+    step = V.VerifyStep(small(base8=True, theta=10000.0, sample=True), n_seqs=2, draft=3, max_tokens=32, device="cpu")
+    found = dict(tensors(step))
+    assert {"step.w_qkv8[0]", "step.x8[1]", "step.rotary.inv_freq", "step.uniform"} <= set(found)
+    assert all(t.device.type == "cpu" for t in found.values())
