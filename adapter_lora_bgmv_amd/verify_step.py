@@ -49,6 +49,8 @@ class Sizes:
 
 
 class VerifyStep:
+    uniform = None  # the numbers that next tokens are drawn with: an array where Sizes asks for them
+
     def __init__(self, sizes: Sizes, n_seqs: int, draft: int, max_tokens: int, seed: int = 0, device="cuda"):
         import torch
         self.s, self.n_seqs, self.draft = sizes, n_seqs, draft
@@ -172,13 +174,18 @@ class VerifyStep:
 
     def run(self, x, lengths, ids, stream=None, uniform=None):
         """Scores of the draft tokens `ids` [n]; `lengths` are the sequences' tokens, these drafts included.
-        `uniform` [n]: the numbers in [0, 1) that next tokens are drawn with.
+        `uniform` [n]: the numbers in [0, 1) that next tokens are drawn with, given with
+        Sizes' sample and only with it; new ones for every step.
 
         The step's inputs are copied on the stream that its kernels run on (a
         torch stream or a raw handle; None: the current one), so that they wait
         for the step before.  x has to be ready on it, and the scores are.
         """
         import torch
+        if uniform is None and self.uniform is not None:
+            raise ValueError("a step that draws next tokens needs uniform, a number for each row")
+        if uniform is not None and self.uniform is None:
+            raise ValueError("uniform was given to a step that draws no tokens: Sizes(sample=True) does")
         if stream is None:
             stream = torch.cuda.current_stream()
         elif not isinstance(stream, torch.cuda.Stream):

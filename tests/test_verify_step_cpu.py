@@ -111,3 +111,16 @@ def test_a_step_with_all_options_lies_on_its_device(monkeypatch):
     found = dict(tensors(step))
     assert {"step.w_qkv8[0]", "step.x8[1]", "step.rotary.inv_freq", "step.uniform"} <= set(found)
     assert all(t.device.type == "cpu" for t in found.values())
+
+
+def test_next_tokens_take_numbers_and_other_steps_none():
+    """No step draws with the numbers of the one before: run refuses a missing
+    argument, and one that nothing would use, before it does anything."""
+    log = Log()
+    for options, uniform in ((dict(sample=True), None), ({}, np.zeros(6))):
+        step = V.VerifyStep(small(**options), n_seqs=2, draft=3, max_tokens=32, device="cpu")
+        step.ids, step.seqs = Record(log, "ids"), type("Seqs", (), {"kv_len": Record(log, "kv_len")})
+        step.parts = lambda x, stream: {"call": lambda: log.append("call")}
+        with pytest.raises(ValueError, match="uniform"):
+            step.run(None, [3, 4], np.arange(6), stream=77, uniform=uniform)
+    assert log == []
