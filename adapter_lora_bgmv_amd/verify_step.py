@@ -94,6 +94,7 @@ class VerifyStep:
             need[0] = B.lora_matmul_fp8_workspace_bytes(B.LORA_BF16, self.row, s.hidden, self.n)
             need[2] = B.lora_matmul_fp8_workspace_bytes(B.LORA_BF16, s.vocab, self.q_dim, self.n)
             self.w_qkv8, self.w_vocab8 = (self._codes(w, 128) for w in (self.w_qkv, self.w_vocab))
+            self.w_qkv = self.w_vocab = None  # the codes take their place
             self.x8, self.out8 = (self._room(self.n, k, 1, device) for k in (s.hidden, self.q_dim))
             self.t = zeros(self.n, s.rank, dtype=torch.float32)
         if s.theta:

@@ -124,3 +124,13 @@ def test_next_tokens_take_numbers_and_other_steps_none():
         with pytest.raises(ValueError, match="uniform"):
             step.run(None, [3, 4], np.arange(6), stream=77, uniform=uniform)
     assert log == []
+
+
+def test_a_step_holds_its_base_weights_once(monkeypatch):
+    """As codes or in 16 bits, not both."""
+    monkeypatch.setattr(V.VerifyStep, "_quantize", staticmethod(lambda *a, **k: None))
+    for base8, size in ((False, 2), (True, 1)):
+        step = V.VerifyStep(small(base8=base8), n_seqs=2, draft=3, max_tokens=32, device="cpu")
+        for shape in ((step.row, step.s.hidden), (step.s.vocab, step.q_dim)):
+            held = [t.element_size() for _, t in tensors(step) if tuple(t.shape) == shape]
+            assert held == [size], (base8, shape, held)
