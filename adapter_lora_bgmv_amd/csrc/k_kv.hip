@@ -503,17 +503,21 @@ __device__ __forceinline__ void turn_queries(const KvDev &a, const RotaryDev &ro
   }
 }
 
-// Grid: touched pages x (groups of HB heads for K, heads for V), then the queries' workgroups.
+// Workgroups: touched pages x (groups of HB heads for K, heads for V), then
+// the queries'.  A dimension of a grid holds less than 2^32 threads, so they
+// are laid out in rows of kGridRow.
+constexpr int kGridRow = 1 << 20;
 template <typename T, int D, int IT, int HB>
 __global__ __launch_bounds__(kKvThreads) void kv_write_rotary_kernel(KvDev a, RotaryDev rot, TurnArgs q, const T *krows,
                                                                      int k_stride, const T *vrows, int v_stride) {
   __shared__ uint32_t wave_max[kKvThreads / 64];
   __shared__ int pos[64];
-  if ((int)blockIdx.x >= q.first) {
-    turn_queries<T, D>(a, rot, q, blockIdx.x - q.first, pos);
+  const int b = blockIdx.y * kGridRow + blockIdx.x;
+  if (b >= q.first) {
+    if (b < q.blocks) turn_queries<T, D>(a, rot, q, b - q.first, pos);
     return;
   }
-  const int k_groups = (a.H + HB - 1) / HB, per = k_groups + a.H, u = blockIdx.x / per, h = blockIdx.x - u * per;
+  const int k_groups = (a.H + HB - 1) / HB, per = k_groups + a.H, u = b / per, h = b - u * per;
   if (h < k_groups) write_turned_page<T, D, IT, HB>(a, rot, u, h * HB, krows, k_stride, wave_max);
   else write_page<T, D, IT>(a, u, h - k_groups, true, krows, k_stride, vrows, v_stride, wave_max);
 }
@@ -647,7 +651,8 @@ struct RotaryK {
       constexpr int HB = IT <= 2 ? 2 : 1;
       const bool two = HB == 2 && (long long)grid.x * grid.y >= 512;
       q.first = (int)grid.x * (two ? (kv.H + 1) / 2 + kv.H : 2 * kv.H);
-      const dim3 all(q.first + row_blocks * q.groups), block(kKvThreads);
+      q.blocks = q.first + row_blocks * q.groups;
+      const dim3 all(std::min(q.blocks, kGridRow), (unsigned)(((long long)q.blocks + kGridRow - 1) / kGridRow)), block(kKvThreads);
       if (two) hipLaunchKernelGGL((kv_write_rotary_kernel<T, D, IT, HB>), all, block, 0, st, kv, rot, q, (const T *)k, ks, (const T *)v, vs);
       else hipLaunchKernelGGL((kv_write_rotary_kernel<T, D, IT, 1>), all, block, 0, st, kv, rot, q, (const T *)k, ks, (const T *)v, vs);
     }

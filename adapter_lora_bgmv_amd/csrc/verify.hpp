@@ -115,7 +115,7 @@ struct TurnArgs {
   const void *q;
   void *out;
   int q_stride, out_stride, heads;
-  int per, groups, first;  // heads of a workgroup, workgroups of a row, the grid's first: set by the launcher
+  int per, groups, first, blocks;  // heads of a workgroup, workgroups of a row, the grid's first and all: set by the launcher
 };
 hipError_t launch_kv_write_rotary(const KvDev &kv, const RotaryDev &rot, const TurnArgs &q, int dim, int dtype, const void *k,
                                   int k_stride, const void *v, int v_stride, hipStream_t st);

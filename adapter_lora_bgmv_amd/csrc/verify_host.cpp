@@ -191,7 +191,7 @@ int lora_kv_write_rotary(const lora_kv_cache *cache, const lora_kv_seqs *seqs, c
                 cache->n_kv_heads, n_heads);
   if (int e = check_device(what)) return e;
   const RotaryDev rot{rotary->inv_freq, (int)rotary->rot_dim, rotary->interleaved != 0};
-  const TurnArgs turn{q, q_out, (int)q_row_stride, (int)q_out_row_stride, (int)n_heads, 0, 0, 0};
+  const TurnArgs turn{q, q_out, (int)q_row_stride, (int)q_out_row_stride, (int)n_heads, 0, 0, 0, 0};
   hipStream_t st = (hipStream_t)stream;
   return timed(what, st, [&] {
     return launch_kv_write_rotary(d, rot, turn, (int)cache->head_dim, dtype, k, (int)k_row_stride, v, (int)v_row_stride, st);

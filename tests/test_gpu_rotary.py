@@ -208,3 +208,35 @@ def test_captured_and_on_another_stream():
         assert np.array_equal(host(c.out), want)
         for name in ("ke", "ve", "k", "v"):
             assert np.array_equal(getattr(got, name), getattr(pages, name))
+
+
+def test_more_workgroups_than_one_dimension_of_a_grid_holds():
+    """2^24 workgroups of pages and heads, and the queries' behind them: a call
+    that lora_kv_write takes, too, and whose angles of 0 leave its codes the same."""
+    n_seqs, rows, H, D_, P, heads = 1024, 8, 4500, 64, 16, 3
+    n, row = n_seqs * rows, H * D_
+    assert min(n, n // P + 2 * n_seqs) * (H + (H + 1) // 2) > 2 ** 24
+    owners = [0, 1, 511, 1023]  # the sequences that have a page; the others' tokens are not written
+    table = torch.full((n_seqs, 1), -1, dtype=torch.int32, device="cuda")
+    table[owners, 0] = torch.tensor([2, 0, 3, 1], dtype=torch.int32, device="cuda")
+    seqs = B.KVSeqs(table, torch.arange(0, n + 1, rows, dtype=torch.int32, device="cuda"),
+                    torch.full((n_seqs,), rows, dtype=torch.int32, device="cuda"), max_rows=rows)
+    x = torch.zeros(n, row, dtype=torch.bfloat16, device="cuda")
+    g = torch.Generator("cuda").manual_seed(5)
+    for i in owners:
+        x[i * rows:(i + 1) * rows].normal_(generator=g)
+    q = torch.randn(n, heads * D_, generator=g, device="cuda").bfloat16()
+    out = torch.zeros_like(q)
+    a, b = (B.KVCache.empty(4, H, D_, P, "cuda") for _ in range(2))
+    for c in (a, b):
+        for t in (c.k, c.v, c.k_scale, c.v_scale):
+            t.zero_()
+    torch.cuda.synchronize()
+    B.lora_kv_write(a, seqs, B.LORA_BF16, x, row, x, row, n)
+    rotary = B.Rotary(torch.zeros(D_ // 2, device="cuda"))
+    B.lora_kv_write_rotary(b, seqs, rotary, B.LORA_BF16, heads, q, heads * D_, out, heads * D_, x, row, x, row, n)
+    torch.cuda.synchronize()
+    assert torch.equal(out, q)
+    assert bool((a.k_scale > 0).all()) and bool((a.k != 0).any())
+    for name in ("k", "v", "k_scale", "v_scale"):
+        assert torch.equal(getattr(a, name), getattr(b, name)), name
