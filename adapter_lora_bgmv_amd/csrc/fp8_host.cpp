@@ -67,11 +67,12 @@ int lora_quantize_fp8(int32_t dtype, uint32_t n_rows, uint32_t k, const void *x,
   return timed(what, st, [&] { return launch_quantize_fp8(a, dtype, (int)block_rows, st); });
 }
 
+// No form needs one.
 size_t lora_matmul_fp8_workspace_bytes(int32_t, uint32_t, uint32_t, uint32_t) { return 0; }
 
 int lora_matmul_fp8(int32_t dtype, uint32_t n_out, uint32_t k_in, const void *W, uint32_t w_row_stride, const float *w_scale,
                     uint32_t w_scale_stride, const void *x, uint32_t x_row_stride, const float *x_scale, uint32_t x_scale_stride,
-                    uint32_t n, void *y, uint32_t y_row_stride, void *workspace, size_t workspace_bytes, void *stream) {
+                    uint32_t n, void *y, uint32_t y_row_stride, void *, size_t, void *stream) {
   clear_err();
   const char *what = "lora_matmul_fp8";
   if (int e = check_type(what, dtype)) return e;
@@ -90,12 +91,6 @@ int lora_matmul_fp8(int32_t dtype, uint32_t n_out, uint32_t k_in, const void *W,
     return fail(LORA_ERR_STRIDE, "%s: row strides of W %u, x %u and x's scales %u must be at most %u", what, w_row_stride, x_row_stride,
                 x_scale_stride, kMaxStride);
   if (n == 0) return LORA_OK;
-  const size_t need = lora_matmul_fp8_workspace_bytes(dtype, n_out, k_in, n);
-  if (need && (!workspace || workspace_bytes < need))
-    return fail(LORA_ERR_WORKSPACE, "%s: [n %u] x [n_out %u x k_in %u]: workspace %p of %zu bytes, %zu needed", what, n, n_out, k_in,
-                workspace, workspace_bytes, need);
-  if (need && !aligned16(workspace))
-    return fail(LORA_ERR_UNSUPPORTED, "%s: workspace %p is not 16-byte aligned", what, workspace);
   if (int e = check_device(what)) return e;
   Fp8Args a{};
   a.W = (const uint8_t *)W;

@@ -639,9 +639,8 @@ int lora_quantize_fp8(int32_t dtype, uint32_t n_rows, uint32_t k, const void *x,
  * by up to 2^-10 of the sum of the products' magnitudes, 2^-16 typically (what
  * the 8-bit matrix instruction keeps).  The order of every sum follows from
  * the sizes alone.  workspace [dev] of at least
- * lora_matmul_fp8_workspace_bytes(...) bytes, which may be 0, zero-filled
- * before its first use with a shape; calls that may run at the same time need
- * one each.
+ * lora_matmul_fp8_workspace_bytes(...) bytes: 0 at every size as it stands, so
+ * that it may be NULL and is not read.
  */
 size_t lora_matmul_fp8_workspace_bytes(int32_t dtype, uint32_t n_out, uint32_t k_in, uint32_t n);
 int lora_matmul_fp8(int32_t dtype, uint32_t n_out, uint32_t k_in, const void *W, uint32_t w_row_stride, const float *w_scale,
