@@ -466,9 +466,12 @@ __device__ __forceinline__ void dma4_buffer(__amdgpu_buffer_rsrc_t r, uint32_t v
 // that way).  NS stages form a ring with NS - 1 in flight; the waits are
 // explicit, and a stage is read only after every wave's share of it landed.
 // Rows past the ends read as nothing and are not stored; chunks past k are
-// zeroed once they have landed.  The matrix instruction bounds the largest
-// tiles: 4096 x 22016 x 4096 in 390 us, 1.9 PFLOP/s, with a multiply-add for
-// each of its results into the accumulators beside it.
+// zeroed once they have landed.  No one unit bounds the largest tiles: 4096 x
+// 22016 x 4096 take 392 to 402 us, 1.9 PFLOP/s, in which the matrix units are
+// busy for 43 % and vector instructions, a multiply-add for each result of the
+// matrix ones above all, for 34 %; the two waves of a SIMD wait 35 % of their
+// time, and 1376 tiles are 5.4 rounds that take 6.  (Single passes range
+// from 376 to 487 us as the clock follows the load.)
 template <typename Y, int BO, int BR, int WGO, int WGR, int NS>
 __global__ __launch_bounds__(WGO *WGR * 64) void matmul_tile_kernel(Fp8Args p, int n_otiles, int n_rtiles) {
   constexpr int NW = WGO * WGR;
@@ -620,9 +623,12 @@ __global__ __launch_bounds__(WGO *WGR * 64) void matmul_tile_kernel(Fp8Args p, i
 
 // Of matmul_rows_kernel: a CU takes in W at about 25 bytes a ns and x, from
 // L2, at about 45, and has room for one workgroup: the rounds of workgroups
-// times what one brings and a little to begin with.  64 rows by k of 4096, us with RG of 8, 4, 2, 1:
-// n_out 32000 31.7 39.6 55.7 94; 22016 26.1 34.2 40.3 68; 11008 24.8 17.5 26.9
-// 36; 6144 24.3 17.0 14.1 24.
+// times what one brings and a little to begin with.  64 rows by k of 4096 in
+// bf16, us with RG of 8, 4, 2, 1: n_out 32000 31.7 39.6 55.7 94; 22016 26.1
+// 34.2 40.3 68; 11008 24.8 17.5 26.9 36; 6144 24.3 17.0 14.1 24.  The rule is
+// fitted to these and sees neither k nor the type; of n_out 4096, 11008 and
+// 32000 it takes the best also at k of 1024 and 11008 and in f32, or one within
+// 6 % of it (k of 11008, 4096 outputs: 28.1, 26.5 with RG of 2).
 static float rows_cost(int groups, int nb, int *best) {
   float least = 0.f;
   *best = 0;
@@ -649,7 +655,10 @@ static void launch_rows(const Fp8Args &a, int rg, hipStream_t st) {
 // several of its workgroups fit a CU, so that there are no rounds, but each
 // reads its rows of x again, and no wave has W of its own in flight behind
 // them.  Us with it and with matmul_rows_kernel, k of 4096: 1 row n_out 4096
-// 5.3 8.4, 32000 26.1 23.4; 16 rows 4096 7.0 8.6, 11008 16.1 14.1, 32000 38 24.
+// 5.3 8.4, 32000 26.1 23.4; 16 rows 4096 7.0 8.6, 11008 16.1 14.1, 32000 38 24,
+// and in f32 the same choice is the better one.  Fitted at that k, it changes
+// over too early at others: k of 1024, 1 row n_out 32000 9.0 20.8, 16 rows
+// 11008 7.2 13.2, 32000 12.8 21.1; k of 11008, 1 row 32000 71 95.
 template <typename Y>
 static void launch_few(const Fp8Args &a, hipStream_t st) {
   const int groups = (a.n_out + 15) / 16;
@@ -678,7 +687,10 @@ static void launch_tiles(const Fp8Args &a, hipStream_t st) {
   // two of 64 x 64, of which the first alone takes as long as both.  Us with
   // tiles of 64, 128, 256, k of 4096: 129 x 4096 17.7 25.0 51.6, 1024 x 4096
   // 40 28 57, 512 x 22016 105 63 60, 4096 x 4096 144 82 72, 4096 x 22016 757
-  // 460 400.
+  // 460 400.  Fitted in bf16 at that k; of 31 sizes of 128 to 2048 rows by 4096
+  // and 11008 in f32 and at k of 1024 and 11008 three take over 5 % longer than
+  // they might: at k of 1024, with 128 and the 256 taken, 2048 x 11008 42.1
+  // 45.5, in f32 59.9 67.8, and 1024 x 11008 in f32 33.0 35.8.
   auto tiles = [&](int e) { return (long long)((a.n_out + e - 1) / e) * ((a.n + e - 1) / e); };
   auto rounds = [](long long n, int of) { return (n + of - 1) / of; };
   const float big = 1.f * rounds(tiles(256), 256), small = 0.33f * rounds(tiles(64), 512);

@@ -10,7 +10,8 @@
     scores the draft tokens (lora_token_logprobs).
 With Sizes' options it also
     keeps its base weights in 8 bits (lora_quantize_fp8 in front of each projection,
-        lora_matmul_fp8, the adapters' delta by lora_shrink and lora_expand_fold),
+        lora_matmul_fp8, the adapters' delta by lora_shrink and lora_expand_fold, so
+        that a row with an adapter is rounded twice),
     turns queries and keys by their positions on the way into the cache
         (lora_kv_write_rotary in the place of lora_kv_write), and
     draws every row's next token (lora_token_sample), by the settings that the

@@ -577,8 +577,8 @@ int lora_token_logprobs(int32_t dtype, uint32_t n_vocab, const void *logits, uin
  * (any alignment of whole elements; dtype is the logits').  With m the row's
  * maximum and T its temperature, token t has the weight
  *   W_t = rint(2^43 exp((x_t - m) / T)),
- * a whole number, so that sums and with them the token depend on the row
- * alone, not on the batch.  In the order by value, equal values by the lower
+ * a whole number, which the exponential in 64 bits leaves off by 1 at most, so
+ * that sums and with them the token depend on the row alone, not on the batch.  In the order by value, equal values by the lower
  * index first, these stay:
  *   the first top_k[i] tokens (all, where it is 0, negative or >= n_vocab);
  *   of those the fewest first ones whose weights reach top_p[i] of theirs
@@ -628,7 +628,8 @@ int lora_quantize_fp8(int32_t dtype, uint32_t n_rows, uint32_t k, const void *x,
  * with codes W [dev] [n_out][w_row_stride], x [dev] [n][x_row_stride] and
  * their scales [dev], any f32 numbers, [ceil(n_out / 128)][w_scale_stride] and
  * [n][x_scale_stride].  dtype is that of y [dev] [n][y_row_stride]; a LoRA
- * term joins through lora_shrink and lora_expand_fold.  k_in is a multiple of
+ * term joins through lora_shrink and lora_expand_fold, by which a bf16 y is
+ * rounded a second time (lora_apply rounds once).  k_in is a multiple of
  * 16, at most 65536, n_out of 8, strides of codes of 16, y_row_stride of 8
  * (bf16) or 4 (f32), and codes and y are 16-byte aligned; n is limited to
  * 16384, strides of codes and x_scale to 2^22.  The scaled sums of the blocks
