@@ -42,8 +42,9 @@
 // reading at HBM's rate would take 50, and a row is read twice), 262 with
 // top-p, which goes through the row once more, 119 with top-k.  Of settings of
 // all kinds, 187 us, vector instructions take 65 %; 2.1 readings come from HBM,
-// and registers that spill write 112 MB.  Chains of launches, round trips and barriers bound few: 64 such
-// rows take 17, 33 and 24 us, one of 131071 in f32 with top-p 32.
+// and registers that spill write 112 MB.  Chains of launches, round trips and
+// barriers bound few: 64 such rows take 17, 33 and 24 us, one of 131071 in f32
+// with top-p 32.
 #include <algorithm>
 #include <climits>
 #include <type_traits>
@@ -363,7 +364,7 @@ __device__ __forceinline__ void eights(const Row<T> &row, int first, const uint4
 #pragma unroll
     for (int e = 0; e < 8; ++e) x[e] = Logits<T>::at(v[i + e / Row<T>::VE], e % Row<T>::VE);
     f(x, [&](int e) { return Row<T>::index(first, i + e / Row<T>::VE, e % Row<T>::VE); });
-    __builtin_amdgcn_sched_barrier(0);  // more of them side by side spill more registers than the 6 to 42 that sample_kernel and sample_draw_kernel do
+    __builtin_amdgcn_sched_barrier(0);  // more side by side spill more than the 6 to 42 registers of sample_kernel and sample_draw_kernel
   }
 }
 

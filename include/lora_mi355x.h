@@ -578,8 +578,8 @@ int lora_token_logprobs(int32_t dtype, uint32_t n_vocab, const void *logits, uin
  * maximum and T its temperature, token t has the weight
  *   W_t = rint(2^43 exp((x_t - m) / T)),
  * a whole number, which the exponential in 64 bits leaves off by 1 at most, so
- * that sums and with them the token depend on the row alone, not on the batch.  In the order by value, equal values by the lower
- * index first, these stay:
+ * that sums and with them the token depend on the row alone, not on the batch.
+ * In the order by value, equal values by the lower index first, these stay:
  *   the first top_k[i] tokens (all, where it is 0, negative or >= n_vocab);
  *   of those the fewest first ones whose weights reach top_p[i] of theirs
  *   (all, where it is 1 or more);
